@@ -346,6 +346,67 @@ SSD_API int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int k
                             void* y_ring, int n_steps, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Norms around a block  (the block the SSD sits in: a norm of the residual stream ahead of
+ * its input projection, a gated norm between the SSD and its output projection)
+ *
+ * Matrices are `rows` rows of D contiguous elements; `ld_*` is the distance between the
+ * starts of two rows in elements (>= D), so an operand may be a slice of a wider row (the gate
+ * inside the input projection's output).  Unlike elsewhere, matrix pointers need only the
+ * alignment of their element type; 16-byte aligned rows (pointer and stride, and D / groups
+ * a multiple of 8) take the vectorised kernels.  weight and dweight are [D] fp32 and 16-byte
+ * aligned.  io is SSD_BF16 or SSD_F32; the residual stream has its own type (SSD_F32 beside
+ * either io, SSD_BF16 beside SSD_BF16).  All arithmetic is fp32, each result rounded once.
+ * A norm spans at most 16384 elements (D, or D / groups).  The rows may number 0 (dweight is
+ * then zeroed) or more than 2^31 / D: offsets are 64 bits.  One row is a decode step's call.
+ *
+ *   ssd_residual_norm            r = residual + scale * x  (residual NULL: r = scale * x)
+ *                                out = r * (mean(r^2) + eps)^(-1/2) * weight;  the mean is of the
+ *                                fp32 r, before residual_out rounds it
+ *                                residual_out (NULL: not stored) = r; may be residual itself
+ *   ssd_residual_norm_backward   from r as stored, dout and dresidual_out (NULL: zero), the
+ *                                gradients dx, dresidual (either may be NULL: not stored) and
+ *                                dweight (NULL: not computed); dresidual may be dresidual_out
+ *                                itself
+ *   ssd_gated_norm               groups of D / groups elements are normalised on their own;
+ *                                norm_before_gate = 0: v = y * silu(z), out = v * k(v) * weight
+ *                                norm_before_gate = 1: out = y * k(y) * weight * silu(z)
+ *                                with k(v) = (mean(v^2) + eps)^(-1/2)
+ *   ssd_gated_norm_backward      the gradients dy, dz and dweight (NULL: not computed)
+ *
+ * dweight sums over the rows in an order fixed by the shape and the device: the same call gives
+ * bitwise the same result.  It needs a workspace of ssd_norm_backward_workspace_size(rows, D,
+ * groups) bytes (groups = 1 for the residual norm); without dweight the workspace may be NULL.
+ * Written buffers must overlap nothing else, apart from the in-place pairs named above (same
+ * pointer and stride); a strided buffer counts from its first element to its last.
+ * Errors: SSD_ERR_INVALID_ARG (null or misaligned pointer, a negative size, D % groups, a stride
+ * below D, eps negative or not finite, scale not finite, a bad enum, an overlap),
+ * SSD_ERR_UNSUPPORTED (a norm above 16384 elements, groups above 65535, a bf16 residual beside
+ * fp32 io), SSD_ERR_WORKSPACE, SSD_ERR_CUDA.
+ * ---------------------------------------------------------------------------------- */
+SSD_API size_t ssd_norm_backward_workspace_size(long long rows, int D, int groups);
+
+SSD_API int ssd_residual_norm(long long rows, int D, int io_dtype, int res_dtype, const void* x, long long ld_x,
+                              const void* residual, long long ld_residual, float scale, const float* weight,
+                              float eps, void* out, long long ld_out, void* residual_out,
+                              long long ld_residual_out, void* stream);
+
+SSD_API int ssd_residual_norm_backward(long long rows, int D, int io_dtype, int res_dtype, const void* dout,
+                                       long long ld_dout, const void* r, long long ld_r, const float* weight,
+                                       const void* dresidual_out, long long ld_dresidual_out, float scale, float eps,
+                                       void* dx, long long ld_dx, void* dresidual, long long ld_dresidual,
+                                       float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+SSD_API int ssd_gated_norm(long long rows, int D, int groups, int io_dtype, int norm_before_gate, const void* y,
+                           long long ld_y, const void* z, long long ld_z, const float* weight, float eps, void* out,
+                           long long ld_out, void* stream);
+
+SSD_API int ssd_gated_norm_backward(long long rows, int D, int groups, int io_dtype, int norm_before_gate,
+                                    const void* dout, long long ld_dout, const void* y, long long ld_y, const void* z,
+                                    long long ld_z, const float* weight, float eps, void* dy, long long ld_dy, void* dz,
+                                    long long ld_dz, float* dweight, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Measurement hooks (no counterpart on the pages; used by the benchmark)
  *
  * ssd_launch_count: total number of kernels this library has enqueued in this process

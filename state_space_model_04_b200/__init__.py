@@ -20,9 +20,12 @@ from .ssd import (  # noqa: F401
     decode_step,
     decode_step_noalloc,
     decode_workspace_size,
+    gated_norm,
+    gated_norm_backward,
     last_error,
     launch_count,
     lib,
+    norm_backward_workspace_size,
     profile_begin,
     profile_end,
     prefill,
@@ -32,5 +35,7 @@ from .ssd import (  # noqa: F401
     prefill_segments,
     prefill_whole_units,
     prefill_workspace_size,
+    residual_norm,
+    residual_norm_backward,
     status_string,
 )

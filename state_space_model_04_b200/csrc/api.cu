@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <string>
 #include <tuple>
@@ -53,6 +54,21 @@ int create_decode_plan(ssd_decode_plan** out, int layers, int b, int H, int N, i
 int launch_decode_plan(ssd_decode_plan* plan, cudaStream_t s);
 int destroy_decode_plan(ssd_decode_plan* plan);
 int decode_noalloc_scratch(void** ptr, size_t* bytes);
+size_t norm_workspace_bytes(long long rows, int D, int groups);
+int launch_residual_norm(long long rows, int D, int io, int res_dtype, const void* x, long long ld_x,
+                         const void* res, long long ld_res, float scale, const float* w, float eps, void* out,
+                         long long ld_out, void* r, long long ld_r, cudaStream_t s);
+int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, const void* dout, long long ld_dout,
+                                  const void* r, long long ld_r, const float* w, const void* dro, long long ld_dro,
+                                  float scale, float eps, void* dx, long long ld_dx, void* dres, long long ld_dres,
+                                  float* dw, void* ws, cudaStream_t s);
+int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first, const void* y, long long ld_y,
+                      const void* z, long long ld_z, const float* w, float eps, void* out, long long ld_out,
+                      cudaStream_t s);
+int launch_gated_norm_backward(long long rows, int D, int groups, int io, int norm_first, const void* dout,
+                               long long ld_dout, const void* y, long long ld_y, const void* z, long long ld_z,
+                               const float* w, float eps, void* dy, long long ld_dy, void* dz, long long ld_dz,
+                               float* dw, void* ws, cudaStream_t s);
 
 static thread_local char g_detail[512];
 
@@ -586,6 +602,168 @@ int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int kconv, in
     // an executable graph destroyed while in flight is freed when it completes
     const int st2 = destroy_decode_plan(plan);
     return st != SSD_OK ? st : st2;
+}
+
+// ---- norms around a block
+
+// A matrix operand of a norm call: rows of D elements, ld elements apart.
+struct NormMat {
+    const char* name;
+    const void* p;
+    long long ld;
+    int elem;       // bytes an element
+    bool required, written;
+};
+
+static constexpr int kNormMaxLen = 16384;  // elements one reduction spans (registers of a block)
+
+static Range norm_range(const NormMat& m, long long rows, int D) {
+    if (!m.p || rows == 0) return {nullptr, 0};
+    return {m.p, ((size_t)(rows - 1) * (size_t)m.ld + (size_t)D) * m.elem};
+}
+
+// Shapes, pointers and overlaps of a norm call.  `inplace` names a pair (input, output) that may
+// be the same memory with the same stride.
+static int check_norm(long long rows, int D, int groups, int io, int res_dtype, float eps, const NormMat* mats, int n,
+                      const float* weight, const float* dweight, int inplace_in, int inplace_out) {
+    if (io != SSD_F32 && io != SSD_BF16) return set_error(SSD_ERR_INVALID_ARG, "io_dtype %d is not SSD_F32/SSD_BF16", io);
+    if (res_dtype != SSD_F32 && res_dtype != SSD_BF16)
+        return set_error(SSD_ERR_INVALID_ARG, "res_dtype %d is not SSD_F32/SSD_BF16", res_dtype);
+    if (io == SSD_F32 && res_dtype == SSD_BF16)
+        return set_error(SSD_ERR_UNSUPPORTED, "a bf16 residual beside fp32 io is not implemented");
+    if (rows < 0) return set_error(SSD_ERR_INVALID_ARG, "negative size rows=%lld", rows);
+    if (D < 1 || groups < 1 || D % groups) return set_error(SSD_ERR_INVALID_ARG, "D=%d groups=%d: D must be a positive multiple of groups", D, groups);
+    if (D / groups > kNormMaxLen) return set_error(SSD_ERR_UNSUPPORTED, "a norm over %d elements (at most %d)", D / groups, kNormMaxLen);
+    if (groups > kMaxGridYZ) return set_error(SSD_ERR_UNSUPPORTED, "groups=%d above 65535", groups);
+    if (!(eps >= 0.f) || std::isinf(eps)) return set_error(SSD_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", (double)eps);
+    SSD_CHECK(check_ptr(weight, "weight", true));
+    SSD_CHECK(check_ptr(dweight, "dweight", false));
+    if (rows == 0) return SSD_OK;
+    for (int i = 0; i < n; ++i) {
+        const NormMat& m = mats[i];
+        if (!m.p) {
+            if (m.required) return set_error(SSD_ERR_INVALID_ARG, "%s is NULL", m.name);
+            continue;
+        }
+        if ((uintptr_t)m.p % m.elem) return set_error(SSD_ERR_INVALID_ARG, "%s is not aligned to its elements", m.name);
+        if (m.ld < D) return set_error(SSD_ERR_INVALID_ARG, "%s has a row stride of %lld, below D=%d", m.name, m.ld, D);
+    }
+    const Range rw{weight, (size_t)D * 4}, rdw{dweight, dweight ? (size_t)D * 4 : 0};
+    if (overlaps(rdw, rw)) return set_error(SSD_ERR_INVALID_ARG, "dweight overlaps weight");
+    for (int i = 0; i < n; ++i) {
+        const Range ri = norm_range(mats[i], rows, D);
+        if (overlaps(rdw, ri)) return set_error(SSD_ERR_INVALID_ARG, "dweight overlaps %s", mats[i].name);
+        if (!mats[i].written) continue;
+        if (overlaps(ri, rw)) return set_error(SSD_ERR_INVALID_ARG, "%s overlaps weight", mats[i].name);
+        for (int j = 0; j < n; ++j) {
+            if (j == i || (mats[j].written && j < i)) continue;
+            if (i == inplace_out && j == inplace_in && mats[i].p == mats[j].p && mats[i].ld == mats[j].ld) continue;
+            if (overlaps(ri, norm_range(mats[j], rows, D)))
+                return set_error(SSD_ERR_INVALID_ARG, "%s overlaps %s", mats[i].name, mats[j].name);
+        }
+    }
+    return SSD_OK;
+}
+
+// The backward passes' workspace: needed for dweight only.
+static int check_norm_workspace(long long rows, int D, int groups, const NormMat* mats, int n, const float* weight,
+                                const float* dweight, void* ws, size_t ws_bytes) {
+    if (!dweight) return SSD_OK;
+    const size_t need = norm_workspace_bytes(rows, D, groups);
+    if (!ws || ws_bytes < need) return set_error(SSD_ERR_WORKSPACE, "workspace %zu bytes at %p, need %zu", ws_bytes, ws, need);
+    if (!aligned16(ws)) return set_error(SSD_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    const Range rws{ws, need};
+    if (overlaps(rws, {weight, (size_t)D * 4}) || overlaps(rws, {dweight, (size_t)D * 4}))
+        return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps weight or dweight");
+    for (int i = 0; i < n; ++i)
+        if (overlaps(rws, norm_range(mats[i], rows, D)))
+            return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps %s", mats[i].name);
+    return SSD_OK;
+}
+
+static int elem_bytes(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+
+size_t ssd_norm_backward_workspace_size(long long rows, int D, int groups) {
+    if (rows < 1 || D < 1 || groups < 1 || D % groups || D / groups > kNormMaxLen || groups > kMaxGridYZ) return 0;
+    return norm_workspace_bytes(rows, D, groups);
+}
+
+int ssd_residual_norm(long long rows, int D, int io_dtype, int res_dtype, const void* x, long long ld_x,
+                      const void* residual, long long ld_residual, float scale, const float* weight, float eps,
+                      void* out, long long ld_out, void* residual_out, long long ld_residual_out, void* stream) {
+    g_detail[0] = 0;
+    const int eb = elem_bytes(io_dtype), rb = elem_bytes(res_dtype);
+    const NormMat mats[] = {{"x", x, ld_x, eb, true, false},
+                            {"residual", residual, ld_residual, rb, false, false},
+                            {"out", out, ld_out, eb, true, true},
+                            {"residual_out", residual_out, ld_residual_out, rb, false, true}};
+    SSD_CHECK(check_norm(rows, D, 1, io_dtype, res_dtype, eps, mats, 4, weight, nullptr, 1, 3));
+    if (!std::isfinite(scale)) return set_error(SSD_ERR_INVALID_ARG, "scale must be finite");
+    if (rows == 0) return SSD_OK;
+    return launch_residual_norm(rows, D, io_dtype, res_dtype, x, ld_x, residual, ld_residual, scale, weight, eps, out,
+                                ld_out, residual_out, ld_residual_out, static_cast<cudaStream_t>(stream));
+}
+
+int ssd_residual_norm_backward(long long rows, int D, int io_dtype, int res_dtype, const void* dout, long long ld_dout,
+                               const void* r, long long ld_r, const float* weight, const void* dresidual_out,
+                               long long ld_dresidual_out, float scale, float eps, void* dx, long long ld_dx,
+                               void* dresidual, long long ld_dresidual, float* dweight, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    g_detail[0] = 0;
+    const int eb = elem_bytes(io_dtype), rb = elem_bytes(res_dtype);
+    const NormMat mats[] = {{"dout", dout, ld_dout, eb, true, false},
+                            {"r", r, ld_r, rb, true, false},
+                            {"dresidual_out", dresidual_out, ld_dresidual_out, rb, false, false},
+                            {"dx", dx, ld_dx, eb, false, true},
+                            {"dresidual", dresidual, ld_dresidual, rb, false, true}};
+    SSD_CHECK(check_norm(rows, D, 1, io_dtype, res_dtype, eps, mats, 5, weight, dweight, 2, 4));
+    if (!std::isfinite(scale)) return set_error(SSD_ERR_INVALID_ARG, "scale must be finite");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // no rows: nothing but an empty sum
+        if (dweight) SSD_CUDA_TRY(cudaMemsetAsync(dweight, 0, (size_t)D * 4, s));
+        return SSD_OK;
+    }
+    SSD_CHECK(check_norm_workspace(rows, D, 1, mats, 5, weight, dweight, workspace, workspace_bytes));
+    return launch_residual_norm_backward(rows, D, io_dtype, res_dtype, dout, ld_dout, r, ld_r, weight, dresidual_out,
+                                         ld_dresidual_out, scale, eps, dx, ld_dx, dresidual, ld_dresidual, dweight,
+                                         workspace, s);
+}
+
+int ssd_gated_norm(long long rows, int D, int groups, int io_dtype, int norm_before_gate, const void* y, long long ld_y,
+                   const void* z, long long ld_z, const float* weight, float eps, void* out, long long ld_out,
+                   void* stream) {
+    g_detail[0] = 0;
+    const int eb = elem_bytes(io_dtype);
+    const NormMat mats[] = {{"y", y, ld_y, eb, true, false}, {"z", z, ld_z, eb, true, false},
+                            {"out", out, ld_out, eb, true, true}};
+    if (norm_before_gate != 0 && norm_before_gate != 1)
+        return set_error(SSD_ERR_INVALID_ARG, "norm_before_gate is %d, not 0 or 1", norm_before_gate);
+    SSD_CHECK(check_norm(rows, D, groups, io_dtype, SSD_F32, eps, mats, 3, weight, nullptr, -1, -1));
+    if (rows == 0) return SSD_OK;
+    return launch_gated_norm(rows, D, groups, io_dtype, norm_before_gate, y, ld_y, z, ld_z, weight, eps, out, ld_out,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int ssd_gated_norm_backward(long long rows, int D, int groups, int io_dtype, int norm_before_gate, const void* dout,
+                            long long ld_dout, const void* y, long long ld_y, const void* z, long long ld_z,
+                            const float* weight, float eps, void* dy, long long ld_dy, void* dz, long long ld_dz,
+                            float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+    g_detail[0] = 0;
+    const int eb = elem_bytes(io_dtype);
+    const NormMat mats[] = {{"dout", dout, ld_dout, eb, true, false}, {"y", y, ld_y, eb, true, false},
+                            {"z", z, ld_z, eb, true, false},          {"dy", dy, ld_dy, eb, true, true},
+                            {"dz", dz, ld_dz, eb, true, true}};
+    if (norm_before_gate != 0 && norm_before_gate != 1)
+        return set_error(SSD_ERR_INVALID_ARG, "norm_before_gate is %d, not 0 or 1", norm_before_gate);
+    SSD_CHECK(check_norm(rows, D, groups, io_dtype, SSD_F32, eps, mats, 5, weight, dweight, -1, -1));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        if (dweight) SSD_CUDA_TRY(cudaMemsetAsync(dweight, 0, (size_t)D * 4, s));
+        return SSD_OK;
+    }
+    SSD_CHECK(check_norm_workspace(rows, D, groups, mats, 5, weight, dweight, workspace, workspace_bytes));
+    return launch_gated_norm_backward(rows, D, groups, io_dtype, norm_before_gate, dout, ld_dout, y, ld_y, z, ld_z,
+                                      weight, eps, dy, ld_dy, dz, ld_dz, dweight, workspace, s);
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@ SSD_F32, SSD_BF16 = 0, 1
 SSD_ACT_NONE, SSD_ACT_SILU = 0, 1
 
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 _sz = ctypes.c_size_t
 _vp = ctypes.c_void_p
 
@@ -91,6 +92,19 @@ def lib() -> ctypes.CDLL:
         L.ssd_decode_loop.restype = _i
         L.ssd_decode_step_noalloc.argtypes = [_i] * 9 + [_vp] * 10
         L.ssd_decode_step_noalloc.restype = _i
+        f = ctypes.c_float
+        mat = [_vp, _ll]  # pointer, row stride
+        L.ssd_norm_backward_workspace_size.argtypes = [_ll, _i, _i]
+        L.ssd_norm_backward_workspace_size.restype = _sz
+        L.ssd_residual_norm.argtypes = [_ll, _i, _i, _i] + mat * 2 + [f, _vp, f] + mat * 2 + [_vp]
+        L.ssd_residual_norm.restype = _i
+        L.ssd_residual_norm_backward.argtypes = ([_ll, _i, _i, _i] + mat * 2 + [_vp] + mat + [f, f] + mat * 2 +
+                                                 [_vp, _vp, _sz, _vp])
+        L.ssd_residual_norm_backward.restype = _i
+        L.ssd_gated_norm.argtypes = [_ll] + [_i] * 4 + mat * 2 + [_vp, f] + mat + [_vp]
+        L.ssd_gated_norm.restype = _i
+        L.ssd_gated_norm_backward.argtypes = [_ll] + [_i] * 4 + mat * 3 + [_vp, f] + mat * 2 + [_vp, _vp, _sz, _vp]
+        L.ssd_gated_norm_backward.restype = _i
         L.ssd_launch_count.restype = ctypes.c_uint64
         L.ssd_profile_begin.restype = _i
         L.ssd_profile_end.argtypes = [ctypes.POINTER(_KernelTime), _i]
@@ -445,3 +459,154 @@ def decode_loop(h, conv_state, xbc_ring, dt_ring, A, D, conv_w, conv_b, n_steps,
     _check(st, "ssd_decode_loop")
     torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
     return y_ring
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """A norm operand as (rows, D, row stride): CUDA, last index contiguous, the leading indices
+    evenly spaced (a slice of a wider row is fine)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % name)
+    if t.dim() < 1:
+        raise ValueError("%s must have at least one dimension" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    D = t.shape[-1]
+    rows = t.numel() // D if D else 0
+    if rows == 0 or t.is_contiguous():
+        return rows, D, D
+    if D > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    ld = None  # leading indices of size 1 have no say in the spacing
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] == 1:
+            continue
+        if ld is None:
+            ld, span = t.stride(i), t.stride(i) * t.shape[i]
+        elif t.stride(i) != span:
+            raise ValueError("%s: its rows are not evenly spaced" % name)
+        else:
+            span *= t.shape[i]
+    ld = D if ld is None else ld
+    if ld < D:
+        raise ValueError("%s: its rows overlap (row stride %d, %d elements)" % (name, ld, D))
+    return rows, D, ld
+
+
+def norm_backward_workspace_size(rows, D, groups=1) -> int:
+    return int(lib().ssd_norm_backward_workspace_size(rows, D, groups))
+
+
+def _norm_workspace(workspace, rows, D, groups, want, device):
+    if workspace is None and want:
+        need = norm_backward_workspace_size(rows, D, groups)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, residual_out=None, stream=None):
+    """The norm ahead of a block, with the residual add in it: r = residual + scale * x,
+    out = r * (mean(r^2) + eps)^(-1/2) * weight over the last dimension.  x [..., D] bf16 or fp32,
+    weight [D] fp32, residual [..., D] fp32 (or bf16 beside bf16 x) or None (r = scale * x).
+    Returns (out, r): out in x's type, r in the residual's (fp32 without one, or residual_out's).
+    residual_out may be the residual itself (updated in place).  Operands may be slices of wider rows."""
+    rows, D, ld_x = _rows(x, "x")
+    io = _io(x)
+    _need(weight, "weight", torch.float32, (D,))
+    ld_res = 0
+    if residual is not None:
+        _, _, ld_res = _rows(residual, "residual", None, x.shape)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=torch.float32 if residual is None else residual.dtype, device=x.device)
+    _, _, ld_ro = _rows(residual_out, "residual_out", None if residual is None else residual.dtype, x.shape)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _, _, ld_out = _rows(out, "out", x.dtype, x.shape)
+    _check_device(x.device, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    st = lib().ssd_residual_norm(rows, D, io, _io(residual_out), _ptr(x), ld_x, _ptr(residual), ld_res, float(scale),
+                                 _ptr(weight), float(eps), _ptr(out), ld_out, _ptr(residual_out), ld_ro,
+                                 _stream(stream))
+    _check(st, "ssd_residual_norm")
+    return out, residual_out
+
+
+def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1e-5, dx=None, dresidual=None,
+                           dweight=None, want_dresidual=True, workspace=None, stream=None):
+    """Gradients of residual_norm from r as it returned it: dout the gradient of out, dresidual_out
+    that of r (None: zero).  Returns (dx, dresidual, dweight): dx in dout's type, dresidual in r's
+    (None with want_dresidual=False), dweight [D] fp32.  dresidual may be dresidual_out itself."""
+    rows, D, ld_do = _rows(dout, "dout")
+    io = _io(dout)
+    _, _, ld_r = _rows(r, "r", None, dout.shape)
+    _need(weight, "weight", torch.float32, (D,))
+    ld_dro = ld_dres = 0
+    if dresidual_out is not None:
+        _, _, ld_dro = _rows(dresidual_out, "dresidual_out", r.dtype, r.shape)
+    if dx is None:
+        dx = torch.empty(dout.shape, dtype=dout.dtype, device=dout.device)
+    _, _, ld_dx = _rows(dx, "dx", dout.dtype, dout.shape)
+    if dresidual is None and want_dresidual:
+        dresidual = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    if dresidual is not None:
+        _, _, ld_dres = _rows(dresidual, "dresidual", r.dtype, r.shape)
+    if dweight is None:
+        dweight = torch.empty(D, dtype=torch.float32, device=dout.device)
+    _need(dweight, "dweight", torch.float32, (D,))
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, True, dout.device)
+    _check_device(dout.device, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
+                  dweight=dweight, workspace=workspace)
+    st = lib().ssd_residual_norm_backward(rows, D, io, _io(r), _ptr(dout), ld_do, _ptr(r), ld_r, _ptr(weight),
+                                          _ptr(dresidual_out), ld_dro, float(scale), float(eps), _ptr(dx), ld_dx,
+                                          _ptr(dresidual), ld_dres, _ptr(dweight), _ptr(workspace), ws_bytes,
+                                          _stream(stream))
+    _check(st, "ssd_residual_norm_backward")
+    return dx, dresidual, dweight
+
+
+def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=None, stream=None):
+    """The norm behind the SSD with its SiLU gate, over groups of D / groups elements of the last
+    dimension: norm(y * silu(z)) * weight, or norm(y) * weight * silu(z) with norm_before_gate.
+    y, z [..., D] bf16 or fp32 (either may be a slice of a wider row), weight [D] fp32."""
+    rows, D, ld_y = _rows(y, "y")
+    io = _io(y)
+    _, _, ld_z = _rows(z, "z", y.dtype, y.shape)
+    _need(weight, "weight", torch.float32, (D,))
+    if out is None:
+        out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
+    _check_device(y.device, z=z, weight=weight, out=out)
+    st = lib().ssd_gated_norm(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
+                              _ptr(weight), float(eps), _ptr(out), ld_out, _stream(stream))
+    _check(st, "ssd_gated_norm")
+    return out
+
+
+def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, dy=None, dz=None,
+                        dweight=None, workspace=None, stream=None):
+    """Gradients of gated_norm: returns (dy, dz, dweight), dweight [D] fp32.  dy and dz may be
+    slices of wider rows (the input projection's gradient)."""
+    rows, D, ld_do = _rows(dout, "dout")
+    io = _io(dout)
+    _, _, ld_y = _rows(y, "y", dout.dtype, dout.shape)
+    _, _, ld_z = _rows(z, "z", dout.dtype, dout.shape)
+    _need(weight, "weight", torch.float32, (D,))
+    if dy is None:
+        dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    _, _, ld_dy = _rows(dy, "dy", y.dtype, y.shape)
+    if dz is None:
+        dz = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    _, _, ld_dz = _rows(dz, "dz", y.dtype, y.shape)
+    if dweight is None:
+        dweight = torch.empty(D, dtype=torch.float32, device=y.device)
+    _need(dweight, "dweight", torch.float32, (D,))
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, groups, True, y.device)
+    _check_device(dout.device, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
+    st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
+                                       _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,
+                                       _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st, "ssd_gated_norm_backward")
+    return dy, dz, dweight
