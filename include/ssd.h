@@ -346,6 +346,41 @@ SSD_API int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int k
                             void* y_ring, int n_steps, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Gradients of the prefill  (the recurrence run backwards in the same chunked dual form)
+ *
+ * For the prefill of the same x, dt, A, B, C, D, h0 (shapes and types as there), given dy, the
+ * gradient of y (x's type), and dh_final, that of h_final (fp32; NULL: zero):
+ *   dx [b][T][H][P], dB, dC [b][T][G][N]  io dtype; a group's dB and dC sum over its heads
+ *   ddt [b][T][H], dA, dD [H]             fp32
+ *   dh0 [b][H][P][N]                      fp32, or NULL to skip
+ * Nothing from the forward call is needed: the states between chunks are recomputed.
+ * ssd_prefill_backward_dt_raw is the gradient of ssd_prefill_dt_raw: ddt_raw is that of the raw
+ * step, ddt_bias [H] (NULL: skip) its sum over sequences and tokens; a step outside the clamp
+ * range passes no gradient, one on a limit does.
+ * T == 0 or b == 0: dA, dD, ddt_bias are zero and dh0 = dh_final (or zero).
+ * Arithmetic: every path sums in fp32 (the decays' prefix sums and the sums over chunks in
+ * fp64) and rounds a stored gradient once.
+ * Written buffers and the workspace must overlap nothing.  No atomics: the same call gives
+ * bitwise the same gradients.
+ * Errors: as for ssd_prefill; SSD_ERR_UNSUPPORTED also where b * T * H exceeds what one launch
+ * holds (2^31 chunks of 64 tokens times heads).
+ * ---------------------------------------------------------------------------------- */
+SSD_API size_t ssd_prefill_backward_workspace_size(int b, int T, int H, int P, int N, int G, int io_dtype);
+
+SSD_API int ssd_prefill_backward(int b, int T, int H, int P, int N, int G, int io_dtype, const void* dy,
+                                 const void* x, const float* dt, const float* A, const void* B, const void* C,
+                                 const float* D, const float* h0, const float* dh_final, void* dx, float* ddt,
+                                 float* dA, void* dB, void* dC, float* dD, float* dh0, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+SSD_API int ssd_prefill_backward_dt_raw(int b, int T, int H, int P, int N, int G, int io_dtype, const void* dy,
+                                        const void* x, const float* dt_raw, const float* dt_bias, float dt_min,
+                                        float dt_max, const float* A, const void* B, const void* C, const float* D,
+                                        const float* h0, const float* dh_final, void* dx, float* ddt_raw,
+                                        float* ddt_bias, float* dA, void* dB, void* dC, float* dD, float* dh0,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Norms around a block  (the block the SSD sits in: a norm of the residual stream ahead of
  * its input projection, a gated norm between the SSD and its output projection)
  *

@@ -10,6 +10,7 @@ from .ssd import (  # noqa: F401
     SSD_BF16,
     SSD_F32,
     DecodePlan,
+    PrefillGrads,
     SSDError,
     debug_decay_precision,
     debug_force_fma_prefill,
@@ -29,6 +30,8 @@ from .ssd import (  # noqa: F401
     profile_begin,
     profile_end,
     prefill,
+    prefill_backward,
+    prefill_backward_workspace_size,
     prefill_check,
     prefill_context_scan,
     prefill_local_state,

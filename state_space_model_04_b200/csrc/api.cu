@@ -2,6 +2,7 @@
 //
 // Host-side only: argument validation (before anything is enqueued), workspace carving
 // and dispatch to the sm_100a kernels.  No device memory is allocated here.
+#include "backward.cuh"
 #include "common.cuh"
 
 #include <stdarg.h>
@@ -54,6 +55,9 @@ int create_decode_plan(ssd_decode_plan** out, int layers, int b, int H, int N, i
 int launch_decode_plan(ssd_decode_plan* plan, cudaStream_t s);
 int destroy_decode_plan(ssd_decode_plan* plan);
 int decode_noalloc_scratch(void** ptr, size_t* bytes);
+size_t backward_simt_workspace_bytes(const BwdArgs& a);
+bool backward_simt_fits(const BwdArgs& a);
+int launch_backward_simt(const BwdArgs& a, void* ws, cudaStream_t s);
 size_t norm_workspace_bytes(long long rows, int D, int groups);
 int launch_residual_norm(long long rows, int D, int io, int res_dtype, const void* x, long long ld_x,
                          const void* res, long long ld_res, float scale, const float* w, float eps, void* out,
@@ -602,6 +606,100 @@ int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int kconv, in
     // an executable graph destroyed while in flight is freed when it completes
     const int st2 = destroy_decode_plan(plan);
     return st != SSD_OK ? st : st2;
+}
+
+// ---- gradients of the prefill
+
+static size_t backward_ws_bytes(const BwdArgs& a) { return kStatusBytes + backward_simt_workspace_bytes(a); }
+
+static BwdArgs backward_shape(int b, int T, int H, int N, int G, int io) {
+    BwdArgs a = {};
+    a.b = b, a.T = T, a.H = H, a.N = N, a.G = G, a.io = io;
+    return a;
+}
+
+size_t ssd_prefill_backward_workspace_size(int b, int T, int H, int P, int N, int G, int io_dtype) {
+    if (check_prefill_shape(b, T, H, P, N, G, 64, io_dtype) != SSD_OK) return 0;
+    if (b == 0 || T == 0) return 0;
+    const BwdArgs a = backward_shape(b, T, H, N, G, io_dtype);
+    return backward_simt_fits(a) ? backward_ws_bytes(a) : 0;
+}
+
+static int backward_impl(const BwdArgs& a, int P, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    const int b = a.b, T = a.T, H = a.H, N = a.N, G = a.G;
+    SSD_CHECK(check_prefill_shape(b, T, H, P, N, G, 64, a.io));
+    const size_t io_b = a.io == SSD_BF16 ? 2 : 4, tok = (size_t)b * T;
+    const size_t state = (size_t)b * H * P * N * sizeof(float), xb = tok * H * P * io_b, bb = tok * G * N * io_b,
+                 db = tok * H * 4, hb = (size_t)H * 4;
+    struct Buf {
+        const char* name;
+        const void* p;
+        size_t n;
+        bool required;
+    };
+    const Buf ins[] = {{"dy", a.dy, xb, true},     {"x", a.x, xb, true},     {"dt", a.dt, db, true},
+                       {"A", a.A, hb, true},       {"B", a.B, bb, true},     {"C", a.C, bb, true},
+                       {"D", a.D, hb, true},       {"h0", a.h0, state, false},
+                       {"dh_final", a.dhf, state, false}, {"dt_bias", a.dtm.bias, hb, false}};
+    const Buf outs[] = {{"dx", a.dx, xb, true},    {"ddt", a.ddt, db, true}, {"dA", a.dA, hb, true},
+                        {"dB", a.dB, bb, true},    {"dC", a.dC, bb, true},   {"dD", a.dD, hb, true},
+                        {"dh0", a.dh0, state, false}, {"ddt_bias", a.dbias, hb, false}};
+    const bool empty = b == 0 || T == 0;
+    for (const Buf& i : ins) SSD_CHECK(check_ptr(i.p, i.name, i.required && !empty));
+    for (const Buf& o : outs) SSD_CHECK(check_ptr(o.p, o.name, o.required && (o.n == hb || !empty)));
+    for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
+        for (const Buf& in : ins)
+            if (overlaps({outs[i].p, outs[i].n}, {in.p, in.n}))
+                return set_error(SSD_ERR_INVALID_ARG, "%s overlaps input %s", outs[i].name, in.name);
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps({outs[i].p, outs[i].n}, {outs[j].p, outs[j].n}))
+                return set_error(SSD_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+    }
+    if (empty) {  // no tokens: empty sums, and the state's adjoint passes through unchanged
+        SSD_CUDA_TRY(cudaMemsetAsync(a.dA, 0, hb, s));
+        SSD_CUDA_TRY(cudaMemsetAsync(a.dD, 0, hb, s));
+        if (a.dbias) SSD_CUDA_TRY(cudaMemsetAsync(a.dbias, 0, hb, s));
+        if (a.dh0 && state) {
+            if (a.dhf) SSD_CUDA_TRY(cudaMemcpyAsync(a.dh0, a.dhf, state, cudaMemcpyDeviceToDevice, s));
+            else SSD_CUDA_TRY(cudaMemsetAsync(a.dh0, 0, state, s));
+        }
+        return SSD_OK;
+    }
+    if (!backward_simt_fits(a)) return set_error(SSD_ERR_UNSUPPORTED, "b * T * H too large for one call");
+    const size_t need = backward_ws_bytes(a);
+    if (!workspace || workspace_bytes < need)
+        return set_error(SSD_ERR_WORKSPACE, "workspace %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
+    if (!aligned16(workspace)) return set_error(SSD_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    for (const Buf& i : ins)
+        if (overlaps({workspace, need}, {i.p, i.n})) return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps %s", i.name);
+    for (const Buf& o : outs)
+        if (overlaps({workspace, need}, {o.p, o.n})) return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps %s", o.name);
+    SSD_CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), s));
+    return launch_backward_simt(a, static_cast<char*>(workspace) + kStatusBytes, s);
+}
+
+int ssd_prefill_backward(int b, int T, int H, int P, int N, int G, int io_dtype, const void* dy, const void* x,
+                         const float* dt, const float* A, const void* B, const void* C, const float* D,
+                         const float* h0, const float* dh_final, void* dx, float* ddt, float* dA, void* dB, void* dC,
+                         float* dD, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+    g_detail[0] = 0;
+    const BwdArgs a{b, T, H, N, G, io_dtype, dy, x, dt, DtMap{nullptr, 0.f, 0.f, 0}, A, B, C, D, h0, dh_final,
+                    dx, ddt, dA, dB, dC, dD, dh0, nullptr};
+    return backward_impl(a, P, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int ssd_prefill_backward_dt_raw(int b, int T, int H, int P, int N, int G, int io_dtype, const void* dy, const void* x,
+                                const float* dt_raw, const float* dt_bias, float dt_min, float dt_max, const float* A,
+                                const void* B, const void* C, const float* D, const float* h0, const float* dh_final,
+                                void* dx, float* ddt_raw, float* ddt_bias, float* dA, void* dB, void* dC, float* dD,
+                                float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+    g_detail[0] = 0;
+    if (!(dt_min >= 0.f) || !(dt_max > dt_min))  // also rejects NaN limits
+        return set_error(SSD_ERR_INVALID_ARG, "dt clamp range [%g, %g] must satisfy 0 <= dt_min < dt_max",
+                         (double)dt_min, (double)dt_max);
+    const BwdArgs a{b, T, H, N, G, io_dtype, dy, x, dt_raw, DtMap{dt_bias, dt_min, dt_max, 1}, A, B, C, D, h0, dh_final,
+                    dx, ddt_raw, dA, dB, dC, dD, dh0, ddt_bias};
+    return backward_impl(a, P, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 // ---- norms around a block

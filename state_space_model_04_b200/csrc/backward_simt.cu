@@ -1,0 +1,615 @@
+// backward_simt.cu -- gradients of the SSD prefill on the fp32 pipes: every fp32 call, and bf16
+// calls whose shape the tensor-core path does not take.
+//
+// The recurrence h_t = e^{a_t} h_{t-1} + dt_t x_t B_t^T, y_t = h_t C_t + D x_t (a = dt A) and its
+// adjoint run in the chunked dual form, kQ = 64 tokens a chunk.  With cs the prefix sum of a in
+// the chunk, L_ij = exp(cs_i - cs_j) for i >= j, S = C B^T, Gm = dy x^T, h the state entering
+// the chunk and dh the adjoint of the state leaving it:
+//   dx_j = dt_j U_j + D dy_j,   U_j = sum_i S_ij L_ij dy_i + exp(cs_Q - cs_j) dh B_j
+//   dC_i = sum_j dS_ij B_j + exp(cs_i) h^T dy_i,        dS_ij = Gm_ij L_ij dt_j
+//   dB_j = sum_i dS_ij C_i + dt_j exp(cs_Q - cs_j) dh^T x_j
+//   ddt_t = x_t . U_t + A da_t
+//   da_t = exp(cs_Q) <h, dh> + sum_{i >= t} E_i + sum_{j < t} F_j + sum_{i >= t > j} W_ij
+//   W = Gm S L dt,  E_i = exp(cs_i) dy_i . h C_i,  F_j = dt_j exp(cs_Q - cs_j) x_j . dh B_j
+// da_t adds the pairs (i, j) that straddle t, as a suffix sum of W's row sums less its column
+// sums over i > j: both sums are of the same fp32 numbers, so what has to cancel does, and no
+// term of the whole sequence's length enters.
+//
+// Launches: per-token decay terms; the chunks' own states in both directions; a scan over the
+// chunks (in place: slot c ends up with the state entering chunk c, or the adjoint of the state
+// leaving it); the gradients per chunk, a block walking heads of one B/C group with dB and dC
+// in registers; sums.  Bound by the fp32 pipes: per token and head about 57,000 multiply-adds
+// at N = 128 against 6 KB of state traffic.
+#include <algorithm>
+#include "backward.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kQ = 64, kP = 64;
+constexpr int kThreads = 256;
+
+struct SimtBwd {
+    BwdArgs a;
+    int nc;       // chunks a sequence
+    int splits;   // blocks a (chunk, group)
+    float* dtv;   // [b nc][H][kQ] step sizes, 0 past the end
+    double* cs;   // [b nc][H][kQ] inclusive prefix sums of dt A
+    float* e;     // [b nc][H][kQ] exp(cs)
+    float* w;     // [b nc][H][kQ] exp(cs_Q - cs)
+    float* hs;    // [b nc][H][P][N] the chunk's own state, then the state entering it
+    float* gs;    // [b nc][H][P][N] the chunk's own adjoint, then the adjoint of the state leaving it
+    float* part;  // [2][splits][b][T][G][N] sums of dB, dC over a block's heads (splits > 1)
+    float *pA, *pD, *pb;  // [b nc][H] sums of dA, dD and the bias gradient over a chunk
+};
+
+// Tiles are [rows][W] floats; the 16-byte piece c of row r sits at piece c ^ (r / 4 % 8), so that
+// threads reading 8 rows 4 apart at one piece, or 8 pieces of one row, meet no bank conflict.
+template <int W> __device__ __forceinline__ int at(int r, int c4) { return r * W + ((c4 ^ ((r >> 2) & 7)) << 2); }
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), c = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    u.x = *reinterpret_cast<const uint32_t*>(&a);
+    u.y = *reinterpret_cast<const uint32_t*>(&c);
+    *reinterpret_cast<uint2*>(p) = u;
+}
+
+// A [kQ][W] tile from rows `stride` elements apart; rows from `valid` on are zero.
+template <int W, typename T>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, size_t stride, int valid) {
+    for (int i = threadIdx.x; i < kQ * (W / 4); i += kThreads) {
+        const int r = i / (W / 4), c = i % (W / 4);
+        const float4 v = r < valid ? ld4(src + r * stride + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + at<W>(r, c)) = v;
+    }
+}
+
+// acc[a][b] += sum_k A[4 ty + a][k] B[4 tx + b][k]  (both along rows)
+template <int K>
+__device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+#pragma unroll 4
+    for (int k = 0; k < K / 4; ++k) {
+        float4 av[4], bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = ld4(A + at<K>(4 * ty + i, k)), bv[i] = ld4(B + at<K>(4 * tx + i, k));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(av[i].x, bv[j].x, acc[i][j]);
+                acc[i][j] = fmaf(av[i].y, bv[j].y, acc[i][j]);
+                acc[i][j] = fmaf(av[i].z, bv[j].z, acc[i][j]);
+                acc[i][j] = fmaf(av[i].w, bv[j].w, acc[i][j]);
+            }
+    }
+}
+__device__ __forceinline__ void axpy4(float s, float4 v, float* acc) {
+    acc[0] = fmaf(s, v.x, acc[0]);
+    acc[1] = fmaf(s, v.y, acc[1]);
+    acc[2] = fmaf(s, v.z, acc[2]);
+    acc[3] = fmaf(s, v.w, acc[3]);
+}
+// acc[a][...] += s_a sum_k A[4 ty + a][k] B[k][columns 4 tx .. and 64 + 4 tx ..]   (K = 64, B [64][W])
+template <int W>
+__device__ __forceinline__ void mm_nn(const float* A, const float* B, int ty, int tx, const float (&s)[4],
+                                      float (&acc)[4][W / 16]) {
+#pragma unroll 2
+    for (int k = 0; k < 16; ++k) {
+        float4 av[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            av[i] = ld4(A + at<64>(4 * ty + i, k));
+            av[i].x *= s[i], av[i].y *= s[i], av[i].z *= s[i], av[i].w *= s[i];
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int n = 0; n < W / 64; ++n) {
+                const float4 bv = ld4(B + at<W>(4 * k + kk, tx + 16 * n));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float m = kk == 0 ? av[i].x : kk == 1 ? av[i].y : kk == 2 ? av[i].z : av[i].w;
+                    axpy4(m, bv, &acc[i][4 * n]);
+                }
+            }
+    }
+}
+// acc[a][...] += sum_k A[k][4 ty + a] B[k][columns 4 tx .. and 64 + 4 tx ..]   (A [64][64], B [64][W])
+template <int W>
+__device__ __forceinline__ void mm_tn(const float* A, const float* B, int ty, int tx, float (&acc)[4][W / 16]) {
+#pragma unroll 4
+    for (int k = 0; k < 64; ++k) {
+        const float4 av = ld4(A + at<64>(k, ty));
+#pragma unroll
+        for (int n = 0; n < W / 64; ++n) {
+            const float4 bv = ld4(B + at<W>(k, tx + 16 * n));
+            axpy4(av.x, bv, &acc[0][4 * n]);
+            axpy4(av.y, bv, &acc[1][4 * n]);
+            axpy4(av.z, bv, &acc[2][4 * n]);
+            axpy4(av.w, bv, &acc[3][4 * n]);
+        }
+    }
+}
+
+// ---- per-token decay terms: one warp per (chunk, head), two tokens a lane
+__global__ void __launch_bounds__(kThreads) ssd_bwd_terms_kernel(const SimtBwd p) {
+    const int lane = threadIdx.x & 31, h = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
+    if (h >= p.a.H) return;
+    const int bc = blockIdx.x, bi = bc / p.nc, t0 = (bc % p.nc) * kQ;
+    const double Ah = p.a.A[h];
+    float dt[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int t = t0 + 2 * lane + k;
+        dt[k] = t < p.a.T ? dt_value(p.a.dt[((size_t)bi * p.a.T + t) * p.a.H + h], p.a.dtm, h) : 0.f;
+    }
+    const double a0 = dt[0] * Ah, a1 = dt[1] * Ah;
+    double s = a0 + a1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+    }
+    const double tot = __shfl_sync(0xffffffffu, s, 31);
+    const size_t o = ((size_t)bc * p.a.H + h) * kQ + 2 * lane;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const double c = k ? s : s - a1;
+        p.dtv[o + k] = dt[k];
+        p.cs[o + k] = c;
+        p.e[o + k] = expf((float)c);
+        p.w[o + k] = expf((float)(tot - c));
+    }
+}
+
+// ---- the chunk's own states: z = 0: sum_j dt_j w_j x_j B_j^T, z = 1: sum_i e_i dy_i C_i^T
+template <typename TIO, int N>
+__global__ void __launch_bounds__(kThreads) ssd_bwd_chunk_states_kernel(const SimtBwd p) {
+    extern __shared__ float sm[];
+    float *sx = sm, *sb = sm + kQ * kP;
+    const int h = blockIdx.x % p.a.H, bc = blockIdx.x / p.a.H, dir = blockIdx.y;
+    const int bi = bc / p.nc, t0 = (bc % p.nc) * kQ, g = h / (p.a.H / p.a.G);
+    const int valid = min(kQ, p.a.T - t0);
+    const size_t tok = (size_t)bi * p.a.T + t0;
+    const TIO* xs = static_cast<const TIO*>(dir ? p.a.dy : p.a.x) + (tok * p.a.H + h) * kP;
+    const TIO* bs = static_cast<const TIO*>(dir ? p.a.C : p.a.B) + (tok * p.a.G + g) * N;
+    load_tile<N>(sb, bs, (size_t)p.a.G * N, valid);
+    const size_t o = (size_t)blockIdx.x * kQ;
+    for (int i = threadIdx.x; i < kQ * (kP / 4); i += kThreads) {
+        const int r = i / (kP / 4), c = i % (kP / 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < valid) {
+            v = ld4(xs + (size_t)r * p.a.H * kP + 4 * c);
+            const float s = dir ? p.e[o + r] : p.w[o + r] * p.dtv[o + r];
+            v.x *= s, v.y *= s, v.z *= s, v.w *= s;
+        }
+        *reinterpret_cast<float4*>(sx + at<64>(r, c)) = v;
+    }
+    __syncthreads();
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    float acc[4][N / 16] = {};
+    mm_tn<N>(sx, sb, ty, tx, acc);
+    float* dst = (dir ? p.gs : p.hs) + (size_t)blockIdx.x * kP * N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < N / 64; ++n)
+            st4(dst + (4 * ty + i) * N + 64 * n + 4 * tx,
+                make_float4(acc[i][4 * n], acc[i][4 * n + 1], acc[i][4 * n + 2], acc[i][4 * n + 3]));
+}
+
+// ---- scan over the chunks, four state entries a thread; z = 0 forwards, z = 1 backwards
+constexpr int kAhead = 8;  // chunks loaded ahead of the dependent updates
+__global__ void __launch_bounds__(kThreads) ssd_bwd_state_scan_kernel(const SimtBwd p) {
+    const int pn = kP * p.a.N, per = pn / (4 * kThreads);
+    const int u = blockIdx.x / per, el = ((blockIdx.x % per) * kThreads + threadIdx.x) * 4;
+    const int h = u % p.a.H, bi = u / p.a.H, dir = blockIdx.y;
+    const float* init = dir ? p.a.dhf : p.a.h0;
+    float4 run = init ? ld4(init + (size_t)u * pn + el) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float* st = dir ? p.gs : p.hs;
+    auto slot = [&](int k) {  // the k-th chunk walked
+        return ((size_t)bi * p.nc + (dir ? p.nc - 1 - k : k)) * p.a.H + h;
+    };
+    for (int k0 = 0; k0 < p.nc; k0 += kAhead) {
+        float4 v[kAhead];
+        float gam[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (k0 + j < p.nc) {
+                v[j] = ld4(st + slot(k0 + j) * pn + el);
+                gam[j] = p.e[slot(k0 + j) * kQ + kQ - 1];
+            }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (k0 + j < p.nc) {
+                st4(st + slot(k0 + j) * pn + el, run);
+                run.x = fmaf(gam[j], run.x, v[j].x);
+                run.y = fmaf(gam[j], run.y, v[j].y);
+                run.z = fmaf(gam[j], run.z, v[j].z);
+                run.w = fmaf(gam[j], run.w, v[j].w);
+            }
+    }
+    if (dir && p.a.dh0) st4(p.a.dh0 + (size_t)u * pn + el, run);
+}
+
+// ---- gradients of a chunk
+template <int N> struct MainSmem {
+    static constexpr int kB = 0, kC = kB + kQ * N, kH = kC + kQ * N, kG = kH + kP * N, kX = kG + kP * N,
+                         kY = kX + kQ * kP, kS = kY + kQ * kP, kM = kS + kQ * kQ, kTerms = kM + kQ * kQ;
+    // per-token: dt, e, w, cs (double), row sums, column parts [8], E, direct, F; 8 warp sums x 2
+    static constexpr int kFloats = kTerms + kQ * (3 + 2 + 1 + 8 + 8 + 3) + 32;
+};
+
+template <typename TIO, int N>
+__global__ void __launch_bounds__(kThreads, 1) ssd_bwd_chunk_kernel(const SimtBwd p) {
+    using SM = MainSmem<N>;
+    extern __shared__ float sm[];
+    float *sB = sm + SM::kB, *sC = sm + SM::kC, *sH = sm + SM::kH, *sG = sm + SM::kG, *sX = sm + SM::kX,
+          *sY = sm + SM::kY, *sS = sm + SM::kS, *sM = sm + SM::kM;
+    double* s_cs = reinterpret_cast<double*>(sm + SM::kTerms);
+    float *s_dt = sm + SM::kTerms + 2 * kQ, *s_e = s_dt + kQ, *s_w = s_e + kQ;
+    float* s_row = s_w + kQ;        // [kQ] sum_j W_ij
+    float* s_col = s_row + kQ;      // [8 warps][kQ] parts of sum_i Gm S L (i > j)
+    float* s_dia = s_col + 8 * kQ;  // [kQ] Gm_jj S_jj, and [kQ] Gm_jj behind it
+    float* s_E = s_dia + 2 * kQ;    // [kQ] E_i
+    float* s_F = s_E + kQ;          // [kQ] F_j / dt_j
+    float* s_z = s_F + kQ;          // [8] warp sums of <h, dh>
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+    const int H = p.a.H, G = p.a.G, T = p.a.T, hg = H / G;
+    const int split = blockIdx.x % p.splits, ug = blockIdx.x / p.splits, g = ug % G, bc = ug / G;
+    const int bi = bc / p.nc, t0 = (bc % p.nc) * kQ, valid = min(kQ, T - t0);
+    const size_t tok = (size_t)bi * T + t0;
+    const int h_lo = (int)((long long)split * hg / p.splits), h_hi = (int)((long long)(split + 1) * hg / p.splits);
+
+    load_tile<N>(sB, static_cast<const TIO*>(p.a.B) + (tok * G + g) * N, (size_t)G * N, valid);
+    load_tile<N>(sC, static_cast<const TIO*>(p.a.C) + (tok * G + g) * N, (size_t)G * N, valid);
+    __syncthreads();
+    {
+        float s[4][4] = {};
+        mm_nt<N>(sC, sB, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(sS + at<64>(4 * ty + i, tx)) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+    }
+    float dS[4][4] = {}, dC[4][N / 16] = {}, dB[4][N / 16] = {};
+
+    for (int hh = h_lo; hh < h_hi; ++hh) {
+        const int h = g * hg + hh;
+        const size_t u = (size_t)bc * H + h;
+        __syncthreads();  // the head before has been read
+        load_tile<kP>(sX, static_cast<const TIO*>(p.a.x) + (tok * H + h) * kP, (size_t)H * kP, valid);
+        load_tile<kP>(sY, static_cast<const TIO*>(p.a.dy) + (tok * H + h) * kP, (size_t)H * kP, valid);
+        float z = 0.f;
+        for (int i = tid; i < kP * (N / 4); i += kThreads) {
+            const int r = i / (N / 4), c = i % (N / 4);
+            const float4 a = ld4(p.hs + u * kP * N + 4 * i), d = ld4(p.gs + u * kP * N + 4 * i);
+            *reinterpret_cast<float4*>(sH + at<N>(r, c)) = a;
+            *reinterpret_cast<float4*>(sG + at<N>(r, c)) = d;
+            z = fmaf(a.x, d.x, fmaf(a.y, d.y, fmaf(a.z, d.z, fmaf(a.w, d.w, z))));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) s_z[warp] = z;
+        if (tid < kQ) {
+            s_cs[tid] = p.cs[u * kQ + tid];
+            s_dt[tid] = p.dtv[u * kQ + tid];
+            s_e[tid] = p.e[u * kQ + tid];
+            s_w[tid] = p.w[u * kQ + tid];
+        }
+        __syncthreads();
+        // ---- Gm, M = S L, dS, W's sums (rows i = 4 ty + a, columns j = 4 tx + b)
+        {
+            float gm[4][4] = {}, row[4] = {}, colp[4] = {};
+            mm_nt<kP>(sY, sX, ty, tx, gm);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int i = 4 * ty + a;
+                const float4 s4 = ld4(sS + at<64>(i, tx));
+                const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+                float m[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = 4 * tx + c;
+                    const float l = i >= j ? expf((float)(s_cs[i] - s_cs[j])) : 0.f;
+                    m[c] = sv[c] * l;
+                    const float wv = gm[a][c] * m[c];
+                    dS[a][c] = fmaf(gm[a][c] * l, s_dt[j], dS[a][c]);
+                    if (i == j) {
+                        s_dia[j] = wv;
+                        s_dia[kQ + j] = gm[a][c];
+                    } else {
+                        row[a] = fmaf(wv, s_dt[j], row[a]);
+                        colp[c] += wv;
+                    }
+                }
+                *reinterpret_cast<float4*>(sM + at<64>(i, tx)) = make_float4(m[0], m[1], m[2], m[3]);
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) row[a] += __shfl_xor_sync(0xffffffffu, row[a], o);
+                if (tx == 0) s_row[4 * ty + a] = row[a];
+                colp[a] += __shfl_xor_sync(0xffffffffu, colp[a], 16);
+                if (lane < 16) s_col[warp * kQ + 4 * tx + a] = colp[a];
+            }
+        }
+        __syncthreads();
+        // ---- dx and F (rows j = 4 ty + a, columns p = 4 tx + b)
+        {
+            float v[4][4] = {}, uu[4][4] = {};
+            mm_nt<N>(sB, sG, ty, tx, v);
+            mm_tn<kP>(sM, sY, ty, tx, uu);
+            const float Dh = p.a.D[h];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int j = 4 * ty + a;
+                const float4 x4 = ld4(sX + at<64>(j, tx)), y4 = ld4(sY + at<64>(j, tx));
+                const float wj = s_w[j], dtj = s_dt[j];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[a][c] *= wj;
+                float f = x4.x * v[a][0] + x4.y * v[a][1] + x4.z * v[a][2] + x4.w * v[a][3];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+                if (tx == 0) s_F[j] = f;
+                const float4 o4 = make_float4(fmaf(dtj, uu[a][0] + v[a][0], Dh * y4.x),
+                                              fmaf(dtj, uu[a][1] + v[a][1], Dh * y4.y),
+                                              fmaf(dtj, uu[a][2] + v[a][2], Dh * y4.z),
+                                              fmaf(dtj, uu[a][3] + v[a][3], Dh * y4.w));
+                if (j < valid) st4(static_cast<TIO*>(p.a.dx) + ((tok + j) * H + h) * kP + 4 * tx, o4);
+            }
+        }
+        // ---- E
+        {
+            float v[4][4] = {};
+            mm_nt<N>(sC, sH, ty, tx, v);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int i = 4 * ty + a;
+                const float4 y4 = ld4(sY + at<64>(i, tx));
+                float f = y4.x * v[a][0] + y4.y * v[a][1] + y4.z * v[a][2] + y4.w * v[a][3];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+                if (tx == 0) s_E[i] = f * s_e[i];
+            }
+        }
+        // ---- the states' parts of dC and dB
+        {
+            float sc[4], sb[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) sc[a] = s_e[4 * ty + a], sb[a] = s_w[4 * ty + a] * s_dt[4 * ty + a];
+            mm_nn<N>(sY, sH, ty, tx, sc, dC);
+            mm_nn<N>(sX, sG, ty, tx, sb, dB);
+        }
+        __syncthreads();
+        // ---- ddt, two tokens a lane of warp 0
+        if (warp == 0) {
+            float zz = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) zz += s_z[k];
+            zz *= s_e[kQ - 1];
+            float col[2], rc[2], f[2], dtv[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = 2 * lane + k;
+                col[k] = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) col[k] += s_col[q * kQ + t];
+                dtv[k] = s_dt[t];
+                f[k] = s_F[t] * dtv[k];
+                rc[k] = s_E[t] + s_row[t] - col[k] * dtv[k];
+            }
+            float suf = rc[0] + rc[1], pre = f[0] + f[1];  // suffix sum of rc, prefix sum of f over lanes
+            const float fs = pre;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float a = __shfl_down_sync(0xffffffffu, suf, o), c = __shfl_up_sync(0xffffffffu, pre, o);
+                if (lane + o < 32) suf += a;
+                if (lane >= o) pre += c;
+            }
+            pre -= fs;
+            float sA = 0.f, sD = 0.f, sb = 0.f;
+            const float Ah = p.a.A[h];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = 2 * lane + k;
+                const float da = zz + (k ? suf - rc[0] : suf) + (k ? pre + f[0] : pre);
+                float ddt = fmaf(Ah, da, s_dia[t] + col[k] + s_F[t]);
+                if (t < valid) {
+                    const size_t o = (tok + t) * H + h;
+                    if (p.a.dtm.raw) ddt *= dt_slope(p.a.dt[o] + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm);
+                    p.a.ddt[o] = ddt;
+                    sA = fmaf(dtv[k], da, sA);
+                    sD += s_dia[kQ + t];
+                    sb += ddt;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sA += __shfl_xor_sync(0xffffffffu, sA, o);
+                sD += __shfl_xor_sync(0xffffffffu, sD, o);
+                sb += __shfl_xor_sync(0xffffffffu, sb, o);
+            }
+            if (lane == 0) {
+                p.pA[u] = sA;
+                p.pD[u] = sD;
+                if (p.pb) p.pb[u] = sb;
+            }
+        }
+    }
+    // ---- the pairs' parts of dC and dB, from the sum of dS over the heads
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+        *reinterpret_cast<float4*>(sM + at<64>(4 * ty + a, tx)) = make_float4(dS[a][0], dS[a][1], dS[a][2], dS[a][3]);
+    __syncthreads();
+    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+    mm_nn<N>(sM, sB, ty, tx, one, dC);
+    mm_tn<N>(sM, sC, ty, tx, dB);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const int r = 4 * ty + a;
+        if (r >= valid) continue;
+#pragma unroll
+        for (int n = 0; n < N / 64; ++n) {
+            const float4 vb = make_float4(dB[a][4 * n], dB[a][4 * n + 1], dB[a][4 * n + 2], dB[a][4 * n + 3]);
+            const float4 vc = make_float4(dC[a][4 * n], dC[a][4 * n + 1], dC[a][4 * n + 2], dC[a][4 * n + 3]);
+            const size_t o = ((tok + r) * G + g) * N + 64 * n + 4 * tx;
+            if (p.splits == 1) {
+                st4(static_cast<TIO*>(p.a.dB) + o, vb);
+                st4(static_cast<TIO*>(p.a.dC) + o, vc);
+            } else {
+                const size_t all = (size_t)p.a.b * T * G * N;
+                st4(p.part + split * all + o, vb);
+                st4(p.part + (p.splits + split) * all + o, vc);
+            }
+        }
+    }
+}
+
+// dB and dC from the blocks' sums, in block order
+template <typename TIO>
+__global__ void __launch_bounds__(kThreads) ssd_bwd_group_sums_kernel(const SimtBwd p) {
+    const size_t all = (size_t)p.a.b * p.a.T * p.a.G * p.a.N;
+    const size_t i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= all) return;
+    const float* src = p.part + (size_t)blockIdx.y * p.splits * all + i;
+    float4 s = ld4(src);
+    for (int k = 1; k < p.splits; ++k) {
+        const float4 v = ld4(src + k * all);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    st4(static_cast<TIO*>(blockIdx.y ? p.a.dC : p.a.dB) + i, s);
+}
+
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads)
+ssd_bwd_head_sums_kernel(const float* pA, const float* pD, const float* pb, int n, int H, float* dA, float* dD, float* db) {
+    __shared__ double s[kSumThreads / 32];
+    const int h = blockIdx.x, which = blockIdx.y;
+    const float* src = which == 0 ? pA : which == 1 ? pD : pb;
+    double a = 0.0;
+    for (int i = threadIdx.x; i < n; i += kSumThreads) a += src[(size_t)i * H + h];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kSumThreads / 32; ++i) a += s[i];
+        (which == 0 ? dA : which == 1 ? dD : db)[h] = (float)a;
+    }
+}
+
+int bwd_sm_count() {
+    static const int n = [] {
+        int v = 0;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess || v < 1) v = 148;
+        return v;
+    }();
+    return n;
+}
+
+// Carves the workspace; returns its size.  ws = nullptr: the size only.
+size_t simt_layout(const BwdArgs& a, char* ws, SimtBwd* p) {
+    p->a = a;
+    p->nc = (a.T + kQ - 1) / kQ;
+    const size_t bc = (size_t)a.b * p->nc, u = bc * a.H;
+    const int hg = a.H / a.G;
+    // one block holds an SM: split a group's heads until there are two waves of blocks
+    const size_t want = 2 * (size_t)bwd_sm_count();
+    p->splits = (int)std::min<size_t>(hg, std::max<size_t>(1, (want + bc * a.G - 1) / (bc * a.G)));
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char* r = ws ? ws + o : nullptr;
+        o += round_up(bytes, 256);
+        return r;
+    };
+    p->dtv = reinterpret_cast<float*>(take(u * kQ * 4));
+    p->cs = reinterpret_cast<double*>(take(u * kQ * 8));
+    p->e = reinterpret_cast<float*>(take(u * kQ * 4));
+    p->w = reinterpret_cast<float*>(take(u * kQ * 4));
+    p->hs = reinterpret_cast<float*>(take(u * kP * a.N * 4));
+    p->gs = reinterpret_cast<float*>(take(u * kP * a.N * 4));
+    p->pA = reinterpret_cast<float*>(take(u * 4));
+    p->pD = reinterpret_cast<float*>(take(u * 4));
+    p->pb = reinterpret_cast<float*>(take(u * 4));
+    p->part = p->splits > 1 ? reinterpret_cast<float*>(take(2 * p->splits * (size_t)a.b * a.T * a.G * a.N * 4)) : nullptr;
+    return o;
+}
+
+template <typename TIO, int N>
+int run_simt(const SimtBwd& p, cudaStream_t s) {
+    const size_t u = (size_t)p.a.b * p.nc * p.a.H;
+    {
+        LaunchScope ls("ssd_bwd_terms", s);
+        ssd_bwd_terms_kernel<<<dim3(p.a.b * p.nc, (p.a.H + 7) / 8), kThreads, 0, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        const int smem = (kQ * kP + kQ * N) * 4;
+        if (const int st = smem_limit_once((const void*)ssd_bwd_chunk_states_kernel<TIO, N>, smem)) return st;
+        LaunchScope ls("ssd_bwd_chunk_states", s);
+        ssd_bwd_chunk_states_kernel<TIO, N><<<dim3((unsigned)u, 2), kThreads, smem, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        LaunchScope ls("ssd_bwd_state_scan", s);
+        ssd_bwd_state_scan_kernel<<<dim3(p.a.b * p.a.H * (kP * N / (4 * kThreads)), 2), kThreads, 0, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        const int smem = MainSmem<N>::kFloats * 4;
+        if (const int st = smem_limit_once((const void*)ssd_bwd_chunk_kernel<TIO, N>, smem)) return st;
+        LaunchScope ls("ssd_bwd_chunk", s);
+        ssd_bwd_chunk_kernel<TIO, N><<<(unsigned)((size_t)p.a.b * p.nc * p.a.G * p.splits), kThreads, smem, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    if (p.splits > 1) {
+        const size_t all = (size_t)p.a.b * p.a.T * p.a.G * N;
+        LaunchScope ls("ssd_bwd_group_sums", s);
+        ssd_bwd_group_sums_kernel<TIO><<<dim3((unsigned)((all / 4 + kThreads - 1) / kThreads), 2), kThreads, 0, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    return launch_bwd_head_sums(p.pA, p.pD, p.pb, p.a.b * p.nc, p.a.H, p.a.dA, p.a.dD, p.a.dbias, s);
+}
+
+}  // namespace
+
+int launch_bwd_head_sums(const float* pA, const float* pD, const float* pb, int n, int H, float* dA, float* dD,
+                         float* db, cudaStream_t s) {
+    LaunchScope ls("ssd_bwd_head_sums", s);
+    ssd_bwd_head_sums_kernel<<<dim3(H, db ? 3 : 2), kSumThreads, 0, s>>>(pA, pD, pb, n, H, dA, dD, db);
+    SSD_CUDA_TRY(cudaGetLastError());
+    return SSD_OK;
+}
+
+size_t backward_simt_workspace_bytes(const BwdArgs& a) {
+    SimtBwd p;
+    return simt_layout(a, nullptr, &p);
+}
+
+// Whether the launches' grids hold the call: (chunk, head) pairs and state entries in one
+// dimension of a grid.
+bool backward_simt_fits(const BwdArgs& a) {
+    const unsigned long long u = (unsigned long long)a.b * ((a.T + kQ - 1) / kQ) * a.H;
+    return u < (1ull << 31) && (unsigned long long)a.b * a.H * 8 < (1ull << 31) &&
+           (unsigned long long)a.b * a.T * a.G * a.N / 4 / kThreads < (1ull << 31);
+}
+
+int launch_backward_simt(const BwdArgs& a, void* ws, cudaStream_t s) {
+    SimtBwd p;
+    simt_layout(a, static_cast<char*>(ws), &p);
+    if (!a.dbias) p.pb = nullptr;
+    if (a.io == SSD_BF16)
+        return a.N == 128 ? run_simt<__nv_bfloat16, 128>(p, s) : run_simt<__nv_bfloat16, 64>(p, s);
+    return a.N == 128 ? run_simt<float, 128>(p, s) : run_simt<float, 64>(p, s);
+}
+
+}  // namespace ssd

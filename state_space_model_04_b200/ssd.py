@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -93,6 +94,12 @@ def lib() -> ctypes.CDLL:
         L.ssd_decode_step_noalloc.argtypes = [_i] * 9 + [_vp] * 10
         L.ssd_decode_step_noalloc.restype = _i
         f = ctypes.c_float
+        L.ssd_prefill_backward_workspace_size.argtypes = [_i] * 7
+        L.ssd_prefill_backward_workspace_size.restype = _sz
+        L.ssd_prefill_backward.argtypes = [_i] * 7 + [_vp] * 17 + [_sz, _vp]
+        L.ssd_prefill_backward.restype = _i
+        L.ssd_prefill_backward_dt_raw.argtypes = [_i] * 7 + [_vp] * 4 + [f] * 2 + [_vp] * 15 + [_sz, _vp]
+        L.ssd_prefill_backward_dt_raw.restype = _i
         mat = [_vp, _ll]  # pointer, row stride
         L.ssd_norm_backward_workspace_size.argtypes = [_ll, _i, _i]
         L.ssd_norm_backward_workspace_size.restype = _sz
@@ -243,6 +250,89 @@ def prefill(x, dt, A, B, C, D, chunk=256, h0=None, y=None, h_final=None, workspa
     if check and workspace is not None:
         prefill_check(workspace, stream)
     return y, h_final
+
+
+class PrefillGrads(NamedTuple):
+    """What prefill_backward returns; dh0 and ddt_bias are None where they were not asked for."""
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: torch.Tensor
+    dh0: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+
+
+def prefill_backward_workspace_size(b, T, H, P, N, G, io_dtype) -> int:
+    return int(lib().ssd_prefill_backward_workspace_size(b, T, H, P, N, G, io_dtype))
+
+
+def prefill_backward(dy, x, dt, A, B, C, D, h0=None, dh_final=None, grads=None, want_dh0=True, workspace=None,
+                     stream=None, check=False, dt_raw=False, dt_bias=None, dt_min=0.0, dt_max=float("inf")):
+    """Gradients of prefill(x, dt, A, B, C, D, h0=h0, ...) from dy [b,T,H,P], the gradient of y, and
+    dh_final [b,H,P,N] f32, that of h_final (None: zero).  Returns PrefillGrads: dx, dB, dC in x's
+    type, ddt [b,T,H], dA, dD [H] and dh0 [b,H,P,N] (None with want_dh0=False) in f32.  With
+    dt_raw=True, ddt is the gradient of the raw step and ddt_bias [H] that of the bias (None without
+    one).  grads: a PrefillGrads whose tensors take the results instead of new ones.
+    check=True synchronises and raises if a device-side wait recorded an error."""
+    _need(x, "x")
+    io = _io(x)
+    b, T, H, P = x.shape
+    _need(B, "B", x.dtype)
+    G, N = B.shape[2], B.shape[3]
+    _need(dy, "dy", x.dtype, x.shape)
+    _need(dt, "dt", torch.float32, (b, T, H))
+    _need(A, "A", torch.float32, (H,))
+    _need(D, "D", torch.float32, (H,))
+    _need(B, "B", x.dtype, (b, T, G, N))
+    _need(C, "C", x.dtype, (b, T, G, N))
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, (b, H, P, N))
+    if dh_final is not None:
+        _need(dh_final, "dh_final", torch.float32, (b, H, P, N))
+    if dt_bias is not None:
+        if not dt_raw:
+            raise ValueError("dt_bias applies to the raw step only (pass dt_raw=True)")
+        _need(dt_bias, "dt_bias", torch.float32, (H,))
+    f32 = dict(dtype=torch.float32, device=x.device)
+    if grads is None:
+        grads = PrefillGrads(torch.empty_like(x), torch.empty((b, T, H), **f32), torch.empty(H, **f32),
+                             torch.empty_like(B), torch.empty_like(C), torch.empty(H, **f32),
+                             torch.empty((b, H, P, N), **f32) if want_dh0 else None,
+                             None if dt_bias is None else torch.empty(H, **f32))
+    _need(grads.dx, "dx", x.dtype, x.shape)
+    _need(grads.ddt, "ddt", torch.float32, (b, T, H))
+    _need(grads.dA, "dA", torch.float32, (H,))
+    _need(grads.dB, "dB", x.dtype, B.shape)
+    _need(grads.dC, "dC", x.dtype, C.shape)
+    _need(grads.dD, "dD", torch.float32, (H,))
+    if grads.dh0 is not None:
+        _need(grads.dh0, "dh0", torch.float32, (b, H, P, N))
+    if grads.ddt_bias is not None:
+        if not dt_raw:
+            raise ValueError("ddt_bias belongs to the raw step only (pass dt_raw=True)")
+        _need(grads.ddt_bias, "ddt_bias", torch.float32, (H,))
+    need = prefill_backward_workspace_size(b, T, H, P, N, G, io)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check_device(x.device, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
+                  workspace=workspace, **grads._asdict())
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    shape = (b, T, H, P, N, G, io, _ptr(dy), _ptr(x), _ptr(dt))
+    rest = (_ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h0), _ptr(dh_final), _ptr(grads.dx), _ptr(grads.ddt))
+    sums = (_ptr(grads.dA), _ptr(grads.dB), _ptr(grads.dC), _ptr(grads.dD), _ptr(grads.dh0), _ptr(workspace), ws_bytes,
+            _stream(stream))
+    if dt_raw:
+        st = lib().ssd_prefill_backward_dt_raw(*shape, _ptr(dt_bias), float(dt_min), float(dt_max), *rest,
+                                               _ptr(grads.ddt_bias), *sums)
+        _check(st, "ssd_prefill_backward_dt_raw")
+    else:
+        st = lib().ssd_prefill_backward(*shape, *rest, *sums)
+        _check(st, "ssd_prefill_backward")
+    if check and workspace is not None:
+        prefill_check(workspace, stream)
+    return grads
 
 
 def prefill_check(workspace, stream=None):
