@@ -179,7 +179,7 @@ SSD_API int ssd_prefill_context_scan(int world, int rank, int b, int H, int P, i
                                      const float* log_decay_all, float* h_in, void* stream);
 
 /* Synchronises `stream` and returns the device-side status recorded by the most recent
- * ssd_prefill that used `workspace` (SSD_OK, or SSD_ERR_TIMEOUT if a bounded wait inside
+ * ssd_prefill or ssd_prefill_backward that used `workspace` (SSD_OK, or SSD_ERR_TIMEOUT if a bounded wait inside
  * the tensor-core kernel expired, or SSD_ERR_INTERNAL for a failed device consistency
  * check: a dynamic shared-memory base that is not 1024-byte aligned, or a tensor-memory
  * allocation whose address never reached the CTA), then clears it; ssd_last_error names
@@ -215,7 +215,7 @@ SSD_API int ssd_debug_force_prefill_split(int n_full, int nseg);
 /* Test and measurement hook: with on = 1, every following ssd_prefill / ssd_prefill_dt_raw
  * in this process (and ssd_prefill_workspace_size, ssd_prefill_segments,
  * ssd_prefill_whole_units) takes the fp32-FMA path even for shapes the tensor-core kernel
- * takes.  That path evaluates the chunked dual form with chunks of exactly `chunk` tokens,
+ * takes (and so do ssd_prefill_backward and its workspace query).  That path evaluates the chunked dual form with chunks of exactly `chunk` tokens,
  * so it serves the literal chunk-length sweep ([CF-SSD] "Chunked recurrence": the chunk
  * size trades arithmetic intensity against sequential overhead) at any shape; it is an
  * order of magnitude slower than the tensor-core kernel.  on = 0 restores the default.
@@ -358,8 +358,12 @@ SSD_API int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int k
  * step, ddt_bias [H] (NULL: skip) its sum over sequences and tokens; a step outside the clamp
  * range passes no gradient, one on a limit does.
  * T == 0 or b == 0: dA, dD, ddt_bias are zero and dh0 = dh_final (or zero).
- * Arithmetic: every path sums in fp32 (the decays' prefix sums and the sums over chunks in
- * fp64) and rounds a stored gradient once.
+ * Arithmetic: SSD_BF16 with N == 128 runs on the tensor cores (tcgen05, 128-token chunks, fp32
+ * accumulation), everything else on the fp32 pipes (64-token chunks).  Decay prefix sums and the
+ * sums over chunks are fp64, states fp32.  On the tensor cores the fp32 gradients (ddt, dA, dD,
+ * dh0) come from operands carried as two bf16 halves (16 bits) or exact; dx, dB and dC, stored
+ * in bf16, round the pair terms and the states to bf16 once on the way.
+ * The workspace's first 256 bytes hold a device status word (see ssd_prefill_check).
  * Written buffers and the workspace must overlap nothing.  No atomics: the same call gives
  * bitwise the same gradients.
  * Errors: as for ssd_prefill; SSD_ERR_UNSUPPORTED also where b * T * H exceeds what one launch
@@ -379,6 +383,11 @@ SSD_API int ssd_prefill_backward_dt_raw(int b, int T, int H, int P, int N, int G
                                         const float* h0, const float* dh_final, void* dx, float* ddt_raw,
                                         float* ddt_bias, float* dA, void* dB, void* dC, float* dD, float* dh0,
                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Failure-detection test hook: as ssd_debug_starve_next_prefill, for the next tensor-core
+ * ssd_prefill_backward(_dt_raw) in this process; its gradients are then undefined.
+ * Errors: SSD_ERR_INVALID_ARG if wait_limit_ns is outside [1e6, 1e10]. */
+SSD_API int ssd_debug_starve_next_prefill_backward(unsigned long long wait_limit_ns);
 
 /* ------------------------------------------------------------------------------------
  * Norms around a block  (the block the SSD sits in: a norm of the residual stream ahead of

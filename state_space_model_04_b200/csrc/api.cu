@@ -58,6 +58,10 @@ int decode_noalloc_scratch(void** ptr, size_t* bytes);
 size_t backward_simt_workspace_bytes(const BwdArgs& a);
 bool backward_simt_fits(const BwdArgs& a);
 int launch_backward_simt(const BwdArgs& a, void* ws, cudaStream_t s);
+bool backward_tc_supported(int P, int N, int io);
+size_t backward_tc_workspace_bytes(const BwdArgs& a);
+int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s);
+void backward_tc_starve_next(unsigned long long wait_ns);
 size_t norm_workspace_bytes(long long rows, int D, int groups);
 int launch_residual_norm(long long rows, int D, int io, int res_dtype, const void* x, long long ld_x,
                          const void* res, long long ld_res, float scale, const float* w, float eps, void* out,
@@ -610,7 +614,19 @@ int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int kconv, in
 
 // ---- gradients of the prefill
 
-static size_t backward_ws_bytes(const BwdArgs& a) { return kStatusBytes + backward_simt_workspace_bytes(a); }
+static bool backward_use_tc(const BwdArgs& a) { return backward_tc_supported(64, a.N, a.io) && !g_force_fma.load(); }
+
+static size_t backward_ws_bytes(const BwdArgs& a) {
+    return kStatusBytes + (backward_use_tc(a) ? backward_tc_workspace_bytes(a) : backward_simt_workspace_bytes(a));
+}
+
+int ssd_debug_starve_next_prefill_backward(unsigned long long wait_limit_ns) {
+    g_detail[0] = 0;
+    if (wait_limit_ns < 1000000ull || wait_limit_ns > 10000000000ull)
+        return set_error(SSD_ERR_INVALID_ARG, "wait_limit_ns %llu outside [1e6, 1e10]", wait_limit_ns);
+    backward_tc_starve_next(wait_limit_ns);
+    return SSD_OK;
+}
 
 static BwdArgs backward_shape(int b, int T, int H, int N, int G, int io) {
     BwdArgs a = {};
@@ -674,6 +690,7 @@ static int backward_impl(const BwdArgs& a, int P, void* workspace, size_t worksp
         if (overlaps({workspace, need}, {i.p, i.n})) return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps %s", i.name);
     for (const Buf& o : outs)
         if (overlaps({workspace, need}, {o.p, o.n})) return set_error(SSD_ERR_INVALID_ARG, "workspace overlaps %s", o.name);
+    if (backward_use_tc(a)) return launch_backward_tc(a, workspace, kStatusBytes, s);
     SSD_CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), s));
     return launch_backward_simt(a, static_cast<char*>(workspace) + kStatusBytes, s);
 }

@@ -1,0 +1,1143 @@
+// backward_tc.cu -- gradients of the SSD prefill on the sm_100a tensor cores (tcgen05 + TMEM +
+// TMA), for bf16 inputs with P = 64, N = 128.  The formulas are those at the head of
+// backward_simt.cu, with chunks of 128 tokens (the M of one tcgen05 MMA).
+//
+// Two passes over the tokens, because the state runs forwards and its adjoint backwards:
+//
+//   state pass   a CTA walks one (sequence, head) chunk by chunk, forwards with x, B for the state
+//                h entering each chunk, backwards with dy, C for the adjoint dh of the state
+//                leaving it, the running state in fp32 registers; each is written as two bf16
+//                halves (hi = bf16(h), lo = bf16(h - hi), 16 bits of h together) in the layout
+//                the next pass's MMAs read.
+//   main pass    a CTA takes a run of (chunk, head) items, heads fastest, so that the heads of a
+//                B/C group follow one another in one CTA and what they share stays on chip:
+//                S^T = B C^T is computed once and held in registers, dB and dC accumulate in
+//                TMEM over the heads, and the pair terms dS are summed over the heads in
+//                registers and multiplied with B and C once a group.  A group's heads may lie in
+//                several CTAs; each then stores its sums in fp32 and a third pass adds them in
+//                CTA order.
+//
+// Per item the main pass multiplies (rows j or i, 128 each)
+//   G^T = X dY^T,   V = B dh^T (hi, lo),   Y = C h^T (hi, lo),
+//   dC += (e o dY) h,   dB += (w dt o X) dh,   U = w o V + M^T dY,  M^T = S^T o L^T
+// with G^T, V and Y in fp32 TMEM.  Precision: ddt, dA and dh0 are fp32 gradients, and what they
+// are made of (G, S, the decays, V, Y, the states) carries 16 bits or more: V and Y take both
+// halves of the states, the state pass both halves of the weighted x and dy.  dx, dB and dC are
+// stored in bf16, so M, dS, the weighted rows and the states are rounded to bf16 once where they
+// feed only those.
+//
+// Bound: memory.  Per item 48 KB of x, dy, dx and 64 KB of state halves in the main pass, 32 KB
+// and 64 KB in the state pass.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+#include "backward.cuh"
+#define SSD_TC_INLINE_WAITS
+#include "tc.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kP = 64, kN = 128;
+constexpr uint32_t kRegion = kBlk * 128;        // one [128 rows][64 bf16] swizzled box: 16 KB
+constexpr uint32_t kImage = 2 * kRegion;        // a state: hi, lo, each [128 n][64 p]
+// per-token terms of an item, [kTerms][128] fp32 (a: step sizes times A; cs: its prefix sum in the
+// chunk, csub: in the token's 32-token group)
+constexpr int kTermCs2 = 0;                     // csub log2(e)
+constexpr int kTermU = 1;                       // exp(csub)
+constexpr int kTermE = 2;                       // exp(cs)
+constexpr int kTermW = 3;                       // exp(cs_last - cs)
+constexpr int kTermDt = 4;                      // dt
+constexpr int kTerms = 5;
+constexpr uint32_t kTermBytes = kTerms * kBlk * 4;
+
+struct BwdTc {
+    CUtensorMap tm_x, tm_dy, tm_B, tm_C, tm_dx;
+    BwdArgs a;
+    int nc;                 // chunks a sequence
+    int ctas;               // of the main pass
+    long long items;        // b nc H
+    float* terms;           // [items][kTerms][128]
+    uint8_t* img_h;         // [items][kImage] state entering the chunk
+    uint8_t* img_g;         // [items][kImage] adjoint of the state leaving it
+    float* part;            // [ctas][2][2][128][128] sums of dB, dC of a CTA's first and last group
+    float *pA, *pD, *pb;    // [b nc][H]
+    int* status;
+    unsigned long long wait_ns;
+    int starve;
+};
+
+__device__ __forceinline__ void split_bf16(float v, float& hi, float& lo) {
+    hi = __bfloat162float(__float2bfloat16_rn(v));
+    lo = v - hi;
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// ------------------------------------------------------------------ per-token terms
+// One warp per item, lane l holds tokens 32 q + l; prefix sums in fp64.
+constexpr int kTermThreads = 256;
+__global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __grid_constant__ BwdTc p) {
+    const int lane = threadIdx.x & 31, h = blockIdx.y * (kTermThreads / 32) + (threadIdx.x >> 5);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
+    if (h >= p.a.H) return;
+    const int bc = blockIdx.x, bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+    const double Ah = p.a.A[h];
+    float dt[4];
+    double cs[4], end[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int t = t0 + 32 * q + lane;
+        dt[q] = t < p.a.T ? dt_value(p.a.dt[((size_t)bi * p.a.T + t) * p.a.H + h], p.a.dtm, h) : 0.f;
+        cs[q] = dt[q] * Ah;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const double v = __shfl_up_sync(0xffffffffu, cs[q], o);
+            if (lane >= o) cs[q] += v;
+        }
+    }
+    double run = 0.0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        end[q] = run;  // the prefix ahead of group q
+        run += __shfl_sync(0xffffffffu, cs[q], 31);
+    }
+    float* t = p.terms + ((size_t)bc * p.a.H + h) * kTerms * kBlk + lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const double c = end[q] + cs[q];
+        t[kTermCs2 * kBlk + 32 * q] = (float)(cs[q] * 1.4426950408889634);
+        t[kTermU * kBlk + 32 * q] = expf((float)cs[q]);
+        t[kTermE * kBlk + 32 * q] = expf((float)c);
+        t[kTermW * kBlk + 32 * q] = expf((float)(run - c));
+        t[kTermDt * kBlk + 32 * q] = dt[q];
+    }
+}
+
+// ------------------------------------------------------------------ state pass
+//   warp 0      TMA producer: X (or dY) and the two boxes of B (or C) of a chunk, 2-slot ring
+//   warp 1      TMEM owner and MMA issuer: D[n][p] = B^T (wX)_hi + B^T (wX)_lo
+//   warps 2-9   weight the rows of the chunk ahead into hi and lo tiles, write the state's halves,
+//               then h <- exp(cs_last) h + D
+constexpr int kSWork = 256;
+constexpr int kSThreads = 64 + kSWork;
+constexpr uint32_t kSSlot = 3 * kRegion;            // X, B (n 0..63), B (n 64..127)
+constexpr uint32_t kSXs = 2 * kSSlot;               // [2] hi, lo tiles of the weighted rows
+constexpr uint32_t kSImg = kSXs + 2 * kImage;       // [2] state images
+constexpr uint32_t kSSmall = kSImg + 2 * kImage;
+constexpr uint32_t kSSmem = kSSmall + 256;
+static_assert(kSSmem <= 232448 - 1024, "state pass shared memory");
+enum { SB_FULL = 0, SB_EMPTY = 2, SB_XS = 4, SB_ACC = 6, SB_FREE = 7, SB_DONE = 8, SB_COUNT };
+
+__device__ __forceinline__ void work_bar() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kSWork) : "memory");
+}
+
+__global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __grid_constant__ BwdTc p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = p.a.H, nc = p.nc;
+    const int u = blockIdx.x, dir = blockIdx.y, h = u % H, bi = u / H, g = h / (H / p.a.G);
+    uint8_t* small = smem + kSSmall;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(small + 128);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 144);
+    volatile int* s_stop = reinterpret_cast<volatile int*>(small + 160);
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto chunk = [&](int k) { return dir ? nc - 1 - k : k; };  // the k-th chunk walked
+
+    if (threadIdx.x == 0) {
+        const bool misaligned = (sbase & 1023u) != 0;
+        if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (5 << 8));
+        for (int i = 0; i < SB_COUNT; ++i)
+            mbar_init(bar(i), i == SB_XS || i == SB_XS + 1 || i == SB_FREE ? kSWork / 32 : 1);
+        *s_abort = misaligned ? 1 : 0;
+        s_stop[0] = s_stop[1] = 0;
+        s_wait_ns = p.wait_ns;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const uint32_t tmem = tmem_alloc_cta(s_tmem, 64, warp == 1);
+    if (tmem == kTmemSentinel) {
+        *s_abort = 1;
+        report_status(p.status, SSD_ERR_INTERNAL | (6 << 8));
+    }
+    // the last chunk's product is only needed for the adjoint of the initial state
+    const int products = dir && p.a.dh0 ? nc : nc - 1;
+
+    if (warp == 0) {
+        if (lane == 0 && !*s_abort && !p.starve) {
+            int issued = 0;
+            for (int k = 0; k < products; ++k) {
+                const int s = k & 1;
+                if (k >= 2 && !mbar_wait(bar(SB_EMPTY + s), ((k - 2) >> 1) & 1, s_abort, p.status, 50)) break;
+                const uint32_t f = bar(SB_FULL + s), slot = sbase + s * kSSlot;
+                const int t0 = chunk(k) * kBlk;
+                mbar_expect_tx(f, kSSlot);
+                tma_load_4d(slot, dir ? &p.tm_dy : &p.tm_x, f, 0, h, t0, bi);
+                tma_load_4d(slot + kRegion, dir ? &p.tm_C : &p.tm_B, f, 0, g, t0, bi);
+                tma_load_4d(slot + 2 * kRegion, dir ? &p.tm_C : &p.tm_B, f, 64, g, t0, bi);
+                issued = k + 1;
+            }
+            for (int k = issued - 2; k < issued; ++k)
+                if (k >= 0) mbar_drain(bar(SB_FULL + (k & 1)), (k >> 1) & 1);
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t id = idesc_bf16(128, 64, 1, 1);
+        auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity, s_abort, p.status, where); };
+        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        for (int k = 0; k < products && ok; ++k) {
+            const int s = k & 1;
+            ok = wt(SB_FULL + s, (k >> 1) & 1, 51) && wt(SB_XS + s, (k >> 1) & 1, 52) &&
+                 (k < 1 || wt(SB_FREE, (k - 1) & 1, 53));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dA = sdesc(sbase + s * kSSlot + kRegion, kRegion, 1024);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t dX = sdesc(sbase + kSXs + s * kImage + half * kRegion, kRegion, 1024);
+#pragma unroll 1
+                for (int kk = 0; kk < kBlk / 16; ++kk)
+                    mma_ss_w(tmem, dA + kk * 128, dX + kk * 128, id, half > 0 || kk > 0);
+            }
+            mma_commit_w(bar(SB_EMPTY + s));
+            mma_commit_w(bar(SB_ACC));
+        }
+        mma_commit_w(bar(SB_DONE));
+        mbar_drain(bar(SB_DONE), 0);
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int r = q * 32 + lane;  // token row of a chunk, and state row n
+        const int p0 = half * 32;
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + p0;
+        const float* init = dir ? p.a.dhf : p.a.h0;
+        float st[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) st[i] = init ? init[(size_t)u * kP * kN + (size_t)(p0 + i) * kN + r] : 0.f;
+        auto item = [&](int k) { return ((size_t)bi * nc + chunk(k)) * H + h; };
+        // weight of the thread's row, and the chunk's decay, fetched a chunk ahead of their use
+        auto load_w = [&](int k) {
+            if (k >= products) return 0.f;
+            const float* t = p.terms + item(k) * kTerms * kBlk + r;
+            return dir ? t[kTermE * kBlk] : t[kTermW * kBlk] * t[kTermDt * kBlk];
+        };
+        auto load_gam = [&](int k) { return k < nc ? p.terms[(item(k) * kTerms + kTermE) * kBlk + kBlk - 1] : 0.f; };
+        float w_next = load_w(0), gam = load_gam(0);
+        bool live = __all_sync(0xffffffffu, !*s_abort);
+        auto weigh = [&](int k) {  // rows of chunk k, weighted, into the hi and lo tiles
+            const float w = w_next;
+            w_next = load_w(k + 1);
+            if (!warp_wait(bar(SB_FULL + (k & 1)), (k >> 1) & 1, s_abort, p.status, 54)) return false;
+            const uint8_t* src = smem + (k & 1) * kSSlot;
+            uint8_t* dst = smem + kSXs + (k & 1) * kImage;
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+                const uint32_t o = swz(r, half * 4 + c4);
+                const uint4 v = *reinterpret_cast<const uint4*>(src + o);
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a, b, al, bl;
+                    split_bf16(w * bf_lo(in[i]), a, al);
+                    split_bf16(w * bf_hi(in[i]), b, bl);
+                    hi[i] = pack_bf16(a, b);
+                    lo[i] = pack_bf16(al, bl);
+                }
+                *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(dst + kRegion + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SB_XS + (k & 1)));
+            return true;
+        };
+        if (live && products > 0) live = weigh(0);
+        uint8_t* images = dir ? p.img_g : p.img_h;
+        for (int k = 0; k < nc; ++k) {
+            // the state as two bf16 halves, image buffer k & 1 (its last store has been read);
+            // a warp that gave up tells the others at the barrier, so all leave together
+            if (!live || *s_abort) s_stop[k & 1] = 1;
+            if (threadIdx.x == 64) bulk_wait_read1();
+            work_bar();
+            if (s_stop[k & 1]) break;
+            uint8_t* img = smem + kSImg + (k & 1) * kImage;
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a, b, al, bl;
+                    split_bf16(st[8 * c4 + 2 * i], a, al);
+                    split_bf16(st[8 * c4 + 2 * i + 1], b, bl);
+                    hi[i] = pack_bf16(a, b);
+                    lo[i] = pack_bf16(al, bl);
+                }
+                const uint32_t o = swz(r, half * 4 + c4);
+                *reinterpret_cast<uint4*>(img + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(img + kRegion + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            work_bar();
+            if (threadIdx.x == 64) {
+                bulk_store(images + item(k) * kImage, smem_u32(img), kImage);
+                bulk_commit();
+            }
+            // rows of the next chunk: the tiles' last reader, the product of chunk k - 1, is done
+            if (live && k + 1 < products) live = weigh(k + 1);
+            if (live && k < products) {
+                live = warp_wait(bar(SB_ACC), k & 1, s_abort, p.status, 55);
+                if (live) {
+                    tc_fence_after();
+                    uint32_t raw[32];
+                    SSD_TMEM_LD32_WAIT(acc, raw);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(SB_FREE));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) st[i] = fmaf(gam, st[i], __uint_as_float(raw[i]));
+                    gam = load_gam(k + 1);
+                }
+            }
+        }
+        if (live && !*s_abort && dir && p.a.dh0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) p.a.dh0[(size_t)u * kP * kN + (size_t)(p0 + i) * kN + r] = st[i];
+        }
+        if (threadIdx.x == 64) bulk_wait0();  // the stores are complete before the shared memory goes away
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1 && tmem != kTmemSentinel) {
+        tc_fence_after();
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(64));
+    }
+}
+
+// ------------------------------------------------------------------ main pass
+//   warp 0        producer: X, dY and the terms of an item (2-slot ring), the state halves (one
+//                 slot), B and C of a group
+//   warp 1        TMEM owner and MMA issuer
+//   warp 2        ddt and the sums behind dA, dD; stores the dx tiles
+//   warp 3        <h, dh>
+//   warps 4-11    "pair" group (two warps a TMEM lane quadrant, half of the columns each): S^T
+//                 and the sum of dS^T in registers; per item M^T and W from G^T; per group dB, dC
+//   warps 12-15   "row" group (one token a thread): the weighted rows, F and E from V and Y, dx
+// Registers are moved to where they are needed (setmaxnreg): 128 x (kRegsWarps + kRegsRow +
+// 2 kRegsPair) is what the block was launched with.
+constexpr int kThreads = 512;
+constexpr int kRegsWarps = 48, kRegsRow = 80, kRegsPair = 192, kRegsLaunch = 128;
+static_assert(kRegsWarps + kRegsRow + 2 * kRegsPair <= 4 * kRegsLaunch, "register split");
+
+constexpr uint32_t kMB = 0;                          // B: n 0..63, 64..127
+constexpr uint32_t kMC = kMB + 2 * kRegion;          // C
+constexpr uint32_t kMX = kMC + 2 * kRegion;          // [2] X, then the dx tile
+constexpr uint32_t kMY = kMX + 2 * kRegion;          // [2] dY
+constexpr uint32_t kMH = kMY + 2 * kRegion;          // h image; at a group's end the dS^T tile
+constexpr uint32_t kMG = kMH + kImage;               // dh image
+constexpr uint32_t kMW = kMG + kImage;               // e o dY, then w dt o X
+constexpr uint32_t kMTerms = kMW + kRegion;          // [2] terms
+constexpr uint32_t kMSums = kMTerms + 2 * kTermBytes;
+// per item, fp32 [128] each: row sums of W by quadrant of j (4), column sums by half (2),
+// Gm_jj S_jj, Gm_jj, E, F / dt; then <h, dh>
+constexpr int kSumRow = 0, kSumCol = 4, kSumDia = 6, kSumGd = 7, kSumE = 8, kSumF = 9, kSums = 10;
+constexpr uint32_t kSumBytes = kSums * kBlk * 4;
+constexpr uint32_t kMSmall = kMSums + 2 * kSumBytes;
+constexpr uint32_t kMSmem = kMSmall + 512;
+static_assert(kMSmem <= 232448 - 1024, "main pass shared memory");
+
+constexpr uint32_t kColB = 0, kColC = 128, kColG = 256, kColV = 384, kColY = 448;
+
+enum {
+    MB_FULLXY = 0,    // [2] X, dY, terms landed
+    MB_EMPTYXY = 2,   // [2] row group done with dY (4 warps), dx tile read out (1)
+    MB_EMPTYT = 4,    // [2] terms read: pair (8), row (4) warps, ddt warp (1)
+    MB_FULLST = 6,    // state halves landed
+    MB_EMPTYST = 7,   // every product that reads them done (1), <h, dh> done (1)
+    MB_FULLBC = 8,    // B, C landed
+    MB_SFULL = 9,     // S^T accumulated
+    MB_SREAD = 10,    // pair group read it (8)
+    MB_GFULL = 11,    // G^T accumulated
+    MB_MREADY = 12,   // pair group wrote M^T (8)
+    MB_UDONE = 13,    // U accumulated: M^T is read too
+    MB_VDONE = 14,    // V accumulated
+    MB_VSCALED = 15,  // row group replaced V by w o V (4)
+    MB_UFREE = 16,    // row group read U (4)
+    MB_YDONE = 17,    // Y accumulated
+    MB_YFREE = 18,    // row group read Y (4)
+    MB_EYREADY = 19,  // row group wrote e o dY (4)
+    MB_DCDONE = 20,   // dC's product done: the tile is free
+    MB_WXREADY = 21,  // row group wrote w dt o X (4)
+    MB_DBDONE = 22,   // dB's product done: the tile is free
+    MB_SUMFULL = 23,  // [2] sums written: pair (8), row (4), <h, dh> (1)
+    MB_SUMEMPTY = 25, // [2] sums read (1)
+    MB_DXSTAGED = 27, // [2] dx tile written (4)
+    MB_DSREADY = 29,  // pair group wrote the dS^T tile (8)
+    MB_ACCDONE = 30,  // dB, dC complete
+    MB_UNITFREE = 31, // pair group read them (8): B, C, the accumulators and the tile are free
+    MB_DONE = 32,
+    MB_COUNT
+};
+static_assert(MB_COUNT * 8 <= 320, "barriers");
+__device__ constexpr uint32_t main_bar_count(int i) {
+    switch (i) {
+        case MB_EMPTYXY: case MB_EMPTYXY + 1: return 5;
+        case MB_EMPTYT: case MB_EMPTYT + 1: case MB_SUMFULL: case MB_SUMFULL + 1: return 13;
+        case MB_EMPTYST: return 2;
+        case MB_SREAD: case MB_MREADY: case MB_DSREADY: case MB_UNITFREE: return 8;
+        case MB_VSCALED: case MB_UFREE: case MB_YFREE: case MB_EYREADY: case MB_WXREADY:
+        case MB_DXSTAGED: case MB_DXSTAGED + 1: return 4;
+        default: return 1;
+    }
+}
+
+// v[i] of every lane summed over the lanes; lane l gets the sum of v[l].  Halving exchange: 31
+// shuffles for 32 sums.
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+template <int kRegs> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+__global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __grid_constant__ BwdTc p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = p.a.H, G = p.a.G, T = p.a.T, hg = H / G;
+    const long long lo = p.items * blockIdx.x / p.ctas, hi = p.items * (blockIdx.x + 1) / p.ctas;
+    uint8_t* small = smem + kMSmall;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(small + 320);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 336);
+    float* s_z = reinterpret_cast<float*>(small + 352);  // [2]
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto wt = [&](int b, uint32_t parity, int where) {
+        return warp_wait(bar(b), parity & 1, s_abort, p.status, where);
+    };
+
+    if (threadIdx.x == 0) {
+        const bool misaligned = (sbase & 1023u) != 0;
+        if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (7 << 8));
+        for (int i = 0; i < MB_COUNT; ++i) mbar_init(bar(i), main_bar_count(i));
+        *s_abort = misaligned ? 1 : 0;
+        s_wait_ns = p.wait_ns;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const uint32_t tmem = tmem_alloc_cta(s_tmem, 512, warp == 1);
+    if (tmem == kTmemSentinel) {
+        *s_abort = 1;
+        report_status(p.status, SSD_ERR_INTERNAL | (8 << 8));
+    }
+    // Every role walks the same items: k counts them (per-item barriers complete once each), n the
+    // groups begun.
+    auto first = [&](long long it) { return it == lo || it % hg == 0; };
+    auto last = [&](long long it) { return it + 1 == hi || (it + 1) % hg == 0; };
+
+    if (warp < 4) {
+        reg_dec<kRegsWarps>();
+        if (warp == 0) {
+            // ============================================================ producer
+            if (lane == 0 && !*s_abort && !p.starve) {
+                int nxy = 0, nst = 0, nbc = 0, n = 0;
+                auto w1 = [&](int b, uint32_t parity, int where) {
+                    return mbar_wait(bar(b), parity & 1, s_abort, p.status, where);
+                };
+                for (long long it = lo; it < hi; ++it) {
+                    const int k = (int)(it - lo), s = k & 1;
+                    const int h = (int)(it % H), bc = (int)(it / H), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+                    if (k >= 2 && !(w1(MB_EMPTYXY + s, (k - 2) >> 1, 60) && w1(MB_EMPTYT + s, (k - 2) >> 1, 61))) break;
+                    const uint32_t f = bar(MB_FULLXY + s);
+                    mbar_expect_tx(f, 2 * kRegion + kTermBytes);
+                    tma_load_4d(sbase + kMX + s * kRegion, &p.tm_x, f, 0, h, t0, bi);
+                    tma_load_4d(sbase + kMY + s * kRegion, &p.tm_dy, f, 0, h, t0, bi);
+                    bulk_load(sbase + kMTerms + s * kTermBytes, p.terms + it * kTerms * kBlk, kTermBytes, f);
+                    nxy = k + 1;
+                    if (first(it)) {
+                        if (n > 0 && !w1(MB_UNITFREE, n - 1, 62)) break;
+                        const uint32_t fb = bar(MB_FULLBC);
+                        const int g = h / hg;
+                        mbar_expect_tx(fb, 4 * kRegion);
+                        tma_load_4d(sbase + kMB, &p.tm_B, fb, 0, g, t0, bi);
+                        tma_load_4d(sbase + kMB + kRegion, &p.tm_B, fb, 64, g, t0, bi);
+                        tma_load_4d(sbase + kMC, &p.tm_C, fb, 0, g, t0, bi);
+                        tma_load_4d(sbase + kMC + kRegion, &p.tm_C, fb, 64, g, t0, bi);
+                        nbc = ++n;
+                    }
+                    if (k >= 1 && !w1(MB_EMPTYST, k - 1, 63)) break;
+                    const uint32_t fs = bar(MB_FULLST);
+                    mbar_expect_tx(fs, 2 * kImage);
+                    bulk_load(sbase + kMG, p.img_g + it * kImage, kImage, fs);
+                    bulk_load(sbase + kMH, p.img_h + it * kImage, kImage, fs);
+                    nst = k + 1;
+                }
+                // loads nobody may have waited for land before the CTA exits
+                for (int k = nxy - 2; k < nxy; ++k)
+                    if (k >= 0) mbar_drain(bar(MB_FULLXY + (k & 1)), (k >> 1) & 1);
+                if (nst > 0) mbar_drain(bar(MB_FULLST), (nst - 1) & 1);
+                if (nbc > 0) mbar_drain(bar(MB_FULLBC), (nbc - 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ============================================================ MMA issuer
+            constexpr uint32_t id_nn = idesc_bf16(128, 128, 0, 0);   // both K-major
+            constexpr uint32_t id_st = idesc_bf16(128, 64, 0, 1);    // state or dY [K rows][64]: MN-major
+            constexpr uint32_t id_db = idesc_bf16(128, 128, 0, 1);
+            constexpr uint32_t id_dc = idesc_bf16(128, 128, 1, 1);
+            auto koff = [](int kk) { return (uint32_t)((kk >> 2) * (kRegion >> 4) + (kk & 3) * 2); };
+            bool ok = __all_sync(0xffffffffu, !*s_abort);
+            int n = 0;
+            for (long long it = lo; it < hi && ok; ++it) {
+                const int k = (int)(it - lo), s = k & 1;
+                const bool fresh = first(it);
+                const uint32_t x = sbase + kMX + s * kRegion, y = sbase + kMY + s * kRegion;
+                // G^T's columns: U of the item before has read M^T there
+                ok = k < 1 || wt(MB_UDONE, k - 1, 70);
+                if (!ok) break;
+                if (fresh) {
+                    ok = (n < 1 || wt(MB_UNITFREE, n - 1, 71)) && wt(MB_FULLBC, n, 72);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dB = sdesc(sbase + kMB, 16, 1024), dC = sdesc(sbase + kMC, 16, 1024);
+#pragma unroll 1
+                    for (int kk = 0; kk < kN / 16; ++kk)
+                        mma_ss_w(tmem + kColG, dB + koff(kk), dC + koff(kk), id_nn, kk > 0);
+                    mma_commit_w(bar(MB_SFULL));
+                    ok = wt(MB_SREAD, n, 73);
+                    if (!ok) break;
+                    ++n;
+                }
+                ok = wt(MB_FULLXY + s, k >> 1, 74);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint64_t dX = sdesc(x, 16, 1024), dY = sdesc(y, 16, 1024);
+#pragma unroll 1
+                    for (int kk = 0; kk < kP / 16; ++kk) mma_ss_w(tmem + kColG, dX + kk * 2, dY + kk * 2, id_nn, kk > 0);
+                    mma_commit_w(bar(MB_GFULL));
+                }
+                // V = B dh^T, Y = C h^T, hi then lo
+                ok = wt(MB_FULLST, k, 75) && (k < 1 || wt(MB_UFREE, k - 1, 76));
+                if (!ok) break;
+                tc_fence_after();
+                auto state_product = [&](uint32_t col, uint32_t left, uint32_t image) {
+                    const uint64_t dL = sdesc(left, 16, 1024);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t dI = sdesc(image + half * kRegion, kRegion, 1024);
+#pragma unroll 1
+                        for (int kk = 0; kk < kN / 16; ++kk)
+                            mma_ss_w(tmem + col, dL + koff(kk), dI + kk * 128, id_st, half > 0 || kk > 0);
+                    }
+                };
+                state_product(kColV, sbase + kMB, sbase + kMG);
+                mma_commit_w(bar(MB_VDONE));
+                ok = k < 1 || wt(MB_YFREE, k - 1, 77);
+                if (!ok) break;
+                tc_fence_after();
+                state_product(kColY, sbase + kMC, sbase + kMH);
+                mma_commit_w(bar(MB_YDONE));
+                // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
+                auto row_product = [&](uint32_t col, uint32_t image) {
+                    const uint64_t dW = sdesc(sbase + kMW, 16, 1024), dI = sdesc(image, 16, 1024);
+#pragma unroll 1
+                    for (int kk = 0; kk < kP / 16; ++kk)
+                        mma_ss_w(tmem + col, dW + kk * 2, dI + kk * 2, id_nn, !fresh || kk > 0);
+                };
+                ok = wt(MB_EYREADY, k, 78);
+                if (!ok) break;
+                tc_fence_after();
+                row_product(kColC, sbase + kMH);
+                mma_commit_w(bar(MB_DCDONE));
+                ok = wt(MB_WXREADY, k, 79);
+                if (!ok) break;
+                tc_fence_after();
+                row_product(kColB, sbase + kMG);
+                mma_commit_w(bar(MB_DBDONE));
+                mma_commit_w(bar(MB_EMPTYST));
+                // U = w o V + M^T dY
+                ok = wt(MB_VSCALED, k, 80) && wt(MB_MREADY, k, 81);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint64_t dY = sdesc(y, kRegion, 1024);
+#pragma unroll 1
+                    for (int kk = 0; kk < kBlk / 16; ++kk)
+                        mma_ts_w(tmem + kColV, tmem + kColG + (kk >> 1) * 32 + (kk & 1) * 8, dY + kk * 128, id_st, 1);
+                    mma_commit_w(bar(MB_UDONE));
+                }
+                if (last(it)) {
+                    ok = wt(MB_DSREADY, n - 1, 82);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dSk = sdesc(sbase + kMH, 16, 1024), dSm = sdesc(sbase + kMH, kRegion, 1024);
+                    const uint64_t dB = sdesc(sbase + kMB, kRegion, 1024), dC = sdesc(sbase + kMC, kRegion, 1024);
+#pragma unroll 1
+                    for (int kk = 0; kk < kBlk / 16; ++kk)
+                        mma_ss_w(tmem + kColB, dSk + koff(kk), dC + kk * 128, id_db, 1);
+#pragma unroll 1
+                    for (int kk = 0; kk < kBlk / 16; ++kk)
+                        mma_ss_w(tmem + kColC, dSm + kk * 128, dB + kk * 128, id_dc, 1);
+                    mma_commit_w(bar(MB_ACCDONE));
+                }
+            }
+            mma_commit_w(bar(MB_DONE));
+            mbar_drain(bar(MB_DONE), 0);
+        } else if (warp == 2) {
+            // ============================================================ ddt, sums, dx stores
+            bool ok = __all_sync(0xffffffffu, !*s_abort);
+            for (long long it = lo; it < hi && ok; ++it) {
+                const int k = (int)(it - lo), s = k & 1;
+                const int h = (int)(it % H), bc = (int)(it / H), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+                ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
+                if (!ok) break;
+                const float* sums = reinterpret_cast<const float*>(smem + kMSums + s * kSumBytes);
+                const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
+                // tokens 4 lane .. 4 lane + 3
+                const int q = lane >> 3;
+                float rc[4], f[4], dir[4];
+                float zz = s_z[s] * terms[kTermE * kBlk + kBlk - 1];
+                float suf = 0.f, pre = 0.f, sD = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * lane + i;
+                    const float dt = terms[kTermDt * kBlk + t];
+                    const float col = sums[kSumCol * kBlk + t] + sums[(kSumCol + 1) * kBlk + t];
+                    const float fj = sums[kSumF * kBlk + t];
+                    float row = sums[kSumE * kBlk + t];
+                    for (int qq = 0; qq <= q; ++qq) row += sums[(kSumRow + qq) * kBlk + t];
+                    rc[i] = fmaf(-col, dt, row);
+                    f[i] = fj * dt;
+                    dir[i] = sums[kSumDia * kBlk + t] + col + fj;
+                    sD += sums[kSumGd * kBlk + t];
+                    suf += rc[i];
+                    pre += f[i];
+                }
+                const float own = suf, fown = pre;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float a = __shfl_down_sync(0xffffffffu, suf, o), c = __shfl_up_sync(0xffffffffu, pre, o);
+                    if (lane + o < 32) suf += a;
+                    if (lane >= o) pre += c;
+                }
+                (void)own;
+                pre -= fown;
+                const float Ah = p.a.A[h];
+                float sA = 0.f, sb = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 4 * lane + i;
+                    const float da = zz + suf + pre;
+                    suf -= rc[i];
+                    pre += f[i];
+                    float ddt = fmaf(Ah, da, dir[i]);
+                    if (t0 + t < T) {
+                        const size_t o = ((size_t)bi * T + t0 + t) * H + h;
+                        if (p.a.dtm.raw) ddt *= dt_slope(p.a.dt[o] + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm);
+                        p.a.ddt[o] = ddt;
+                        sA = fmaf(terms[kTermDt * kBlk + t], da, sA);
+                        sb += ddt;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    sA += __shfl_xor_sync(0xffffffffu, sA, o);
+                    sD += __shfl_xor_sync(0xffffffffu, sD, o);
+                    sb += __shfl_xor_sync(0xffffffffu, sb, o);
+                }
+                if (lane == 0) {
+                    p.pA[it] = sA;
+                    p.pD[it] = sD;
+                    if (p.pb) p.pb[it] = sb;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(MB_SUMEMPTY + s));
+                    mbar_arrive(bar(MB_EMPTYT + s));
+                }
+                ok = wt(MB_DXSTAGED + s, k >> 1, 92);
+                if (!ok) break;
+                if (lane == 0) {
+                    tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, h, t0, bi);
+                    bulk_commit();
+                    bulk_wait_read0();
+                    mbar_arrive(bar(MB_EMPTYXY + s));
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait0();
+        } else {
+            // ============================================================ <h, dh>
+            bool ok = __all_sync(0xffffffffu, !*s_abort);
+            for (long long it = lo; it < hi && ok; ++it) {
+                const int k = (int)(it - lo), s = k & 1;
+                ok = wt(MB_FULLST, k, 95);
+                if (!ok) break;
+                const uint4 *h4 = reinterpret_cast<const uint4*>(smem + kMH), *g4 = reinterpret_cast<const uint4*>(smem + kMG);
+                float z0 = 0.f, z1 = 0.f;
+#pragma unroll 2
+                for (int i = lane; i < (int)(kRegion / 16); i += 32) {
+                    const uint4 a = h4[i], al = h4[i + kRegion / 16], b = g4[i], bl = g4[i + kRegion / 16];
+                    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, av2[4] = {al.x, al.y, al.z, al.w};
+                    const uint32_t bv[4] = {b.x, b.y, b.z, b.w}, bv2[4] = {bl.x, bl.y, bl.z, bl.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        z0 = fmaf(bf_lo(av[j]) + bf_lo(av2[j]), bf_lo(bv[j]) + bf_lo(bv2[j]), z0);
+                        z1 = fmaf(bf_hi(av[j]) + bf_hi(av2[j]), bf_hi(bv[j]) + bf_hi(bv2[j]), z1);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(MB_EMPTYST));
+                z0 += z1;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) z0 += __shfl_xor_sync(0xffffffffu, z0, o);
+                ok = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 96);
+                if (!ok) break;
+                if (lane == 0) {
+                    s_z[s] = z0;
+                    mbar_arrive(bar(MB_SUMFULL + s));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < 12) {
+        // ================================================================ pair group
+        reg_inc<kRegsPair>();
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int r = q * 32 + lane;  // token j
+        const uint32_t buf = tmem + ((uint32_t)(q * 32) << 16) + kColG;
+        // columns i: 32-token groups c = half and half + 2; the pair needs c >= q
+        float S[2][32], dS[2][32];
+        bool live = __all_sync(0xffffffffu, !*s_abort);
+        int n = 0;
+        for (long long it = lo; it < hi && live; ++it) {
+            const int k = (int)(it - lo), s = k & 1;
+            if (first(it)) {
+                live = wt(MB_SFULL, n, 100);
+                if (!live) break;
+                tc_fence_after();
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t raw[32];
+                    SSD_TMEM_LD32_WAIT(buf + (half + 2 * cc) * 32, raw);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) S[cc][i] = __uint_as_float(raw[i]), dS[cc][i] = 0.f;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(MB_SREAD));
+                ++n;
+            }
+            live = wt(MB_FULLXY + s, k >> 1, 101) && (k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 102)) &&
+                   wt(MB_GFULL, k, 103);
+            if (!live) break;
+            tc_fence_after();
+            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
+            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
+            const float cs2 = terms[kTermCs2 * kBlk + r], dtj = terms[kTermDt * kBlk + r];
+            float col = 0.f;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                const int c = half + 2 * cc;
+                const uint32_t at = buf + c * 32;
+                uint32_t pk[8];  // M^T of 16 columns, in the first 16 of the group's 32 columns
+                if (c < q) {  // i < j: nothing
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) pk[i] = 0u;
+                    SSD_TMEM_ST8_WAIT(at, pk);
+                    SSD_TMEM_ST8_WAIT(at + 8, pk);
+                    continue;
+                }
+                float w[32];
+                uint32_t* raw = reinterpret_cast<uint32_t*>(w);
+                SSD_TMEM_LD32_WAIT(at, raw);
+                if (c > q) {
+                    // L_ij = exp(csub_i) exp(cs at the end of group c - 1, less cs_j)
+                    float d = terms[kTermCs2 * kBlk + 32 * q + 31] - cs2;
+                    for (int b = q + 1; b < c; ++b) d += terms[kTermCs2 * kBlk + 32 * b + 31];
+                    const float v = ex2(d);
+#pragma unroll
+                    for (int i4 = 0; i4 < 8; ++i4) {
+                        const float4 u4 = *reinterpret_cast<const float4*>(terms + kTermU * kBlk + 32 * c + 4 * i4);
+                        const float uu[4] = {u4.x, u4.y, u4.z, u4.w};
+                        float m[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 4 * i4 + e;
+                            const float l = uu[e] * v, t = w[i] * l;
+                            dS[cc][i] = fmaf(t, dtj, dS[cc][i]);
+                            m[e] = S[cc][i] * l;
+                            w[i] = S[cc][i] * t;
+                            col += w[i];
+                            w[i] *= dtj;
+                        }
+                        pk[2 * (i4 & 3)] = pack_bf16(m[0], m[1]);
+                        pk[2 * (i4 & 3) + 1] = pack_bf16(m[2], m[3]);
+                        if ((i4 & 3) == 3) SSD_TMEM_ST8_WAIT(at + (i4 >> 2) * 8, pk);
+                    }
+                } else {  // the diagonal group: i > j pairs by their own exponential, i = j apart
+                    float dia = 0.f, gd = 0.f;
+#pragma unroll
+                    for (int i4 = 0; i4 < 8; ++i4) {
+                        const float4 c4 = *reinterpret_cast<const float4*>(terms + kTermCs2 * kBlk + 32 * c + 4 * i4);
+                        const float ci[4] = {c4.x, c4.y, c4.z, c4.w};
+                        float m[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 4 * i4 + e;
+                            const bool below = i > lane, on = i == lane;
+                            const float l = below ? ex2(ci[e] - cs2) : on ? 1.f : 0.f;
+                            const float t = below || on ? w[i] * l : 0.f;
+                            dS[cc][i] = fmaf(t, dtj, dS[cc][i]);
+                            m[e] = l != 0.f ? S[cc][i] * l : 0.f;
+                            const float ww = t != 0.f ? S[cc][i] * t : 0.f;
+                            if (on) dia = ww, gd = t;
+                            w[i] = below ? ww : 0.f;
+                            col += w[i];
+                            w[i] *= dtj;
+                        }
+                        pk[2 * (i4 & 3)] = pack_bf16(m[0], m[1]);
+                        pk[2 * (i4 & 3) + 1] = pack_bf16(m[2], m[3]);
+                        if ((i4 & 3) == 3) SSD_TMEM_ST8_WAIT(at + (i4 >> 2) * 8, pk);
+                    }
+                    sums[kSumDia * kBlk + r] = dia;
+                    sums[kSumGd * kBlk + r] = gd;
+                }
+                sums[(kSumRow + q) * kBlk + 32 * c + lane] = transpose_sum(w, lane);
+            }
+            sums[(kSumCol + half) * kBlk + r] = col;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(MB_MREADY));
+                mbar_arrive(bar(MB_SUMFULL + s));
+                mbar_arrive(bar(MB_EMPTYT + s));
+            }
+            if (last(it)) {
+                // dS^T [j][i] in bf16 over the h image, once the item's products have read it
+                live = wt(MB_EMPTYST, k, 104);
+                if (!live) break;
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    const int c = half + 2 * cc;
+                    uint8_t* tile = smem + kMH + (c >> 1) * kRegion;
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (c >= q) {
+                            v.x = pack_bf16(dS[cc][8 * c4 + 0], dS[cc][8 * c4 + 1]);
+                            v.y = pack_bf16(dS[cc][8 * c4 + 2], dS[cc][8 * c4 + 3]);
+                            v.z = pack_bf16(dS[cc][8 * c4 + 4], dS[cc][8 * c4 + 5]);
+                            v.w = pack_bf16(dS[cc][8 * c4 + 6], dS[cc][8 * c4 + 7]);
+                        }
+                        *reinterpret_cast<uint4*>(tile + swz(r, (c & 1) * 4 + c4)) = v;
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(MB_DSREADY));
+                live = wt(MB_ACCDONE, n - 1, 105);
+                if (!live) break;
+                tc_fence_after();
+                // row r of dB and dC, columns [64 half, 64 half + 64): in full here, or one CTA's share
+                const long long unit = it / hg;
+                const int g = (int)(unit % G), bc = (int)(unit / G), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+                const bool whole = unit * hg >= lo && (unit + 1) * hg <= hi;
+                const size_t row = (((size_t)bi * T + t0 + r) * G + g) * kN + half * 64;
+                float* part = p.part + (((size_t)blockIdx.x * 2 + (unit * hg < lo || unit * hg == lo ? 0 : 1)) * 2) * kBlk * kN +
+                              (size_t)r * kN + half * 64;
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {  // dB, dC by 32 columns
+                    uint32_t raw[32];
+                    const int which = m >> 1, o = (m & 1) * 32;
+                    SSD_TMEM_LD32_WAIT(tmem + ((uint32_t)(q * 32) << 16) + (which ? kColC : kColB) + half * 64 + o, raw);
+                    if (whole) {
+                        if (t0 + r < T) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(which ? p.a.dC : p.a.dB) + row + o);
+#pragma unroll
+                            for (int c4 = 0; c4 < 4; ++c4)
+                                dst[c4] = make_uint4(
+                                    pack_bf16(__uint_as_float(raw[8 * c4 + 0]), __uint_as_float(raw[8 * c4 + 1])),
+                                    pack_bf16(__uint_as_float(raw[8 * c4 + 2]), __uint_as_float(raw[8 * c4 + 3])),
+                                    pack_bf16(__uint_as_float(raw[8 * c4 + 4]), __uint_as_float(raw[8 * c4 + 5])),
+                                    pack_bf16(__uint_as_float(raw[8 * c4 + 6]), __uint_as_float(raw[8 * c4 + 7])));
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(part + which * kBlk * kN + o);
+#pragma unroll
+                        for (int c4 = 0; c4 < 8; ++c4)
+                            dst[c4] = make_uint4(raw[4 * c4], raw[4 * c4 + 1], raw[4 * c4 + 2], raw[4 * c4 + 3]);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(MB_UNITFREE));
+            }
+        }
+    } else {
+        // ================================================================ row group
+        reg_dec<kRegsRow>();
+        const int q = warp & 3, r = q * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+        bool live = __all_sync(0xffffffffu, !*s_abort);
+        for (long long it = lo; it < hi && live; ++it) {
+            const int k = (int)(it - lo), s = k & 1;
+            const int h = (int)(it % H);
+            live = wt(MB_FULLXY + s, k >> 1, 110) && (k < 1 || wt(MB_DBDONE, k - 1, 111));
+            if (!live) break;
+            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
+            const float er = terms[kTermE * kBlk + r], wr = terms[kTermW * kBlk + r], dtr = terms[kTermDt * kBlk + r];
+            const float Dh = p.a.D[h];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(MB_EMPTYT + s));
+            uint8_t* xs = smem + kMX + s * kRegion;
+            const uint8_t* ys = smem + kMY + s * kRegion;
+            auto weigh = [&](const uint8_t* src, float w) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c));
+                    *reinterpret_cast<uint4*>(smem + kMW + swz(r, c)) =
+                        make_uint4(pack_bf16(w * bf_lo(v.x), w * bf_hi(v.x)), pack_bf16(w * bf_lo(v.y), w * bf_hi(v.y)),
+                                   pack_bf16(w * bf_lo(v.z), w * bf_hi(v.z)), pack_bf16(w * bf_lo(v.w), w * bf_hi(v.w)));
+                }
+                fence_proxy_async();
+                __syncwarp();
+            };
+            weigh(ys, er);
+            if (lane == 0) mbar_arrive(bar(MB_EYREADY));
+            // sum over 32 columns of a row of `src` times raw
+            auto dot = [&](const uint8_t* src, int c0, const uint32_t (&raw)[32]) {
+                float f = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c0 + c));
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f = fmaf(bf_lo(in[i]), __uint_as_float(raw[8 * c + 2 * i]), f);
+                        f = fmaf(bf_hi(in[i]), __uint_as_float(raw[8 * c + 2 * i + 1]), f);
+                    }
+                }
+                return f;
+            };
+            // V: F_j / dt_j = w_j x_j . V_j, and w o V in its place
+            live = wt(MB_VDONE, k, 112);
+            if (!live) break;
+            tc_fence_after();
+            float F = 0.f, E = 0.f;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                uint32_t raw[32];
+                SSD_TMEM_LD32_WAIT(lane_addr + kColV + 32 * o, raw);
+                F += dot(xs, 4 * o, raw);
+                uint32_t *ra = raw, *rb = raw + 16;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(wr * __uint_as_float(raw[i]));
+                SSD_TMEM_ST16x2_WAIT(lane_addr + kColV + 32 * o, ra, lane_addr + kColV + 32 * o + 16, rb);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(MB_VSCALED));
+            // Y: E_i = e_i dy_i . Y_i
+            live = wt(MB_YDONE, k, 113);
+            if (!live) break;
+            tc_fence_after();
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                uint32_t raw[32];
+                SSD_TMEM_LD32_WAIT(lane_addr + kColY + 32 * o, raw);
+                E += dot(ys, 4 * o, raw);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(MB_YFREE));
+            live = wt(MB_DCDONE, k, 114);
+            if (!live) break;
+            weigh(xs, wr * dtr);
+            if (lane == 0) mbar_arrive(bar(MB_WXREADY));
+            live = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 115);
+            if (!live) break;
+            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
+            sums[kSumE * kBlk + r] = er * E;
+            sums[kSumF * kBlk + r] = wr * F;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(MB_SUMFULL + s));
+            // dx = dt U + D dy, over the thread's own row of X
+            live = wt(MB_UDONE, k, 116);
+            if (!live) break;
+            tc_fence_after();
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                uint32_t raw[32];
+                SSD_TMEM_LD32_WAIT(lane_addr + kColV + 32 * o, raw);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(ys + swz(r, 4 * o + c));
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t out[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = pack_bf16(fmaf(dtr, __uint_as_float(raw[8 * c + 2 * i]), Dh * bf_lo(in[i])),
+                                           fmaf(dtr, __uint_as_float(raw[8 * c + 2 * i + 1]), Dh * bf_hi(in[i])));
+                    *reinterpret_cast<uint4*>(xs + swz(r, 4 * o + c)) = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(MB_UFREE));
+                mbar_arrive(bar(MB_DXSTAGED + s));
+                mbar_arrive(bar(MB_EMPTYXY + s));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1 && tmem != kTmemSentinel) {
+        tc_fence_after();
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// ------------------------------------------------------------------ dB, dC of split groups
+// One block per (chunk, group); a group whose heads lie in one CTA has been stored already.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __grid_constant__ BwdTc p) {
+    const long long unit = blockIdx.x, hg = p.a.H / p.a.G, it0 = unit * hg, it1 = it0 + hg;
+    // CTA x holds items [items x / ctas, items (x + 1) / ctas): the CTA of an item by that rule
+    auto owner = [&](long long it) {
+        long long x = it * p.ctas / p.items;
+        while (p.items * (x + 1) / p.ctas <= it) ++x;
+        while (p.items * x / p.ctas > it) --x;
+        return x;
+    };
+    const long long x0 = owner(it0), x1 = owner(it1 - 1);
+    if (x0 == x1) return;
+    const int g = (int)(unit % p.a.G), bc = (int)(unit / p.a.G), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+    const int rows = min(kBlk, p.a.T - t0);
+    for (int i = threadIdx.x; i < 2 * kBlk * kN / 4; i += kJoinThreads) {
+        const int which = i / (kBlk * kN / 4), e = (i % (kBlk * kN / 4)) * 4, r = e / kN, c = e % kN;
+        if (r >= rows) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (long long x = x0; x <= x1; ++x) {
+            // a CTA's first group sits in its slot 0, a later one (its last) in slot 1
+            const int slot = it0 <= p.items * x / p.ctas ? 0 : 1;
+            const float4 v = *reinterpret_cast<const float4*>(p.part + ((x * 2 + slot) * 2 + which) * kBlk * kN + e);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.a.dC : p.a.dB) + (((size_t)bi * p.a.T + t0 + r) * p.a.G + g) * kN + c;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+}
+
+int tc_sm_count() {
+    static const int n = [] {
+        int v = 0;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess || v < 1) v = 148;
+        return v;
+    }();
+    return n;
+}
+
+size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
+    p->a = a;
+    p->nc = (a.T + kBlk - 1) / kBlk;
+    p->items = (long long)a.b * p->nc * a.H;
+    p->ctas = (int)std::min<long long>(p->items, tc_sm_count());
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char* r = ws ? ws + o : nullptr;
+        o += round_up(bytes, 256);
+        return r;
+    };
+    const size_t n = (size_t)p->items;
+    p->terms = reinterpret_cast<float*>(take(n * kTermBytes));
+    p->img_h = reinterpret_cast<uint8_t*>(take(n * kImage));
+    p->img_g = reinterpret_cast<uint8_t*>(take(n * kImage));
+    p->part = reinterpret_cast<float*>(take((size_t)p->ctas * 4 * kBlk * kN * 4));
+    p->pA = reinterpret_cast<float*>(take(n * 4));
+    p->pD = reinterpret_cast<float*>(take(n * 4));
+    p->pb = reinterpret_cast<float*>(take(n * 4));
+    return o;
+}
+
+std::atomic<unsigned long long> g_starve_bwd{0};
+
+}  // namespace
+
+bool backward_tc_supported(int P, int N, int io) { return io == SSD_BF16 && P == kP && N == kN; }
+
+size_t backward_tc_workspace_bytes(const BwdArgs& a) {
+    BwdTc p;
+    return tc_layout(a, nullptr, &p);
+}
+
+void backward_tc_starve_next(unsigned long long wait_ns) { g_starve_bwd.store(wait_ns); }
+
+// ws: the status word at its start, the passes' scratch `offset` bytes behind it
+int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s) {
+    BwdTc p;
+    memset(&p, 0, sizeof(p));
+    tc_layout(a, static_cast<char*>(ws) + offset, &p);
+    if (!a.dbias) p.pb = nullptr;
+    p.status = static_cast<int*>(ws);
+    const unsigned long long starve = g_starve_bwd.exchange(0);
+    p.starve = starve != 0;
+    p.wait_ns = starve ? starve : kWaitLimitNs;
+    int st;
+    if ((st = make_map(&p.tm_x, a.x, kP, a.H, a.T, a.b)) != SSD_OK) return st;
+    if ((st = make_map(&p.tm_dy, a.dy, kP, a.H, a.T, a.b)) != SSD_OK) return st;
+    if ((st = make_map(&p.tm_B, a.B, kN, a.G, a.T, a.b)) != SSD_OK) return st;
+    if ((st = make_map(&p.tm_C, a.C, kN, a.G, a.T, a.b)) != SSD_OK) return st;
+    if ((st = make_map(&p.tm_dx, a.dx, kP, a.H, a.T, a.b)) != SSD_OK) return st;
+    if ((st = smem_limit_once((const void*)ssd_bwd_tc_state_kernel, (int)kSSmem)) != SSD_OK) return st;
+    if ((st = smem_limit_once((const void*)ssd_bwd_tc_main_kernel, (int)kMSmem)) != SSD_OK) return st;
+    // the main pass waits for registers its warps give up: what it is launched with must cover them
+    static const int main_regs = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, (const void*)ssd_bwd_tc_main_kernel) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (main_regs < kRegsLaunch)
+        return set_error(SSD_ERR_INTERNAL, "main pass built with %d registers a thread, its split needs %d", main_regs, kRegsLaunch);
+    {
+        LaunchScope ls("ssd_bwd_tc_terms", s);
+        ssd_bwd_tc_terms_kernel<<<dim3(a.b * p.nc, (a.H + 7) / 8), kTermThreads, 0, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        LaunchScope ls("ssd_bwd_tc_state", s);
+        ssd_bwd_tc_state_kernel<<<dim3(a.b * a.H, 2), kSThreads, kSSmem, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        LaunchScope ls("ssd_bwd_tc_main", s);
+        ssd_bwd_tc_main_kernel<<<p.ctas, kThreads, kMSmem, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    {
+        LaunchScope ls("ssd_bwd_tc_join", s);
+        ssd_bwd_tc_join_kernel<<<(unsigned)((size_t)a.b * p.nc * a.G), kJoinThreads, 0, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
+    return launch_bwd_head_sums(p.pA, p.pD, p.pb, a.b * p.nc, a.H, a.dA, a.dD, a.dbias, s);
+}
+
+}  // namespace ssd

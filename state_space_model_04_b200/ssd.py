@@ -61,6 +61,8 @@ def lib() -> ctypes.CDLL:
         L.ssd_prefill_check.restype = _i
         L.ssd_debug_starve_next_prefill.argtypes = [ctypes.c_ulonglong]
         L.ssd_debug_starve_next_prefill.restype = _i
+        L.ssd_debug_starve_next_prefill_backward.argtypes = [ctypes.c_ulonglong]
+        L.ssd_debug_starve_next_prefill_backward.restype = _i
         L.ssd_prefill_local_state_workspace_size.argtypes = [_i] * 7
         L.ssd_prefill_local_state_workspace_size.restype = _sz
         L.ssd_prefill_local_state.argtypes = [_i] * 7 + [_vp] * 7 + [_sz, _vp]
@@ -344,6 +346,12 @@ def debug_starve_next_prefill(wait_limit_s=0.1):
     """Failure-detection test hook: the next tensor-core prefill issues no loads, so its
     bounded waits expire after `wait_limit_s` and prefill_check raises SSD_ERR_TIMEOUT."""
     _check(lib().ssd_debug_starve_next_prefill(int(wait_limit_s * 1e9)), "ssd_debug_starve_next_prefill")
+
+
+def debug_starve_next_prefill_backward(wait_limit_s=0.1):
+    """The same hook for the next tensor-core prefill_backward."""
+    _check(lib().ssd_debug_starve_next_prefill_backward(int(wait_limit_s * 1e9)),
+           "ssd_debug_starve_next_prefill_backward")
 
 
 def prefill_local_state(x, dt, A, B, h_local=None, log_decay=None, workspace=None, stream=None):
