@@ -32,7 +32,6 @@
 #include <atomic>
 #include <cstring>
 #include "backward.cuh"
-#define SSD_TC_INLINE_WAITS
 #include "tc.cuh"
 
 namespace ssd {
@@ -44,10 +43,10 @@ constexpr uint32_t kImage = 2 * kRegion;        // a state: hi, lo, each [128 n]
 // per-token terms of an item, [kTerms][128] fp32 (a: step sizes times A; cs: its prefix sum in the
 // chunk, csub: in the token's 32-token group)
 constexpr int kTermCs2 = 0;                     // csub log2(e)
-constexpr int kTermU = 1;                       // exp(csub)
-constexpr int kTermE = 2;                       // exp(cs)
-constexpr int kTermW = 3;                       // exp(cs_last - cs)
-constexpr int kTermDt = 4;                      // dt
+constexpr int kTermE = 1;                       // exp(cs)
+constexpr int kTermW = 2;                       // exp(cs_last - cs)
+constexpr int kTermDt = 3;                      // dt
+constexpr int kTermSlope = 4;                   // of dt over its raw step (1 without one)
 constexpr int kTerms = 5;
 constexpr uint32_t kTermBytes = kTerms * kBlk * 4;
 
@@ -83,12 +82,14 @@ __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __
     if (h >= p.a.H) return;
     const int bc = blockIdx.x, bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
     const double Ah = p.a.A[h];
-    float dt[4];
+    float dt[4], slope[4];
     double cs[4], end[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int t = t0 + 32 * q + lane;
-        dt[q] = t < p.a.T ? dt_value(p.a.dt[((size_t)bi * p.a.T + t) * p.a.H + h], p.a.dtm, h) : 0.f;
+        const float raw = t < p.a.T ? p.a.dt[((size_t)bi * p.a.T + t) * p.a.H + h] : 0.f;
+        dt[q] = t < p.a.T ? dt_value(raw, p.a.dtm, h) : 0.f;
+        slope[q] = p.a.dtm.raw ? dt_slope(raw + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm) : 1.f;
         cs[q] = dt[q] * Ah;
     }
 #pragma unroll
@@ -110,10 +111,10 @@ __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __
     for (int q = 0; q < 4; ++q) {
         const double c = end[q] + cs[q];
         t[kTermCs2 * kBlk + 32 * q] = (float)(cs[q] * 1.4426950408889634);
-        t[kTermU * kBlk + 32 * q] = expf((float)cs[q]);
         t[kTermE * kBlk + 32 * q] = expf((float)c);
         t[kTermW * kBlk + 32 * q] = expf((float)(run - c));
         t[kTermDt * kBlk + 32 * q] = dt[q];
+        t[kTermSlope * kBlk + 32 * q] = slope[q];
     }
 }
 
@@ -139,7 +140,7 @@ __device__ __forceinline__ void work_bar() {
 
 __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __grid_constant__ BwdTc p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int H = p.a.H, nc = p.nc;
     const int u = blockIdx.x, dir = blockIdx.y, h = u % H, bi = u / H, g = h / (H / p.a.G);
     uint8_t* small = smem + kSSmall;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         s_wait_ns = p.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const uint32_t tmem = tmem_alloc_cta(s_tmem, 64, warp == 1);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, 64, warp == 1), 0);
     if (tmem == kTmemSentinel) {
         *s_abort = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (6 << 8));
@@ -187,9 +188,10 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
                 if (k >= 0) mbar_drain(bar(SB_FULL + (k & 1)), (k >> 1) & 1);
         }
     } else if (warp == 1) {
+        if (elect_one()) {
         constexpr uint32_t id = idesc_bf16(128, 64, 1, 1);
-        auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity, s_abort, p.status, where); };
-        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        auto wt = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity, s_abort, p.status, where); };
+        bool ok = !*s_abort;
         for (int k = 0; k < products && ok; ++k) {
             const int s = k & 1;
             ok = wt(SB_FULL + s, (k >> 1) & 1, 51) && wt(SB_XS + s, (k >> 1) & 1, 52) &&
@@ -202,13 +204,15 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
                 const uint64_t dX = sdesc(sbase + kSXs + s * kImage + half * kRegion, kRegion, 1024);
 #pragma unroll 1
                 for (int kk = 0; kk < kBlk / 16; ++kk)
-                    mma_ss_w(tmem, dA + kk * 128, dX + kk * 128, id, half > 0 || kk > 0);
+                    mma_ss(tmem, dA + kk * 128, dX + kk * 128, id, half > 0 || kk > 0);
             }
-            mma_commit_w(bar(SB_EMPTY + s));
-            mma_commit_w(bar(SB_ACC));
+            mma_commit(bar(SB_EMPTY + s));
+            mma_commit(bar(SB_ACC));
         }
-        mma_commit_w(bar(SB_DONE));
+        mma_commit(bar(SB_DONE));
         mbar_drain(bar(SB_DONE), 0);
+        }
+        __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
         const int r = q * 32 + lane;  // token row of a chunk, and state row n
@@ -321,19 +325,30 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
 }
 
 // ------------------------------------------------------------------ main pass
-//   warp 0        producer: X, dY and the terms of an item (2-slot ring), the state halves (one
-//                 slot), B and C of a group
-//   warp 1        TMEM owner and MMA issuer
-//   warp 2        ddt and the sums behind dA, dD; stores the dx tiles
-//   warp 3        <h, dh>
-//   warps 4-11    "pair" group (two warps a TMEM lane quadrant, half of the columns each): S^T
-//                 and the sum of dS^T in registers; per item M^T and W from G^T; per group dB, dC
-//   warps 12-15   "row" group (one token a thread): the weighted rows, F and E from V and Y, dx
-// Registers are moved to where they are needed (setmaxnreg): 128 x (kRegsWarps + kRegsRow +
-// 2 kRegsPair) is what the block was launched with.
-constexpr int kThreads = 512;
-constexpr int kRegsWarps = 48, kRegsRow = 80, kRegsPair = 192, kRegsLaunch = 128;
-static_assert(kRegsWarps + kRegsRow + 2 * kRegsPair <= 4 * kRegsLaunch, "register split");
+// 18 warps; a warp's TMEM lane quadrant is q = warp % 4, and the work of the quadrants differs
+// (tokens j of quadrant q meet tokens i of the 32-token groups c >= q only):
+//
+//   pair warps (q, c), q <= c: 10    S^T and the sum of dS^T of their 32 x 32 block in registers;
+//                                    per item M^T and W from G^T; per group of heads dB, dC
+//   row warps q: 4                   one token a thread: the weighted rows, F and E from V and Y, dx
+//   producer                         X, dY and the terms of an item (2-slot ring), the state halves
+//                                    (one slot), B and C of a group of heads
+//   issuer                           TMEM owner; every tcgen05.mma
+//   ddt                              ddt, the sums behind dA and dD; stores the dx tiles
+//   dot                              <h, dh>
+//
+// The roles' code runs at the same time and is fetched through one instruction cache: straight
+// FMA code measures 2.4 cycles an instruction up to 24 KB and 6 from 48 KB on (one warp a
+// scheduler), so loops stay rolled wherever registers need no constant index, and the slow side of
+// every wait is one call.
+constexpr int kWarps = 18, kThreads = 32 * kWarps;
+enum { ROLE_PAIR, ROLE_ROW, ROLE_ISSUER, ROLE_DDT, ROLE_PRODUCER, ROLE_DOT };
+__device__ __forceinline__ int role_of(int warp) {
+    const int q = warp & 3, j = warp >> 2;
+    if (j < 4 - q) return ROLE_PAIR;  // c = q + j
+    if (j == 4 - q) return ROLE_ROW;
+    return q == 1 ? ROLE_ISSUER : q == 2 ? ROLE_DDT : j == 2 ? ROLE_PRODUCER : ROLE_DOT;
+}
 
 constexpr uint32_t kMB = 0;                          // B: n 0..63, 64..127
 constexpr uint32_t kMC = kMB + 2 * kRegion;          // C
@@ -344,9 +359,9 @@ constexpr uint32_t kMG = kMH + kImage;               // dh image
 constexpr uint32_t kMW = kMG + kImage;               // e o dY, then w dt o X
 constexpr uint32_t kMTerms = kMW + kRegion;          // [2] terms
 constexpr uint32_t kMSums = kMTerms + 2 * kTermBytes;
-// per item, fp32 [128] each: row sums of W by quadrant of j (4), column sums by half (2),
-// Gm_jj S_jj, Gm_jj, E, F / dt; then <h, dh>
-constexpr int kSumRow = 0, kSumCol = 4, kSumDia = 6, kSumGd = 7, kSumE = 8, kSumF = 9, kSums = 10;
+// per item, fp32 [128] each: row sums of W by quadrant of j (4), column sums by group of i (4),
+// S_jj, Gm_jj, E, F / dt
+constexpr int kSumRow = 0, kSumCol = 4, kSumSd = 8, kSumGd = 9, kSumE = 10, kSumF = 11, kSums = 12;
 constexpr uint32_t kSumBytes = kSums * kBlk * 4;
 constexpr uint32_t kMSmall = kMSums + 2 * kSumBytes;
 constexpr uint32_t kMSmem = kMSmall + 512;
@@ -356,52 +371,52 @@ constexpr uint32_t kColB = 0, kColC = 128, kColG = 256, kColV = 384, kColY = 448
 
 enum {
     MB_FULLXY = 0,    // [2] X, dY, terms landed
-    MB_EMPTYXY = 2,   // [2] row group done with dY (4 warps), dx tile read out (1)
-    MB_EMPTYT = 4,    // [2] terms read: pair (8), row (4) warps, ddt warp (1)
+    MB_EMPTYXY = 2,   // [2] row warps done with dY (4), dx tile read out (1)
+    MB_EMPTYT = 4,    // [2] terms read: pair (10), row (4), ddt (1)
     MB_FULLST = 6,    // state halves landed
     MB_EMPTYST = 7,   // every product that reads them done (1), <h, dh> done (1)
     MB_FULLBC = 8,    // B, C landed
     MB_SFULL = 9,     // S^T accumulated
-    MB_SREAD = 10,    // pair group read it (8)
+    MB_SREAD = 10,    // pair warps read it (10)
     MB_GFULL = 11,    // G^T accumulated
-    MB_MREADY = 12,   // pair group wrote M^T (8)
+    MB_MREADY = 12,   // pair warps wrote M^T (10)
     MB_UDONE = 13,    // U accumulated: M^T is read too
     MB_VDONE = 14,    // V accumulated
-    MB_VSCALED = 15,  // row group replaced V by w o V (4)
-    MB_UFREE = 16,    // row group read U (4)
+    MB_VSCALED = 15,  // row warps replaced V by w o V (4)
+    MB_UFREE = 16,    // row warps read U (4)
     MB_YDONE = 17,    // Y accumulated
-    MB_YFREE = 18,    // row group read Y (4)
-    MB_EYREADY = 19,  // row group wrote e o dY (4)
+    MB_YFREE = 18,    // row warps read Y (4)
+    MB_EYREADY = 19,  // row warps wrote e o dY (4)
     MB_DCDONE = 20,   // dC's product done: the tile is free
-    MB_WXREADY = 21,  // row group wrote w dt o X (4)
+    MB_WXREADY = 21,  // row warps wrote w dt o X (4)
     MB_DBDONE = 22,   // dB's product done: the tile is free
-    MB_SUMFULL = 23,  // [2] sums written: pair (8), row (4), <h, dh> (1)
+    MB_SUMFULL = 23,  // [2] sums written: pair (10), row (4), <h, dh> (1)
     MB_SUMEMPTY = 25, // [2] sums read (1)
     MB_DXSTAGED = 27, // [2] dx tile written (4)
-    MB_DSREADY = 29,  // pair group wrote the dS^T tile (8)
+    MB_DSREADY = 29,  // pair warps wrote the dS^T tile (10)
     MB_ACCDONE = 30,  // dB, dC complete
-    MB_UNITFREE = 31, // pair group read them (8): B, C, the accumulators and the tile are free
+    MB_UNITFREE = 31, // pair warps read them (10): B, C, the accumulators and the tile are free
     MB_DONE = 32,
     MB_COUNT
 };
 static_assert(MB_COUNT * 8 <= 320, "barriers");
-__device__ constexpr uint32_t main_bar_count(int i) {
+__device__ __forceinline__ uint32_t main_bar_count(int i) {
     switch (i) {
         case MB_EMPTYXY: case MB_EMPTYXY + 1: return 5;
-        case MB_EMPTYT: case MB_EMPTYT + 1: case MB_SUMFULL: case MB_SUMFULL + 1: return 13;
+        case MB_EMPTYT: case MB_EMPTYT + 1: case MB_SUMFULL: case MB_SUMFULL + 1: return 15;
         case MB_EMPTYST: return 2;
-        case MB_SREAD: case MB_MREADY: case MB_DSREADY: case MB_UNITFREE: return 8;
+        case MB_SREAD: case MB_MREADY: case MB_DSREADY: case MB_UNITFREE: return 10;
         case MB_VSCALED: case MB_UFREE: case MB_YFREE: case MB_EYREADY: case MB_WXREADY:
         case MB_DXSTAGED: case MB_DXSTAGED + 1: return 4;
         default: return 1;
     }
 }
 
-// v[i] of every lane summed over the lanes; lane l gets the sum of v[l].  Halving exchange: 31
-// shuffles for 32 sums.
-__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+// v[i] of every lane summed over the lanes; lane l gets the sum of v[l % 8].  Halving exchange: 9
+// shuffles for 8 sums.
+__device__ __forceinline__ float transpose_sum(float (&v)[8], int lane) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 4; o > 0; o >>= 1) {
         const bool up = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -409,17 +424,38 @@ __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
-    return v[0];
+    const float a = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 8);
+    return a + __shfl_xor_sync(0xffffffffu, a, 16);
 }
 
-template <int kRegs> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+// The items of one CTA, [lo, hi) of items = b nc H (< 2^31), in order: item (chunk bc of all
+// sequences' chunks, head h), the head's place hh in its group.  Divisions happen once.
+struct Walk {
+    int k, n, h, hh, bc;  // k-th of n
+    int H, hg;
+    __device__ __forceinline__ Walk(int lo, int hi, int H_, int hg_) : k(0), n(hi - lo), H(H_), hg(hg_) {
+        bc = lo / H;
+        h = lo - bc * H;
+        hh = h % hg;
+    }
+    __device__ __forceinline__ bool first() const { return k == 0 || hh == 0; }  // of its group, in this CTA
+    __device__ __forceinline__ bool last() const { return k + 1 == n || hh + 1 == hg; }
+    __device__ __forceinline__ bool more() const { return k < n; }
+    __device__ __forceinline__ void next() {
+        ++k;
+        if (++hh == hg) hh = 0;
+        if (++h == H) h = 0, ++bc;
+    }
+    __device__ __forceinline__ int next_head() const { return h + 1 == H ? 0 : h + 1; }
+};
 
 __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __grid_constant__ BwdTc p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // uniform for the compiler too: what a warp feeds to tcgen05 and TMA stays in uniform registers
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int role = role_of(warp), q = warp & 3;
     const int H = p.a.H, G = p.a.G, T = p.a.T, hg = H / G;
-    const long long lo = p.items * blockIdx.x / p.ctas, hi = p.items * (blockIdx.x + 1) / p.ctas;
+    const int lo = (int)(p.items * blockIdx.x / p.ctas), hi = (int)(p.items * (blockIdx.x + 1) / p.ctas);
     uint8_t* small = smem + kMSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
     volatile int* s_abort = reinterpret_cast<volatile int*>(small + 320);
@@ -427,8 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
     float* s_z = reinterpret_cast<float*>(small + 352);  // [2]
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    auto wt = [&](int b, uint32_t parity, int where) {
-        return warp_wait(bar(b), parity & 1, s_abort, p.status, where);
+    // waits of a whole warp, and of one thread
+    auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity & 1, s_abort, p.status, where); };
+    auto w1 = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity & 1, s_abort, p.status, where); };
+    // one arrival of the warp, once all its lanes are here
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
     };
 
     if (threadIdx.x == 0) {
@@ -439,432 +480,157 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
         s_wait_ns = p.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const uint32_t tmem = tmem_alloc_cta(s_tmem, 512, warp == 1);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, 512, role == ROLE_ISSUER), 0);
     if (tmem == kTmemSentinel) {
         *s_abort = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (8 << 8));
     }
-    // Every role walks the same items: k counts them (per-item barriers complete once each), n the
-    // groups begun.
-    auto first = [&](long long it) { return it == lo || it % hg == 0; };
-    auto last = [&](long long it) { return it + 1 == hi || (it + 1) % hg == 0; };
-
-    if (warp < 4) {
-        reg_dec<kRegsWarps>();
-        if (warp == 0) {
-            // ============================================================ producer
-            if (lane == 0 && !*s_abort && !p.starve) {
-                int nxy = 0, nst = 0, nbc = 0, n = 0;
-                auto w1 = [&](int b, uint32_t parity, int where) {
-                    return mbar_wait(bar(b), parity & 1, s_abort, p.status, where);
-                };
-                for (long long it = lo; it < hi; ++it) {
-                    const int k = (int)(it - lo), s = k & 1;
-                    const int h = (int)(it % H), bc = (int)(it / H), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
-                    if (k >= 2 && !(w1(MB_EMPTYXY + s, (k - 2) >> 1, 60) && w1(MB_EMPTYT + s, (k - 2) >> 1, 61))) break;
-                    const uint32_t f = bar(MB_FULLXY + s);
-                    mbar_expect_tx(f, 2 * kRegion + kTermBytes);
-                    tma_load_4d(sbase + kMX + s * kRegion, &p.tm_x, f, 0, h, t0, bi);
-                    tma_load_4d(sbase + kMY + s * kRegion, &p.tm_dy, f, 0, h, t0, bi);
-                    bulk_load(sbase + kMTerms + s * kTermBytes, p.terms + it * kTerms * kBlk, kTermBytes, f);
-                    nxy = k + 1;
-                    if (first(it)) {
-                        if (n > 0 && !w1(MB_UNITFREE, n - 1, 62)) break;
-                        const uint32_t fb = bar(MB_FULLBC);
-                        const int g = h / hg;
-                        mbar_expect_tx(fb, 4 * kRegion);
-                        tma_load_4d(sbase + kMB, &p.tm_B, fb, 0, g, t0, bi);
-                        tma_load_4d(sbase + kMB + kRegion, &p.tm_B, fb, 64, g, t0, bi);
-                        tma_load_4d(sbase + kMC, &p.tm_C, fb, 0, g, t0, bi);
-                        tma_load_4d(sbase + kMC + kRegion, &p.tm_C, fb, 64, g, t0, bi);
-                        nbc = ++n;
-                    }
-                    if (k >= 1 && !w1(MB_EMPTYST, k - 1, 63)) break;
-                    const uint32_t fs = bar(MB_FULLST);
-                    mbar_expect_tx(fs, 2 * kImage);
-                    bulk_load(sbase + kMG, p.img_g + it * kImage, kImage, fs);
-                    bulk_load(sbase + kMH, p.img_h + it * kImage, kImage, fs);
-                    nst = k + 1;
-                }
-                // loads nobody may have waited for land before the CTA exits
-                for (int k = nxy - 2; k < nxy; ++k)
-                    if (k >= 0) mbar_drain(bar(MB_FULLXY + (k & 1)), (k >> 1) & 1);
-                if (nst > 0) mbar_drain(bar(MB_FULLST), (nst - 1) & 1);
-                if (nbc > 0) mbar_drain(bar(MB_FULLBC), (nbc - 1) & 1);
-            }
-        } else if (warp == 1) {
-            // ============================================================ MMA issuer
-            constexpr uint32_t id_nn = idesc_bf16(128, 128, 0, 0);   // both K-major
-            constexpr uint32_t id_st = idesc_bf16(128, 64, 0, 1);    // state or dY [K rows][64]: MN-major
-            constexpr uint32_t id_db = idesc_bf16(128, 128, 0, 1);
-            constexpr uint32_t id_dc = idesc_bf16(128, 128, 1, 1);
-            auto koff = [](int kk) { return (uint32_t)((kk >> 2) * (kRegion >> 4) + (kk & 3) * 2); };
-            bool ok = __all_sync(0xffffffffu, !*s_abort);
-            int n = 0;
-            for (long long it = lo; it < hi && ok; ++it) {
-                const int k = (int)(it - lo), s = k & 1;
-                const bool fresh = first(it);
-                const uint32_t x = sbase + kMX + s * kRegion, y = sbase + kMY + s * kRegion;
-                // G^T's columns: U of the item before has read M^T there
-                ok = k < 1 || wt(MB_UDONE, k - 1, 70);
-                if (!ok) break;
-                if (fresh) {
-                    ok = (n < 1 || wt(MB_UNITFREE, n - 1, 71)) && wt(MB_FULLBC, n, 72);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dB = sdesc(sbase + kMB, 16, 1024), dC = sdesc(sbase + kMC, 16, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < kN / 16; ++kk)
-                        mma_ss_w(tmem + kColG, dB + koff(kk), dC + koff(kk), id_nn, kk > 0);
-                    mma_commit_w(bar(MB_SFULL));
-                    ok = wt(MB_SREAD, n, 73);
-                    if (!ok) break;
-                    ++n;
-                }
-                ok = wt(MB_FULLXY + s, k >> 1, 74);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    const uint64_t dX = sdesc(x, 16, 1024), dY = sdesc(y, 16, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < kP / 16; ++kk) mma_ss_w(tmem + kColG, dX + kk * 2, dY + kk * 2, id_nn, kk > 0);
-                    mma_commit_w(bar(MB_GFULL));
-                }
-                // V = B dh^T, Y = C h^T, hi then lo
-                ok = wt(MB_FULLST, k, 75) && (k < 1 || wt(MB_UFREE, k - 1, 76));
-                if (!ok) break;
-                tc_fence_after();
-                auto state_product = [&](uint32_t col, uint32_t left, uint32_t image) {
-                    const uint64_t dL = sdesc(left, 16, 1024);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const uint64_t dI = sdesc(image + half * kRegion, kRegion, 1024);
-#pragma unroll 1
-                        for (int kk = 0; kk < kN / 16; ++kk)
-                            mma_ss_w(tmem + col, dL + koff(kk), dI + kk * 128, id_st, half > 0 || kk > 0);
-                    }
-                };
-                state_product(kColV, sbase + kMB, sbase + kMG);
-                mma_commit_w(bar(MB_VDONE));
-                ok = k < 1 || wt(MB_YFREE, k - 1, 77);
-                if (!ok) break;
-                tc_fence_after();
-                state_product(kColY, sbase + kMC, sbase + kMH);
-                mma_commit_w(bar(MB_YDONE));
-                // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
-                auto row_product = [&](uint32_t col, uint32_t image) {
-                    const uint64_t dW = sdesc(sbase + kMW, 16, 1024), dI = sdesc(image, 16, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < kP / 16; ++kk)
-                        mma_ss_w(tmem + col, dW + kk * 2, dI + kk * 2, id_nn, !fresh || kk > 0);
-                };
-                ok = wt(MB_EYREADY, k, 78);
-                if (!ok) break;
-                tc_fence_after();
-                row_product(kColC, sbase + kMH);
-                mma_commit_w(bar(MB_DCDONE));
-                ok = wt(MB_WXREADY, k, 79);
-                if (!ok) break;
-                tc_fence_after();
-                row_product(kColB, sbase + kMG);
-                mma_commit_w(bar(MB_DBDONE));
-                mma_commit_w(bar(MB_EMPTYST));
-                // U = w o V + M^T dY
-                ok = wt(MB_VSCALED, k, 80) && wt(MB_MREADY, k, 81);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    const uint64_t dY = sdesc(y, kRegion, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < kBlk / 16; ++kk)
-                        mma_ts_w(tmem + kColV, tmem + kColG + (kk >> 1) * 32 + (kk & 1) * 8, dY + kk * 128, id_st, 1);
-                    mma_commit_w(bar(MB_UDONE));
-                }
-                if (last(it)) {
-                    ok = wt(MB_DSREADY, n - 1, 82);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dSk = sdesc(sbase + kMH, 16, 1024), dSm = sdesc(sbase + kMH, kRegion, 1024);
-                    const uint64_t dB = sdesc(sbase + kMB, kRegion, 1024), dC = sdesc(sbase + kMC, kRegion, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < kBlk / 16; ++kk)
-                        mma_ss_w(tmem + kColB, dSk + koff(kk), dC + kk * 128, id_db, 1);
-#pragma unroll 1
-                    for (int kk = 0; kk < kBlk / 16; ++kk)
-                        mma_ss_w(tmem + kColC, dSm + kk * 128, dB + kk * 128, id_dc, 1);
-                    mma_commit_w(bar(MB_ACCDONE));
-                }
-            }
-            mma_commit_w(bar(MB_DONE));
-            mbar_drain(bar(MB_DONE), 0);
-        } else if (warp == 2) {
-            // ============================================================ ddt, sums, dx stores
-            bool ok = __all_sync(0xffffffffu, !*s_abort);
-            for (long long it = lo; it < hi && ok; ++it) {
-                const int k = (int)(it - lo), s = k & 1;
-                const int h = (int)(it % H), bc = (int)(it / H), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
-                ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
-                if (!ok) break;
-                const float* sums = reinterpret_cast<const float*>(smem + kMSums + s * kSumBytes);
-                const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
-                // tokens 4 lane .. 4 lane + 3
-                const int q = lane >> 3;
-                float rc[4], f[4], dir[4];
-                float zz = s_z[s] * terms[kTermE * kBlk + kBlk - 1];
-                float suf = 0.f, pre = 0.f, sD = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 4 * lane + i;
-                    const float dt = terms[kTermDt * kBlk + t];
-                    const float col = sums[kSumCol * kBlk + t] + sums[(kSumCol + 1) * kBlk + t];
-                    const float fj = sums[kSumF * kBlk + t];
-                    float row = sums[kSumE * kBlk + t];
-                    for (int qq = 0; qq <= q; ++qq) row += sums[(kSumRow + qq) * kBlk + t];
-                    rc[i] = fmaf(-col, dt, row);
-                    f[i] = fj * dt;
-                    dir[i] = sums[kSumDia * kBlk + t] + col + fj;
-                    sD += sums[kSumGd * kBlk + t];
-                    suf += rc[i];
-                    pre += f[i];
-                }
-                const float own = suf, fown = pre;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_down_sync(0xffffffffu, suf, o), c = __shfl_up_sync(0xffffffffu, pre, o);
-                    if (lane + o < 32) suf += a;
-                    if (lane >= o) pre += c;
-                }
-                (void)own;
-                pre -= fown;
-                const float Ah = p.a.A[h];
-                float sA = 0.f, sb = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 4 * lane + i;
-                    const float da = zz + suf + pre;
-                    suf -= rc[i];
-                    pre += f[i];
-                    float ddt = fmaf(Ah, da, dir[i]);
-                    if (t0 + t < T) {
-                        const size_t o = ((size_t)bi * T + t0 + t) * H + h;
-                        if (p.a.dtm.raw) ddt *= dt_slope(p.a.dt[o] + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm);
-                        p.a.ddt[o] = ddt;
-                        sA = fmaf(terms[kTermDt * kBlk + t], da, sA);
-                        sb += ddt;
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    sA += __shfl_xor_sync(0xffffffffu, sA, o);
-                    sD += __shfl_xor_sync(0xffffffffu, sD, o);
-                    sb += __shfl_xor_sync(0xffffffffu, sb, o);
-                }
-                if (lane == 0) {
-                    p.pA[it] = sA;
-                    p.pD[it] = sD;
-                    if (p.pb) p.pb[it] = sb;
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(MB_SUMEMPTY + s));
-                    mbar_arrive(bar(MB_EMPTYT + s));
-                }
-                ok = wt(MB_DXSTAGED + s, k >> 1, 92);
-                if (!ok) break;
-                if (lane == 0) {
-                    tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, h, t0, bi);
-                    bulk_commit();
-                    bulk_wait_read0();
-                    mbar_arrive(bar(MB_EMPTYXY + s));
-                }
-                __syncwarp();
-            }
-            if (lane == 0) bulk_wait0();
-        } else {
-            // ============================================================ <h, dh>
-            bool ok = __all_sync(0xffffffffu, !*s_abort);
-            for (long long it = lo; it < hi && ok; ++it) {
-                const int k = (int)(it - lo), s = k & 1;
-                ok = wt(MB_FULLST, k, 95);
-                if (!ok) break;
-                const uint4 *h4 = reinterpret_cast<const uint4*>(smem + kMH), *g4 = reinterpret_cast<const uint4*>(smem + kMG);
-                float z0 = 0.f, z1 = 0.f;
-#pragma unroll 2
-                for (int i = lane; i < (int)(kRegion / 16); i += 32) {
-                    const uint4 a = h4[i], al = h4[i + kRegion / 16], b = g4[i], bl = g4[i + kRegion / 16];
-                    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, av2[4] = {al.x, al.y, al.z, al.w};
-                    const uint32_t bv[4] = {b.x, b.y, b.z, b.w}, bv2[4] = {bl.x, bl.y, bl.z, bl.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        z0 = fmaf(bf_lo(av[j]) + bf_lo(av2[j]), bf_lo(bv[j]) + bf_lo(bv2[j]), z0);
-                        z1 = fmaf(bf_hi(av[j]) + bf_hi(av2[j]), bf_hi(bv[j]) + bf_hi(bv2[j]), z1);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(MB_EMPTYST));
-                z0 += z1;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) z0 += __shfl_xor_sync(0xffffffffu, z0, o);
-                ok = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 96);
-                if (!ok) break;
-                if (lane == 0) {
-                    s_z[s] = z0;
-                    mbar_arrive(bar(MB_SUMFULL + s));
-                }
-                __syncwarp();
-            }
-        }
-    } else if (warp < 12) {
-        // ================================================================ pair group
-        reg_inc<kRegsPair>();
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        const int r = q * 32 + lane;  // token j
-        const uint32_t buf = tmem + ((uint32_t)(q * 32) << 16) + kColG;
-        // columns i: 32-token groups c = half and half + 2; the pair needs c >= q
-        float S[2][32], dS[2][32];
+    // Every role walks the same items: i.k counts them (per-item barriers complete once each), n
+    // the groups begun.
+    if (role == ROLE_PAIR) {
+        const int c = q + (warp >> 2);  // columns i: tokens 32 c ..
+        const bool diagonal = c == q;
+        const int r = q * 32 + lane;    // row: token j
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), at = lanes + kColG + c * 32;
+        // the blocks of quadrant q with i < j, which its 4 - q warps keep zero between them
+        const int z0 = c - q, zstep = 4 - q;
+        f32x2 S[16], dS[16];  // pairs of columns
+        float sd = 0.f;       // S_jj
         bool live = __all_sync(0xffffffffu, !*s_abort);
         int n = 0;
-        for (long long it = lo; it < hi && live; ++it) {
-            const int k = (int)(it - lo), s = k & 1;
-            if (first(it)) {
+        for (Walk i(lo, hi, H, hg); i.more() && live; i.next()) {
+            const int k = i.k, s = k & 1;
+            if (i.first()) {
                 live = wt(MB_SFULL, n, 100);
                 if (!live) break;
                 tc_fence_after();
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    uint32_t raw[32];
-                    SSD_TMEM_LD32_WAIT(buf + (half + 2 * cc) * 32, raw);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) S[cc][i] = __uint_as_float(raw[i]), dS[cc][i] = 0.f;
-                }
+                uint32_t raw[32];
+                SSD_TMEM_LD32_WAIT(at, raw);
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(MB_SREAD));
+                arrive(MB_SREAD);
                 ++n;
+                // of the diagonal block only i > j stays: i = j, where L = 1, goes by S_jj and Gm_jj
+                // (its terms of W straddle no token, and dx_j takes dt_j S_jj dy_j from the row warp)
+                if (diagonal) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j == lane) sd = __uint_as_float(raw[j]);
+                        if (j <= lane) raw[j] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    S[j] = pack2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
+                    dS[j] = 0ull;
+                }
             }
             live = wt(MB_FULLXY + s, k >> 1, 101) && (k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 102)) &&
                    wt(MB_GFULL, k, 103);
             if (!live) break;
             tc_fence_after();
-            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
+            const float* cs2 = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + kTermCs2 * kBlk;
             float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
-            const float cs2 = terms[kTermCs2 * kBlk + r], dtj = terms[kTermDt * kBlk + r];
-            float col = 0.f;
+            const float dtj = cs2[(kTermDt - kTermCs2) * kBlk + r];
+            // L_ij = exp(cs_i - cs_j) = 2^(csub_i + d): -d is csub_j, less the totals of the groups
+            // between
+            float d = -cs2[r];
+#pragma unroll 1
+            for (int b = q; b < c; ++b) d += cs2[32 * b + 31];
+            const f32x2 d2 = pack2(d, d), dt2 = pack2(dtj, dtj);
+            f32x2 col2 = 0ull;
+            float gd = 0.f;
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                const int c = half + 2 * cc;
-                const uint32_t at = buf + c * 32;
-                uint32_t pk[8];  // M^T of 16 columns, in the first 16 of the group's 32 columns
-                if (c < q) {  // i < j: nothing
+            for (int o = 0; o < 4; ++o) {  // 8 columns at a time: few enough registers beside S and dS
+                uint32_t raw[8];
+                SSD_TMEM_LD8_WAIT(at + 8 * o, raw);
+                float w[8], e[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) pk[i] = 0u;
-                    SSD_TMEM_ST8_WAIT(at, pk);
-                    SSD_TMEM_ST8_WAIT(at + 8, pk);
-                    continue;
+                for (int j = 0; j < 2; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(cs2 + 32 * c + 8 * o + 4 * j);
+                    unpack2(add2(pack2(v.x, v.y), d2), e[4 * j], e[4 * j + 1]);
+                    unpack2(add2(pack2(v.z, v.w), d2), e[4 * j + 2], e[4 * j + 3]);
                 }
-                float w[32];
-                uint32_t* raw = reinterpret_cast<uint32_t*>(w);
-                SSD_TMEM_LD32_WAIT(at, raw);
-                if (c > q) {
-                    // L_ij = exp(csub_i) exp(cs at the end of group c - 1, less cs_j)
-                    float d = terms[kTermCs2 * kBlk + 32 * q + 31] - cs2;
-                    for (int b = q + 1; b < c; ++b) d += terms[kTermCs2 * kBlk + 32 * b + 31];
-                    const float v = ex2(d);
 #pragma unroll
-                    for (int i4 = 0; i4 < 8; ++i4) {
-                        const float4 u4 = *reinterpret_cast<const float4*>(terms + kTermU * kBlk + 32 * c + 4 * i4);
-                        const float uu[4] = {u4.x, u4.y, u4.z, u4.w};
-                        float m[4];
+                for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(raw[j]);
+                if (diagonal) {  // i < j counts for nothing, whatever G holds there
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = 4 * i4 + e;
-                            const float l = uu[e] * v, t = w[i] * l;
-                            dS[cc][i] = fmaf(t, dtj, dS[cc][i]);
-                            m[e] = S[cc][i] * l;
-                            w[i] = S[cc][i] * t;
-                            col += w[i];
-                            w[i] *= dtj;
-                        }
-                        pk[2 * (i4 & 3)] = pack_bf16(m[0], m[1]);
-                        pk[2 * (i4 & 3) + 1] = pack_bf16(m[2], m[3]);
-                        if ((i4 & 3) == 3) SSD_TMEM_ST8_WAIT(at + (i4 >> 2) * 8, pk);
+                    for (int j = 0; j < 8; ++j) {
+                        const int col = 8 * o + j;
+                        if (col < lane) e[j] = __int_as_float(0xff800000), w[j] = 0.f;
+                        if (col == lane) gd = w[j];
                     }
-                } else {  // the diagonal group: i > j pairs by their own exponential, i = j apart
-                    float dia = 0.f, gd = 0.f;
-#pragma unroll
-                    for (int i4 = 0; i4 < 8; ++i4) {
-                        const float4 c4 = *reinterpret_cast<const float4*>(terms + kTermCs2 * kBlk + 32 * c + 4 * i4);
-                        const float ci[4] = {c4.x, c4.y, c4.z, c4.w};
-                        float m[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = 4 * i4 + e;
-                            const bool below = i > lane, on = i == lane;
-                            const float l = below ? ex2(ci[e] - cs2) : on ? 1.f : 0.f;
-                            const float t = below || on ? w[i] * l : 0.f;
-                            dS[cc][i] = fmaf(t, dtj, dS[cc][i]);
-                            m[e] = l != 0.f ? S[cc][i] * l : 0.f;
-                            const float ww = t != 0.f ? S[cc][i] * t : 0.f;
-                            if (on) dia = ww, gd = t;
-                            w[i] = below ? ww : 0.f;
-                            col += w[i];
-                            w[i] *= dtj;
-                        }
-                        pk[2 * (i4 & 3)] = pack_bf16(m[0], m[1]);
-                        pk[2 * (i4 & 3) + 1] = pack_bf16(m[2], m[3]);
-                        if ((i4 & 3) == 3) SSD_TMEM_ST8_WAIT(at + (i4 >> 2) * 8, pk);
-                    }
-                    sums[kSumDia * kBlk + r] = dia;
-                    sums[kSumGd * kBlk + r] = gd;
                 }
-                sums[(kSumRow + q) * kBlk + 32 * c + lane] = transpose_sum(w, lane);
+                uint32_t pk[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = 4 * o + j;
+                    const f32x2 l = pack2(ex2(e[2 * j]), ex2(e[2 * j + 1])), t = mul2(pack2(w[2 * j], w[2 * j + 1]), l);
+                    dS[m] = fma2(t, dt2, dS[m]);
+                    float a, b;
+                    unpack2(mul2(S[m], l), a, b);
+                    pk[j] = pack_bf16(a, b);
+                    const f32x2 ww = mul2(S[m], t);
+                    col2 = add2(col2, ww);
+                    unpack2(mul2(ww, dt2), w[2 * j], w[2 * j + 1]);
+                }
+                SSD_TMEM_ST4_WAIT(at + 4 * o, pk);  // over the first 16 of the block's columns
+                const float row = transpose_sum(w, lane);
+                if (lane < 8) sums[(kSumRow + q) * kBlk + 32 * c + 8 * o + lane] = row;
             }
-            sums[(kSumCol + half) * kBlk + r] = col;
+            {
+                uint32_t zero[16] = {};
+#pragma unroll 1
+                for (int z = z0; z < q; z += zstep) SSD_TMEM_ST16_WAIT(lanes + kColG + z * 32, zero);
+            }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(MB_MREADY));
-                mbar_arrive(bar(MB_SUMFULL + s));
-                mbar_arrive(bar(MB_EMPTYT + s));
+            arrive(MB_MREADY);
+            float ca, cb;
+            unpack2(col2, ca, cb);
+            sums[(kSumCol + c) * kBlk + r] = ca + cb;
+            if (diagonal) {
+                sums[kSumSd * kBlk + r] = sd;
+                sums[kSumGd * kBlk + r] = gd;
             }
-            if (last(it)) {
+            arrive(MB_SUMFULL + s);
+            arrive(MB_EMPTYT + s);
+            if (i.last()) {
                 // dS^T [j][i] in bf16 over the h image, once the item's products have read it
                 live = wt(MB_EMPTYST, k, 104);
                 if (!live) break;
+                uint8_t* tile = smem + kMH;
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    const int c = half + 2 * cc;
-                    uint8_t* tile = smem + kMH + (c >> 1) * kRegion;
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    uint32_t o[4];
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (c >= q) {
-                            v.x = pack_bf16(dS[cc][8 * c4 + 0], dS[cc][8 * c4 + 1]);
-                            v.y = pack_bf16(dS[cc][8 * c4 + 2], dS[cc][8 * c4 + 3]);
-                            v.z = pack_bf16(dS[cc][8 * c4 + 4], dS[cc][8 * c4 + 5]);
-                            v.w = pack_bf16(dS[cc][8 * c4 + 6], dS[cc][8 * c4 + 7]);
-                        }
-                        *reinterpret_cast<uint4*>(tile + swz(r, (c & 1) * 4 + c4)) = v;
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b;
+                        unpack2(dS[4 * c4 + j], a, b);
+                        o[j] = pack_bf16(a, b);
                     }
+                    *reinterpret_cast<uint4*>(tile + (c >> 1) * kRegion + swz(r, (c & 1) * 4 + c4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
+#pragma unroll 1
+                for (int z = z0; z < q; z += zstep)
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+                        *reinterpret_cast<uint4*>(tile + (z >> 1) * kRegion + swz(r, (z & 1) * 4 + c4)) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(MB_DSREADY));
+                arrive(MB_DSREADY);
                 live = wt(MB_ACCDONE, n - 1, 105);
                 if (!live) break;
                 tc_fence_after();
-                // row r of dB and dC, columns [64 half, 64 half + 64): in full here, or one CTA's share
-                const long long unit = it / hg;
-                const int g = (int)(unit % G), bc = (int)(unit / G), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
-                const bool whole = unit * hg >= lo && (unit + 1) * hg <= hi;
-                const size_t row = (((size_t)bi * T + t0 + r) * G + g) * kN + half * 64;
-                float* part = p.part + (((size_t)blockIdx.x * 2 + (unit * hg < lo || unit * hg == lo ? 0 : 1)) * 2) * kBlk * kN +
-                              (size_t)r * kN + half * 64;
+                // row r of dB, dC by 32 columns, the quadrant's warps in turn: complete if all the
+                // group's heads were here, else the CTA's share.  Its first group's share lies in slot 0,
+                // a later one's in slot 1
+                const int g = i.h / hg, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
+                const bool whole = k - i.hh >= 0 && i.hh + 1 == hg;
+                const size_t row = (((size_t)bi * T + t0 + r) * G + g) * kN;
+                float* part = p.part + ((size_t)blockIdx.x * 2 + (k - i.hh > 0 ? 1 : 0)) * 2 * kBlk * kN + (size_t)r * kN;
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {  // dB, dC by 32 columns
+                for (int m = z0; m < 8; m += zstep) {
                     uint32_t raw[32];
-                    const int which = m >> 1, o = (m & 1) * 32;
-                    SSD_TMEM_LD32_WAIT(tmem + ((uint32_t)(q * 32) << 16) + (which ? kColC : kColB) + half * 64 + o, raw);
+                    const int which = m >> 2, o = (m & 3) * 32;
+                    SSD_TMEM_LD32_WAIT(lanes + (which ? kColC : kColB) + o, raw);
                     if (whole) {
                         if (t0 + r < T) {
                             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(which ? p.a.dC : p.a.dB) + row + o);
@@ -885,132 +651,380 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                     __syncwarp();
                 }
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(MB_UNITFREE));
+                arrive(MB_UNITFREE);
             }
         }
-    } else {
-        // ================================================================ row group
-        reg_dec<kRegsRow>();
-        const int q = warp & 3, r = q * 32 + lane;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    } else if (role == ROLE_ROW) {
+        const int r = q * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         bool live = __all_sync(0xffffffffu, !*s_abort);
-        for (long long it = lo; it < hi && live; ++it) {
-            const int k = (int)(it - lo), s = k & 1;
-            const int h = (int)(it % H);
+        float D_next = p.a.D[lo % H];
+        for (Walk i(lo, hi, H, hg); i.more() && live; i.next()) {
+            const int k = i.k, s = k & 1;
             live = wt(MB_FULLXY + s, k >> 1, 110) && (k < 1 || wt(MB_DBDONE, k - 1, 111));
             if (!live) break;
             const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
             const float er = terms[kTermE * kBlk + r], wr = terms[kTermW * kBlk + r], dtr = terms[kTermDt * kBlk + r];
-            const float Dh = p.a.D[h];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(MB_EMPTYT + s));
+            const float Dh = D_next;
+            D_next = p.a.D[i.next_head()];
+            arrive(MB_EMPTYT + s);
             uint8_t* xs = smem + kMX + s * kRegion;
             const uint8_t* ys = smem + kMY + s * kRegion;
-            auto weigh = [&](const uint8_t* src, float w) {
-#pragma unroll
+            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
+            float F = 0.f, E = 0.f;
+            // Two rounds of the same steps: the row of dY weighted with e, then V against x;
+            // the row of X weighted with w dt, then Y against dy.  V is replaced by w o V on the way.
+#pragma unroll 1
+            for (int round = 0; round < 2; ++round) {
+                if (round) live = wt(MB_DCDONE, k, 112);
+                if (!live) break;
+                const uint8_t* src = round ? xs : ys;
+                const float weight = round ? wr * dtr : er;
+                const f32x2 w2 = pack2(weight, weight);
+#pragma unroll 2
                 for (int c = 0; c < 8; ++c) {
                     const uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c));
-                    *reinterpret_cast<uint4*>(smem + kMW + swz(r, c)) =
-                        make_uint4(pack_bf16(w * bf_lo(v.x), w * bf_hi(v.x)), pack_bf16(w * bf_lo(v.y), w * bf_hi(v.y)),
-                                   pack_bf16(w * bf_lo(v.z), w * bf_hi(v.z)), pack_bf16(w * bf_lo(v.w), w * bf_hi(v.w)));
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b;
+                        unpack2(mul2(pack2(bf_lo(in[j]), bf_hi(in[j])), w2), a, b);
+                        o[j] = pack_bf16(a, b);
+                    }
+                    *reinterpret_cast<uint4*>(smem + kMW + swz(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 fence_proxy_async();
-                __syncwarp();
-            };
-            weigh(ys, er);
-            if (lane == 0) mbar_arrive(bar(MB_EYREADY));
-            // sum over 32 columns of a row of `src` times raw
-            auto dot = [&](const uint8_t* src, int c0, const uint32_t (&raw)[32]) {
-                float f = 0.f;
+                arrive(round ? MB_WXREADY : MB_EYREADY);
+                live = wt(round ? MB_YDONE : MB_VDONE, k, 113);
+                if (!live) break;
+                tc_fence_after();
+                const uint8_t* other = round ? ys : xs;
+                const uint32_t from = lanes + (round ? kColY : kColV);
+                const f32x2 wr2 = pack2(wr, wr);
+                f32x2 dot2 = 0ull;
+#pragma unroll 1
+                for (int o = 0; o < 4; ++o) {
+                    uint32_t raw[16];
+                    SSD_TMEM_LD16_WAIT(from + 16 * o, raw);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c0 + c));
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    for (int c = 0; c < 2; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(other + swz(r, 2 * o + c));
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f = fmaf(bf_lo(in[i]), __uint_as_float(raw[8 * c + 2 * i]), f);
-                        f = fmaf(bf_hi(in[i]), __uint_as_float(raw[8 * c + 2 * i + 1]), f);
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t &ra = raw[8 * c + 2 * j], &rb = raw[8 * c + 2 * j + 1];
+                            const f32x2 t = pack2(__uint_as_float(ra), __uint_as_float(rb));
+                            dot2 = fma2(pack2(bf_lo(in[j]), bf_hi(in[j])), t, dot2);
+                            float a, b;
+                            unpack2(mul2(t, wr2), a, b);
+                            ra = __float_as_uint(a), rb = __float_as_uint(b);
+                        }
                     }
+                    if (!round) SSD_TMEM_ST16_WAIT(from + 16 * o, raw);
                 }
-                return f;
-            };
-            // V: F_j / dt_j = w_j x_j . V_j, and w o V in its place
-            live = wt(MB_VDONE, k, 112);
-            if (!live) break;
-            tc_fence_after();
-            float F = 0.f, E = 0.f;
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                uint32_t raw[32];
-                SSD_TMEM_LD32_WAIT(lane_addr + kColV + 32 * o, raw);
-                F += dot(xs, 4 * o, raw);
-                uint32_t *ra = raw, *rb = raw + 16;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(wr * __uint_as_float(raw[i]));
-                SSD_TMEM_ST16x2_WAIT(lane_addr + kColV + 32 * o, ra, lane_addr + kColV + 32 * o + 16, rb);
+                tc_fence_before();
+                arrive(round ? MB_YFREE : MB_VSCALED);
+                float a, b;
+                unpack2(dot2, a, b);
+                if (round) E = a + b;  // E_i = e_i dy_i . Y_i
+                else F = a + b;        // F_j / dt_j = w_j x_j . V_j
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(MB_VSCALED));
-            // Y: E_i = e_i dy_i . Y_i
-            live = wt(MB_YDONE, k, 113);
+            live = live && (k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 115));
             if (!live) break;
-            tc_fence_after();
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                uint32_t raw[32];
-                SSD_TMEM_LD32_WAIT(lane_addr + kColY + 32 * o, raw);
-                E += dot(ys, 4 * o, raw);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(MB_YFREE));
-            live = wt(MB_DCDONE, k, 114);
-            if (!live) break;
-            weigh(xs, wr * dtr);
-            if (lane == 0) mbar_arrive(bar(MB_WXREADY));
-            live = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 115);
-            if (!live) break;
-            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
             sums[kSumE * kBlk + r] = er * E;
             sums[kSumF * kBlk + r] = wr * F;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(MB_SUMFULL + s));
-            // dx = dt U + D dy, over the thread's own row of X
+            arrive(MB_SUMFULL + s);
+            // dx = dt (U + S_jj dy) + D dy, over the thread's own row of X
             live = wt(MB_UDONE, k, 116);
             if (!live) break;
             tc_fence_after();
+            const float dyw = fmaf(dtr, sums[kSumSd * kBlk + r], Dh);
+            const f32x2 dy2 = pack2(dyw, dyw), dt2 = pack2(dtr, dtr);
+#pragma unroll 1
+            for (int o = 0; o < 4; ++o) {
+                uint32_t raw[16];
+                SSD_TMEM_LD16_WAIT(lanes + kColV + 16 * o, raw);
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                uint32_t raw[32];
-                SSD_TMEM_LD32_WAIT(lane_addr + kColV + 32 * o, raw);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(ys + swz(r, 4 * o + c));
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(ys + swz(r, 2 * o + c));
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                     uint32_t out[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        out[i] = pack_bf16(fmaf(dtr, __uint_as_float(raw[8 * c + 2 * i]), Dh * bf_lo(in[i])),
-                                           fmaf(dtr, __uint_as_float(raw[8 * c + 2 * i + 1]), Dh * bf_hi(in[i])));
-                    *reinterpret_cast<uint4*>(xs + swz(r, 4 * o + c)) = make_uint4(out[0], out[1], out[2], out[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x2 y2 = mul2(pack2(bf_lo(in[j]), bf_hi(in[j])), dy2);
+                        float a, b;
+                        unpack2(fma2(pack2(__uint_as_float(raw[8 * c + 2 * j]), __uint_as_float(raw[8 * c + 2 * j + 1])), dt2, y2), a, b);
+                        out[j] = pack_bf16(a, b);
+                    }
+                    *reinterpret_cast<uint4*>(xs + swz(r, 2 * o + c)) = make_uint4(out[0], out[1], out[2], out[3]);
                 }
             }
             fence_proxy_async();
             tc_fence_before();
-            __syncwarp();
+            arrive(MB_UFREE);
+            arrive(MB_DXSTAGED + s);
+            arrive(MB_EMPTYXY + s);
+        }
+    } else if (role == ROLE_PRODUCER) {
+        if (lane == 0 && !*s_abort && !p.starve) {
+            int nxy = 0, nst = 0, nbc = 0, n = 0;
+            for (Walk i(lo, hi, H, hg); i.more(); i.next()) {
+                const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
+                const size_t it = (size_t)(lo + k);
+                if (k >= 2 && !(w1(MB_EMPTYXY + s, (k - 2) >> 1, 60) && w1(MB_EMPTYT + s, (k - 2) >> 1, 61))) break;
+                const uint32_t f = bar(MB_FULLXY + s);
+                mbar_expect_tx(f, 2 * kRegion + kTermBytes);
+                tma_load_4d(sbase + kMX + s * kRegion, &p.tm_x, f, 0, h, t0, bi);
+                tma_load_4d(sbase + kMY + s * kRegion, &p.tm_dy, f, 0, h, t0, bi);
+                bulk_load(sbase + kMTerms + s * kTermBytes, p.terms + it * kTerms * kBlk, kTermBytes, f);
+                nxy = k + 1;
+                if (i.first()) {
+                    if (n > 0 && !w1(MB_UNITFREE, n - 1, 62)) break;
+                    const uint32_t fb = bar(MB_FULLBC);
+                    const int g = h / hg;
+                    mbar_expect_tx(fb, 4 * kRegion);
+                    tma_load_4d(sbase + kMB, &p.tm_B, fb, 0, g, t0, bi);
+                    tma_load_4d(sbase + kMB + kRegion, &p.tm_B, fb, 64, g, t0, bi);
+                    tma_load_4d(sbase + kMC, &p.tm_C, fb, 0, g, t0, bi);
+                    tma_load_4d(sbase + kMC + kRegion, &p.tm_C, fb, 64, g, t0, bi);
+                    nbc = ++n;
+                }
+                if (k >= 1 && !w1(MB_EMPTYST, k - 1, 63)) break;
+                const uint32_t fs = bar(MB_FULLST);
+                mbar_expect_tx(fs, 2 * kImage);
+                bulk_load(sbase + kMG, p.img_g + it * kImage, kImage, fs);
+                bulk_load(sbase + kMH, p.img_h + it * kImage, kImage, fs);
+                nst = k + 1;
+            }
+            // loads nobody may have waited for land before the CTA exits
+            for (int k = nxy - 2; k < nxy; ++k)
+                if (k >= 0) mbar_drain(bar(MB_FULLXY + (k & 1)), (k >> 1) & 1);
+            if (nst > 0) mbar_drain(bar(MB_FULLST), (nst - 1) & 1);
+            if (nbc > 0) mbar_drain(bar(MB_FULLBC), (nbc - 1) & 1);
+        }
+        __syncwarp();
+    } else if (role == ROLE_ISSUER) {
+        // One lane issues everything, with constant descriptor steps: an address formed per
+        // instruction measured 190 cycles a product step against 40.
+                    if (elect_one()) {
+                        constexpr uint32_t id_nn = idesc_bf16(128, 128, 0, 0);   // both K-major
+                        constexpr uint32_t id_st = idesc_bf16(128, 64, 0, 1);    // state or dY [K rows][64]: MN-major
+                        constexpr uint32_t id_db = idesc_bf16(128, 128, 0, 1);
+                        constexpr uint32_t id_dc = idesc_bf16(128, 128, 1, 1);
+                        // K-major operands step 16 elements along a row (32 bytes, regions of 64 columns),
+                        // MN-major ones 16 rows
+                        auto k_major = [](uint32_t a) { return sdesc(a, 16, 1024); };
+                        auto mn_major = [](uint32_t a) { return sdesc(a, kRegion, 1024); };
+                        auto koff = [](int kk) { return (uint32_t)((kk >> 2) * (kRegion >> 4) + (kk & 3) * 2); };
+                        constexpr uint32_t kRowStep = 128;
+                        const uint64_t kB = k_major(sbase + kMB), kC = k_major(sbase + kMC), kW = k_major(sbase + kMW);
+                        const uint64_t kX0 = k_major(sbase + kMX), kY0 = k_major(sbase + kMY), mY0 = mn_major(sbase + kMY);
+                        const uint64_t kH = k_major(sbase + kMH), kG = k_major(sbase + kMG);
+                        const uint64_t mH = mn_major(sbase + kMH), mG = mn_major(sbase + kMG);
+                        bool ok = !*s_abort;
+                        int n = -1;
+                        for (Walk i(lo, hi, H, hg); i.more() && ok; i.next()) {
+                            const int k = i.k, s = k & 1;
+                            const bool fresh = i.first();
+                            const uint32_t stage = s * (kRegion >> 4);
+                            // G^T's columns: U of the item before has read M^T there
+                            ok = k < 1 || w1(MB_UDONE, k - 1, 70);
+                            if (!ok) break;
+                            if (fresh) {
+                                ++n;
+                                ok = w1(MB_FULLBC, n, 71);
+                                if (!ok) break;
+                                tc_fence_after();
+        #pragma unroll
+                                for (int kk = 0; kk < kN / 16; ++kk)
+                                    mma_ss(tmem + kColG, kB + koff(kk), kC + koff(kk), id_nn, kk > 0);
+                                mma_commit(bar(MB_SFULL));
+                                ok = w1(MB_SREAD, n, 72);
+                                if (!ok) break;
+                            }
+                            ok = w1(MB_FULLXY + s, k >> 1, 73);
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < kP / 16; ++kk)
+                                mma_ss(tmem + kColG, kX0 + stage + kk * 2, kY0 + stage + kk * 2, id_nn, kk > 0);
+                            mma_commit(bar(MB_GFULL));
+                            // V = B dh^T, Y = C h^T, hi then lo
+                            ok = w1(MB_FULLST, k, 74) && (k < 1 || w1(MB_UFREE, k - 1, 75));
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < 2 * kN / 16; ++kk)
+                                mma_ss(tmem + kColV, kB + koff(kk & 7), mG + (kk >> 3) * (kRegion >> 4) + (kk & 7) * kRowStep, id_st, kk > 0);
+                            mma_commit(bar(MB_VDONE));
+                            ok = k < 1 || w1(MB_YFREE, k - 1, 76);
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < 2 * kN / 16; ++kk)
+                                mma_ss(tmem + kColY, kC + koff(kk & 7), mH + (kk >> 3) * (kRegion >> 4) + (kk & 7) * kRowStep, id_st, kk > 0);
+                            mma_commit(bar(MB_YDONE));
+                            // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
+                            ok = w1(MB_EYREADY, k, 77);
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < kP / 16; ++kk)
+                                mma_ss(tmem + kColC, kW + kk * 2, kH + kk * 2, id_nn, !fresh || kk > 0);
+                            mma_commit(bar(MB_DCDONE));
+                            ok = w1(MB_WXREADY, k, 78);
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < kP / 16; ++kk)
+                                mma_ss(tmem + kColB, kW + kk * 2, kG + kk * 2, id_nn, !fresh || kk > 0);
+                            mma_commit(bar(MB_DBDONE));
+                            mma_commit(bar(MB_EMPTYST));
+                            // U = w o V + M^T dY
+                            ok = w1(MB_VSCALED, k, 79) && w1(MB_MREADY, k, 80);
+                            if (!ok) break;
+                            tc_fence_after();
+        #pragma unroll
+                            for (int kk = 0; kk < kBlk / 16; ++kk)
+                                mma_ts(tmem + kColV, tmem + kColG + (kk >> 1) * 32 + (kk & 1) * 8, mY0 + stage + kk * kRowStep, id_st, 1);
+                            mma_commit(bar(MB_UDONE));
+                            if (i.last()) {  // dB += dS^T C, dC += dS B
+                                ok = w1(MB_DSREADY, n, 81);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint64_t mB = mn_major(sbase + kMB), mC = mn_major(sbase + kMC);
+        #pragma unroll
+                                for (int kk = 0; kk < kBlk / 16; ++kk)
+                                    mma_ss(tmem + kColB, kH + koff(kk), mC + kk * kRowStep, id_db, 1);
+        #pragma unroll
+                                for (int kk = 0; kk < kBlk / 16; ++kk)
+                                    mma_ss(tmem + kColC, mH + kk * kRowStep, mB + kk * kRowStep, id_dc, 1);
+                                mma_commit(bar(MB_ACCDONE));
+                            }
+                        }
+                        mma_commit(bar(MB_DONE));
+                        mbar_drain(bar(MB_DONE), 0);
+                    }
+        __syncwarp();
+    } else if (role == ROLE_DDT) {
+        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        float A_next = p.a.A[lo % H];
+        for (Walk i(lo, hi, H, hg); i.more() && ok; i.next()) {
+            const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
+            ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
+            if (!ok) break;
+            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes) + lane;
+            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + lane;
+            // da_t adds a prefix of F (exclusive) and a suffix of E + rows - columns; 32 tokens a step
+            const float zz = s_z[s] * (terms - lane)[kTermE * kBlk + kBlk - 1];
+            const float Ah = A_next;
+            A_next = p.a.A[i.next_head()];
+            float sA = 0.f, sD = 0.f, sb = 0.f, carry = 0.f;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                const int t = 32 * g;
+                const float f = sums[kSumF * kBlk + t] * terms[kTermDt * kBlk + t];
+                float v = f;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float a = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += a;
+                }
+                float row = sums[kSumE * kBlk + t];
+#pragma unroll 1
+                for (int j = 0; j <= g; ++j) row += sums[(kSumRow + j) * kBlk + t];
+                sums[kSumE * kBlk + t] = row;
+                sums[kSumRow * kBlk + t] = carry + v - f;  // the prefix, in a place its token has done with
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+            carry = zz;
+            size_t o = ((size_t)bi * T + t0 + 96 + lane) * H + h;
+#pragma unroll 1
+            for (int g = 3; g >= 0; --g) {
+                const int t = 32 * g;
+                const float dt = terms[kTermDt * kBlk + t];
+                float col = 0.f;
+#pragma unroll 1
+                for (int j = g; j < 4; ++j) col += sums[(kSumCol + j) * kBlk + t];
+                float v = fmaf(-col, dt, sums[kSumE * kBlk + t]);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float a = __shfl_down_sync(0xffffffffu, v, o);
+                    if (lane + o < 32) v += a;
+                }
+                const float da = carry + v + sums[kSumRow * kBlk + t];
+                carry += __shfl_sync(0xffffffffu, v, 0);
+                const float gd = sums[kSumGd * kBlk + t];
+                const float ddt = fmaf(Ah, da, fmaf(gd, sums[kSumSd * kBlk + t], col + sums[kSumF * kBlk + t])) *
+                                  terms[kTermSlope * kBlk + t];
+                sD += gd;
+                if (t0 + t + lane < T) {
+                    p.a.ddt[o] = ddt;
+                    sA = fmaf(dt, da, sA);
+                    sb += ddt;
+                }
+                o -= (size_t)32 * H;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sA += __shfl_xor_sync(0xffffffffu, sA, o);
+                sD += __shfl_xor_sync(0xffffffffu, sD, o);
+                sb += __shfl_xor_sync(0xffffffffu, sb, o);
+            }
             if (lane == 0) {
-                mbar_arrive(bar(MB_UFREE));
-                mbar_arrive(bar(MB_DXSTAGED + s));
+                p.pA[lo + k] = sA;
+                p.pD[lo + k] = sD;
+                if (p.pb) p.pb[lo + k] = sb;
+            }
+            arrive(MB_SUMEMPTY + s);
+            arrive(MB_EMPTYT + s);
+            ok = wt(MB_DXSTAGED + s, k >> 1, 92);
+            if (!ok) break;
+            if (lane == 0) {
+                tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, h, t0, bi);
+                bulk_commit();
+                bulk_wait_read0();
                 mbar_arrive(bar(MB_EMPTYXY + s));
             }
+            __syncwarp();
+        }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
+    } else {
+        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        for (int k = 0; k < hi - lo && ok; ++k) {
+            const int s = k & 1;
+            ok = wt(MB_FULLST, k, 95);
+            if (!ok) break;
+            const uint4 *h4 = reinterpret_cast<const uint4*>(smem + kMH), *g4 = reinterpret_cast<const uint4*>(smem + kMG);
+            f32x2 z2 = 0ull;
+#pragma unroll 2
+            for (int i = lane; i < (int)(kRegion / 16); i += 32) {
+                const uint4 a = h4[i], al = h4[i + kRegion / 16], b = g4[i], bl = g4[i + kRegion / 16];
+                const uint32_t ah[4] = {a.x, a.y, a.z, a.w}, ao[4] = {al.x, al.y, al.z, al.w};
+                const uint32_t bh[4] = {b.x, b.y, b.z, b.w}, bo[4] = {bl.x, bl.y, bl.z, bl.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    z2 = fma2(add2(pack2(bf_lo(ah[j]), bf_hi(ah[j])), pack2(bf_lo(ao[j]), bf_hi(ao[j]))),
+                              add2(pack2(bf_lo(bh[j]), bf_hi(bh[j])), pack2(bf_lo(bo[j]), bf_hi(bo[j]))), z2);
+            }
+            arrive(MB_EMPTYST);
+            float z, z1;
+            unpack2(z2, z, z1);
+            z += z1;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+            ok = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 96);
+            if (!ok) break;
+            if (lane == 0) s_z[s] = z;
+            arrive(MB_SUMFULL + s);
         }
     }
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (warp == 1 && tmem != kTmemSentinel) {
+    if (role == ROLE_ISSUER && tmem != kTmemSentinel) {
         tc_fence_after();
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -1110,13 +1124,6 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     if ((st = make_map(&p.tm_dx, a.dx, kP, a.H, a.T, a.b)) != SSD_OK) return st;
     if ((st = smem_limit_once((const void*)ssd_bwd_tc_state_kernel, (int)kSSmem)) != SSD_OK) return st;
     if ((st = smem_limit_once((const void*)ssd_bwd_tc_main_kernel, (int)kMSmem)) != SSD_OK) return st;
-    // the main pass waits for registers its warps give up: what it is launched with must cover them
-    static const int main_regs = [] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, (const void*)ssd_bwd_tc_main_kernel) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (main_regs < kRegsLaunch)
-        return set_error(SSD_ERR_INTERNAL, "main pass built with %d registers a thread, its split needs %d", main_regs, kRegsLaunch);
     {
         LaunchScope ls("ssd_bwd_tc_terms", s);
         ssd_bwd_tc_terms_kernel<<<dim3(a.b * p.nc, (a.H + 7) / 8), kTermThreads, 0, s>>>(p);

@@ -65,17 +65,9 @@ __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
 // next grid in the stream start before this one ends.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// The waits' out-of-line copies keep the hot code small.  A translation unit whose kernels move
-// registers between warps (setmaxnreg) defines SSD_TC_INLINE_WAITS: with a call in the kernel the
-// compiler holds every warp to the launch's register count.
-#ifdef SSD_TC_INLINE_WAITS
-#define SSD_TC_WAIT_CALL __forceinline__
-#else
-#define SSD_TC_WAIT_CALL __noinline__
-#endif
 // Records a failure in the status word (the first one wins).  The word is cleared by the
 // grid that runs ahead of every prefill, so the write waits until that grid is done.
-__device__ SSD_TC_WAIT_CALL void report_status(int* status, int code) {
+__device__ __noinline__ void report_status(int* status, int code) {
     griddep_wait();
     atomicCAS(status, 0, code);
 }
@@ -84,7 +76,7 @@ __device__ SSD_TC_WAIT_CALL void report_status(int* status, int code) {
 // other role give up) if the CTA is aborting or the limit expires.  The first test is
 // inline; the waiting loop is one out-of-line copy shared by every call site, which keeps
 // the kernel's hot code small (instruction fetch, not arithmetic, bounds the busy warps).
-__device__ SSD_TC_WAIT_CALL bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
                                             int where) {
     const unsigned long long t0 = globaltimer();
     while (true) {
@@ -225,6 +217,58 @@ __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
         : "memory");
 }
+// One-thread variants: a warp that only issues (its waits included) runs on one elected lane, the
+// same one for all its tcgen05 instructions.  The whole-warp forms above measure about 65 cycles
+// an instruction in a rolled loop, these about 47 (128 x 64 x 16; its operands alone take 48
+// cycles of shared-memory bandwidth).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Two fp32 values in one 64-bit register: sm_100's packed adds, multiplies and fused
+// multiply-adds do both in one instruction, each rounded as its scalar form.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 // TMEM <-> register moves.  tcgen05.ld/st/wait are .sync.aligned: the whole warp must
 // execute them converged, so each macro first reconverges the warp (a store by a few
 // lanes or a lane-dependent select ahead of a move may otherwise leave it split).
@@ -247,6 +291,27 @@ __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
           "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), \
           "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), \
           "=r"(r[29]), "=r"(r[30]), "=r"(r[31]) \
+        : "r"(taddr) \
+        : "memory"); \
+    } while (0)
+#define SSD_TMEM_LD8_WAIT(taddr, r) \
+    do { \
+    __syncwarp(); \
+    asm volatile( \
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t" \
+        "tcgen05.wait::ld.sync.aligned;" \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) \
+        : "r"(taddr) \
+        : "memory"); \
+    } while (0)
+#define SSD_TMEM_LD16_WAIT(taddr, r) \
+    do { \
+    __syncwarp(); \
+    asm volatile( \
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t" \
+        "tcgen05.wait::ld.sync.aligned;" \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), \
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) \
         : "r"(taddr) \
         : "memory"); \
     } while (0)
@@ -289,14 +354,14 @@ __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
         : "r"(ta), kind(off) \
         : "memory"); \
     } while (0)
-#define SSD_TMEM_ST8_WAIT(ta, ra) \
+#define SSD_TMEM_ST4_WAIT(ta, ra) \
     do { \
     __syncwarp(); \
     asm volatile( \
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t" \
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t" \
         "tcgen05.wait::st.sync.aligned;" \
         : \
-        : "r"(ta), "r"(ra[0]), "r"(ra[1]), "r"(ra[2]), "r"(ra[3]), "r"(ra[4]), "r"(ra[5]), "r"(ra[6]), "r"(ra[7]) \
+        : "r"(ta), "r"(ra[0]), "r"(ra[1]), "r"(ra[2]), "r"(ra[3]) \
         : "memory"); \
     } while (0)
 #define SSD_TMEM_ST16_WAIT(ta, ra) \
