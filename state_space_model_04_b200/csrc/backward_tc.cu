@@ -55,6 +55,10 @@ struct BwdTc {
     BwdArgs a;
     int nc;                 // chunks a sequence
     int ctas;               // of the main pass
+    int nseg, cseg;         // the state pass's segments a sequence, chunks a segment
+    float* seg_end;         // [b H][2 directions][nseg - 1][P][N] end states of segments run from zero (the first
+                            // from the initial state)
+    float* seg_decay;       // [b H][2][nseg - 1] their whole decay
     long long items;        // b nc H
     float* terms;           // [items][kTerms][128]
     uint8_t* img_h;         // [items][kImage] state entering the chunk
@@ -66,10 +70,6 @@ struct BwdTc {
     int starve;
 };
 
-__device__ __forceinline__ void split_bf16(float v, float& hi, float& lo) {
-    hi = __bfloat162float(__float2bfloat16_rn(v));
-    lo = v - hi;
-}
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -120,62 +120,70 @@ __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __
 
 // ------------------------------------------------------------------ state pass
 //   warp 0      TMA producer: X (or dY) and the two boxes of B (or C) of a chunk, 2-slot ring
-//   warp 1      TMEM owner and MMA issuer: D[n][p] = B^T (wX)_hi + B^T (wX)_lo
-//   warps 2-9   weight the rows of the chunk ahead into hi and lo tiles, write the state's halves,
-//               then h <- exp(cs_last) h + D
-constexpr int kSWork = 256;
-constexpr int kSThreads = 64 + kSWork;
+//   warp 1      TMEM owner and MMA issuer: D[n][hi p | lo p] = B^T [wX_hi | wX_lo], one product of
+//               N = 128 (the halves in products of their own would read B from shared memory twice)
+//   warps 2-5   one token row a thread: weighted into hi and lo tiles, a chunk ahead
+//   warps 6-9   one state row n a thread, 64 fp32 entries in registers: stores the entering state's
+//               halves, then h <- exp(cs_last) h + D_hi + D_lo.  A warp's 32 rows are a contiguous
+//               piece of the image, so it stores them on its own
+// A sequence may be cut into segments of whole chunks to fill the SMs: the ends kernel runs all but
+// the last segment from zero for their end states, and the state kernel's segments start from the
+// fold of the ends before them.
+constexpr int kSThreads = 320;
 constexpr uint32_t kSSlot = 3 * kRegion;            // X, B (n 0..63), B (n 64..127)
 constexpr uint32_t kSXs = 2 * kSSlot;               // [2] hi, lo tiles of the weighted rows
 constexpr uint32_t kSImg = kSXs + 2 * kImage;       // [2] state images
 constexpr uint32_t kSSmall = kSImg + 2 * kImage;
 constexpr uint32_t kSSmem = kSSmall + 256;
 static_assert(kSSmem <= 232448 - 1024, "state pass shared memory");
-enum { SB_FULL = 0, SB_EMPTY = 2, SB_XS = 4, SB_ACC = 6, SB_FREE = 7, SB_DONE = 8, SB_COUNT };
+constexpr uint32_t kSCols = 256;                    // two accumulators of 128 columns
+enum { SB_FULL = 0, SB_EMPTY = 2, SB_XS = 4, SB_ACC = 6, SB_ACCFREE = 8, SB_DONE = 10, SB_COUNT };
 
-__device__ __forceinline__ void work_bar() {
-    __syncwarp();
-    asm volatile("bar.sync 1, %0;" ::"n"(kSWork) : "memory");
-}
-
+template <bool kEnds>
 __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __grid_constant__ BwdTc p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int H = p.a.H, nc = p.nc;
-    const int u = blockIdx.x, dir = blockIdx.y, h = u % H, bi = u / H, g = h / (H / p.a.G);
+    const int segs = kEnds ? p.nseg - 1 : p.nseg;
+    const int u = blockIdx.x / segs, seg = blockIdx.x % segs, dir = blockIdx.y;
+    const int h = u % H, bi = u / H, g = h / (H / p.a.G);
+    // this CTA's chunks in walking order: [c0, c0 + n)
+    const int c0 = seg * p.cseg, n = min(p.cseg, nc - c0);
+    auto chunk = [&](int k) { return dir ? nc - 1 - c0 - k : c0 + k; };
     uint8_t* small = smem + kSSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
     volatile int* s_abort = reinterpret_cast<volatile int*>(small + 128);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 144);
-    volatile int* s_stop = reinterpret_cast<volatile int*>(small + 160);
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    auto chunk = [&](int k) { return dir ? nc - 1 - k : k; };  // the k-th chunk walked
+    auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity & 1, s_abort, p.status, where); };
+    auto w1 = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity & 1, s_abort, p.status, where); };
 
     if (threadIdx.x == 0) {
         const bool misaligned = (sbase & 1023u) != 0;
         if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (5 << 8));
         for (int i = 0; i < SB_COUNT; ++i)
-            mbar_init(bar(i), i == SB_XS || i == SB_XS + 1 || i == SB_FREE ? kSWork / 32 : 1);
+            mbar_init(bar(i), i == SB_XS || i == SB_XS + 1 || i == SB_ACCFREE || i == SB_ACCFREE + 1 ? 4 : 1);
         *s_abort = misaligned ? 1 : 0;
-        s_stop[0] = s_stop[1] = 0;
         s_wait_ns = p.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, 64, warp == 1), 0);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, kSCols, warp == 1), 0);
     if (tmem == kTmemSentinel) {
         *s_abort = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (6 << 8));
     }
-    // the last chunk's product is only needed for the adjoint of the initial state
-    const int products = dir && p.a.dh0 ? nc : nc - 1;
+    // the product of the sequence's last chunk walked only feeds the adjoint of the initial state
+    const bool final = !kEnds && c0 + n == nc;
+    const int products = final && !(dir && p.a.dh0) ? n - 1 : n;
 
     if (warp == 0) {
         if (lane == 0 && !*s_abort && !p.starve) {
             int issued = 0;
+#pragma unroll 1
             for (int k = 0; k < products; ++k) {
                 const int s = k & 1;
-                if (k >= 2 && !mbar_wait(bar(SB_EMPTY + s), ((k - 2) >> 1) & 1, s_abort, p.status, 50)) break;
+                if (k >= 2 && !w1(SB_EMPTY + s, (k - 2) >> 1, 50)) break;
                 const uint32_t f = bar(SB_FULL + s), slot = sbase + s * kSSlot;
                 const int t0 = chunk(k) * kBlk;
                 mbar_expect_tx(f, kSSlot);
@@ -187,132 +195,171 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             for (int k = issued - 2; k < issued; ++k)
                 if (k >= 0) mbar_drain(bar(SB_FULL + (k & 1)), (k >> 1) & 1);
         }
+        __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-        constexpr uint32_t id = idesc_bf16(128, 64, 1, 1);
-        auto wt = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity, s_abort, p.status, where); };
-        bool ok = !*s_abort;
-        for (int k = 0; k < products && ok; ++k) {
-            const int s = k & 1;
-            ok = wt(SB_FULL + s, (k >> 1) & 1, 51) && wt(SB_XS + s, (k >> 1) & 1, 52) &&
-                 (k < 1 || wt(SB_FREE, (k - 1) & 1, 53));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dA = sdesc(sbase + s * kSSlot + kRegion, kRegion, 1024);
+            constexpr uint32_t id = idesc_bf16(128, 128, 1, 1);
+            const uint64_t mB = sdesc(sbase + kRegion, kRegion, 1024), mX = sdesc(sbase + kSXs, kRegion, 1024);
+            bool ok = !*s_abort;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const uint64_t dX = sdesc(sbase + kSXs + s * kImage + half * kRegion, kRegion, 1024);
-#pragma unroll 1
-                for (int kk = 0; kk < kBlk / 16; ++kk)
-                    mma_ss(tmem, dA + kk * 128, dX + kk * 128, id, half > 0 || kk > 0);
+            for (int k = 0; k < products && ok; ++k) {
+                const int s = k & 1;
+                ok = w1(SB_FULL + s, k >> 1, 51) && w1(SB_XS + s, k >> 1, 52) &&
+                     (k < 2 || w1(SB_ACCFREE + s, (k - 2) >> 1, 53));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t a = mB + s * (kSSlot >> 4), b = mX + s * (kImage >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kBlk / 16; ++kk) mma_ss(tmem + s * 128, a + kk * 128, b + kk * 128, id, kk > 0);
+                mma_commit(bar(SB_EMPTY + s));
+                mma_commit(bar(SB_ACC + s));
             }
-            mma_commit(bar(SB_EMPTY + s));
-            mma_commit(bar(SB_ACC));
-        }
-        mma_commit(bar(SB_DONE));
-        mbar_drain(bar(SB_DONE), 0);
+            mma_commit(bar(SB_DONE));
+            mbar_drain(bar(SB_DONE), 0);
         }
         __syncwarp();
-    } else {
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        const int r = q * 32 + lane;  // token row of a chunk, and state row n
-        const int p0 = half * 32;
-        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + p0;
-        const float* init = dir ? p.a.dhf : p.a.h0;
-        float st[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) st[i] = init ? init[(size_t)u * kP * kN + (size_t)(p0 + i) * kN + r] : 0.f;
-        auto item = [&](int k) { return ((size_t)bi * nc + chunk(k)) * H + h; };
-        // weight of the thread's row, and the chunk's decay, fetched a chunk ahead of their use
-        auto load_w = [&](int k) {
+    } else if (warp < 6) {
+        const int r = (warp - 2) * 32 + lane;  // token
+        const float* tm = p.terms + ((size_t)bi * nc * H + h) * kTerms * kBlk + r;
+        auto weight = [&](int k) {
             if (k >= products) return 0.f;
-            const float* t = p.terms + item(k) * kTerms * kBlk + r;
+            const float* t = tm + (size_t)chunk(k) * H * kTerms * kBlk;
             return dir ? t[kTermE * kBlk] : t[kTermW * kBlk] * t[kTermDt * kBlk];
         };
-        auto load_gam = [&](int k) { return k < nc ? p.terms[(item(k) * kTerms + kTermE) * kBlk + kBlk - 1] : 0.f; };
-        float w_next = load_w(0), gam = load_gam(0);
+        float next = weight(0);
         bool live = __all_sync(0xffffffffu, !*s_abort);
-        auto weigh = [&](int k) {  // rows of chunk k, weighted, into the hi and lo tiles
-            const float w = w_next;
-            w_next = load_w(k + 1);
-            if (!warp_wait(bar(SB_FULL + (k & 1)), (k >> 1) & 1, s_abort, p.status, 54)) return false;
-            const uint8_t* src = smem + (k & 1) * kSSlot;
-            uint8_t* dst = smem + kSXs + (k & 1) * kImage;
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-                const uint32_t o = swz(r, half * 4 + c4);
+#pragma unroll 1
+        for (int k = 0; k < products && live; ++k) {
+            const int s = k & 1;
+            const f32x2 w2 = pack2(next, next), minus = pack2(-1.f, -1.f);
+            next = weight(k + 1);
+            live = (k < 2 || wt(SB_EMPTY + s, (k - 2) >> 1, 54)) && wt(SB_FULL + s, k >> 1, 55);
+            if (!live) break;
+            const uint8_t* src = smem + s * kSSlot;
+            uint8_t* dst = smem + kSXs + s * kImage;
+#pragma unroll 2
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t o = swz(r, c);
                 const uint4 v = *reinterpret_cast<const uint4*>(src + o);
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float a, b, al, bl;
-                    split_bf16(w * bf_lo(in[i]), a, al);
-                    split_bf16(w * bf_hi(in[i]), b, bl);
-                    hi[i] = pack_bf16(a, b);
-                    lo[i] = pack_bf16(al, bl);
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2 t = mul2(pack2(bf_lo(in[j]), bf_hi(in[j])), w2);
+                    float a, b;
+                    unpack2(t, a, b);
+                    hi[j] = pack_bf16(a, b);
+                    unpack2(fma2(pack2(bf_lo(hi[j]), bf_hi(hi[j])), minus, t), a, b);
+                    lo[j] = pack_bf16(a, b);
                 }
                 *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(dst + kRegion + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SB_XS + (k & 1)));
-            return true;
-        };
-        if (live && products > 0) live = weigh(0);
-        uint8_t* images = dir ? p.img_g : p.img_h;
-        for (int k = 0; k < nc; ++k) {
-            // the state as two bf16 halves, image buffer k & 1 (its last store has been read);
-            // a warp that gave up tells the others at the barrier, so all leave together
-            if (!live || *s_abort) s_stop[k & 1] = 1;
-            if (threadIdx.x == 64) bulk_wait_read1();
-            work_bar();
-            if (s_stop[k & 1]) break;
-            uint8_t* img = smem + kSImg + (k & 1) * kImage;
+            if (lane == 0) mbar_arrive(bar(SB_XS + s));
+        }
+    } else {
+        const int q = warp & 3, r = q * 32 + lane;  // state row n
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const size_t un = (size_t)u * 2 + dir;      // (sequence, head, direction)
+        const float* init = dir ? p.a.dhf : p.a.h0;
+        f32x2 st[32];
+        if (init && seg == 0) {
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-                uint32_t hi[4], lo[4];
+            for (int i = 0; i < 32; ++i)
+                st[i] = pack2(init[(size_t)u * kP * kN + (size_t)(2 * i) * kN + r], init[(size_t)u * kP * kN + (size_t)(2 * i + 1) * kN + r]);
+        } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float a, b, al, bl;
-                    split_bf16(st[8 * c4 + 2 * i], a, al);
-                    split_bf16(st[8 * c4 + 2 * i + 1], b, bl);
-                    hi[i] = pack_bf16(a, b);
-                    lo[i] = pack_bf16(al, bl);
-                }
-                const uint32_t o = swz(r, half * 4 + c4);
-                *reinterpret_cast<uint4*>(img + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(img + kRegion + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-            fence_proxy_async();
-            work_bar();
-            if (threadIdx.x == 64) {
-                bulk_store(images + item(k) * kImage, smem_u32(img), kImage);
-                bulk_commit();
-            }
-            // rows of the next chunk: the tiles' last reader, the product of chunk k - 1, is done
-            if (live && k + 1 < products) live = weigh(k + 1);
-            if (live && k < products) {
-                live = warp_wait(bar(SB_ACC), k & 1, s_abort, p.status, 55);
-                if (live) {
-                    tc_fence_after();
-                    uint32_t raw[32];
-                    SSD_TMEM_LD32_WAIT(acc, raw);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(SB_FREE));
+            for (int i = 0; i < 32; ++i) st[i] = 0ull;
+        }
+        const float* gp = p.terms + (((size_t)bi * nc * H + h) * kTerms + kTermE) * kBlk + kBlk - 1;
+        auto decay = [&](int k) { return k < n ? gp[(size_t)chunk(k) * H * kTerms * kBlk] : 0.f; };
+        if constexpr (!kEnds) {
+            // the ends of the segments before, in order; the first already starts from the initial state
+#pragma unroll 1
+            for (int s = 0; s < seg; ++s) {
+                const float* e = p.seg_end + (un * (p.nseg - 1) + s) * kP * kN + r;
+                const float d = s ? p.seg_decay[un * (p.nseg - 1) + s] : 0.f;
+                const f32x2 d2 = pack2(d, d);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) st[i] = fmaf(gam, st[i], __uint_as_float(raw[i]));
-                    gam = load_gam(k + 1);
-                }
+                for (int i = 0; i < 32; ++i)
+                    st[i] = fma2(d2, s ? st[i] : 0ull, pack2(e[(size_t)(2 * i) * kN], e[(size_t)(2 * i + 1) * kN]));
             }
         }
-        if (live && !*s_abort && dir && p.a.dh0) {
+        float next = decay(0), total = 1.f;
+        uint8_t* images = (dir ? p.img_g : p.img_h) + ((size_t)bi * nc * H + h) * kImage;
+        bool live = __all_sync(0xffffffffu, !*s_abort);
+#pragma unroll 1
+        for (int k = 0; k < n && live; ++k) {
+            const int s = k & 1;
+            const float gam = next;
+            next = decay(k + 1);
+            total *= gam;
+            if constexpr (!kEnds) {
+                // the state as two bf16 halves; the warp's store of two chunks ago has read the buffer
+                uint8_t* img = smem + kSImg + s * kImage;
+                if (lane == 0) bulk_wait_read1();
+                __syncwarp();
+                const f32x2 minus = pack2(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) p.a.dh0[(size_t)u * kP * kN + (size_t)(p0 + i) * kN + r] = st[i];
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b;
+                        unpack2(st[4 * c + j], a, b);
+                        hi[j] = pack_bf16(a, b);
+                        unpack2(fma2(pack2(bf_lo(hi[j]), bf_hi(hi[j])), minus, st[4 * c + j]), a, b);
+                        lo[j] = pack_bf16(a, b);
+                    }
+                    *reinterpret_cast<uint4*>(img + swz(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(img + kRegion + swz(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    uint8_t* dst = images + (size_t)chunk(k) * H * kImage + q * 4096;
+                    const uint32_t from = smem_u32(img) + q * 4096;
+                    bulk_store(dst, from, 4096);
+                    bulk_store(dst + kRegion, from + kRegion, 4096);
+                    bulk_commit();
+                }
+            }
+            if (k < products) {
+                live = wt(SB_ACC + s, k >> 1, 56);
+                if (!live) break;
+                tc_fence_after();
+                const f32x2 g2 = pack2(gam, gam);
+#pragma unroll
+                for (int o = 0; o < 4; ++o) {
+                    uint32_t hi[16], lo[16];
+                    SSD_TMEM_LD16x2_WAIT(lanes + s * 128 + 16 * o, 64, hi, lo);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        st[8 * o + j] = fma2(g2, st[8 * o + j],
+                                             add2(pack2(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1])),
+                                                  pack2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]))));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SB_ACCFREE + s));
+            }
         }
-        if (threadIdx.x == 64) bulk_wait0();  // the stores are complete before the shared memory goes away
+        float* out = kEnds ? p.seg_end + (un * (p.nseg - 1) + seg) * kP * kN : final && dir ? p.a.dh0 : nullptr;
+        if (live && !*s_abort && out) {
+            if (!kEnds) out += (size_t)u * kP * kN;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                float a, b;
+                unpack2(st[i], a, b);
+                out[(size_t)(2 * i) * kN + r] = a;
+                out[(size_t)(2 * i + 1) * kN + r] = b;
+            }
+            if (kEnds && r == 0) p.seg_decay[un * (p.nseg - 1) + seg] = total;
+        }
+        if (lane == 0) bulk_wait0();  // the stores are complete before the shared memory goes away
+        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
@@ -320,7 +367,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
     if (warp == 1 && tmem != kTmemSentinel) {
         tc_fence_after();
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(64));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSCols));
     }
 }
 
@@ -582,15 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
 #pragma unroll 1
                 for (int z = z0; z < q; z += zstep) SSD_TMEM_ST16_WAIT(lanes + kColG + z * 32, zero);
             }
+            if (diagonal) {  // ahead of M^T: the row warps read S_jj once U, which waits for it, is done
+                sums[kSumSd * kBlk + r] = sd;
+                sums[kSumGd * kBlk + r] = gd;
+            }
             tc_fence_before();
             arrive(MB_MREADY);
             float ca, cb;
             unpack2(col2, ca, cb);
             sums[(kSumCol + c) * kBlk + r] = ca + cb;
-            if (diagonal) {
-                sums[kSumSd * kBlk + r] = sd;
-                sums[kSumGd * kBlk + r] = gd;
-            }
             arrive(MB_SUMFULL + s);
             arrive(MB_EMPTYT + s);
             if (i.last()) {
@@ -939,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 carry += __shfl_sync(0xffffffffu, v, 31);
             }
             carry = zz;
-            size_t o = ((size_t)bi * T + t0 + 96 + lane) * H + h;
+            size_t at = ((size_t)bi * T + t0 + 96 + lane) * H + h;
 #pragma unroll 1
             for (int g = 3; g >= 0; --g) {
                 const int t = 32 * g;
@@ -960,11 +1007,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                                   terms[kTermSlope * kBlk + t];
                 sD += gd;
                 if (t0 + t + lane < T) {
-                    p.a.ddt[o] = ddt;
+                    p.a.ddt[at] = ddt;
                     sA = fmaf(dt, da, sA);
                     sb += ddt;
                 }
-                o -= (size_t)32 * H;
+                at -= (size_t)32 * H;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -1032,10 +1079,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ dB, dC of split groups
-// One block per (chunk, group); a group whose heads lie in one CTA has been stored already.
-constexpr int kJoinThreads = 256;
+// kJoinSplit blocks per (chunk, group); a group whose heads lie in one CTA has been stored already.
+constexpr int kJoinThreads = 256, kJoinSplit = 16;
 __global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __grid_constant__ BwdTc p) {
-    const long long unit = blockIdx.x, hg = p.a.H / p.a.G, it0 = unit * hg, it1 = it0 + hg;
+    const long long unit = blockIdx.x / kJoinSplit, hg = p.a.H / p.a.G, it0 = unit * hg, it1 = it0 + hg;
     // CTA x holds items [items x / ctas, items (x + 1) / ctas): the CTA of an item by that rule
     auto owner = [&](long long it) {
         long long x = it * p.ctas / p.items;
@@ -1047,10 +1094,14 @@ __global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __g
     if (x0 == x1) return;
     const int g = (int)(unit % p.a.G), bc = (int)(unit / p.a.G), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
     const int rows = min(kBlk, p.a.T - t0);
-    for (int i = threadIdx.x; i < 2 * kBlk * kN / 4; i += kJoinThreads) {
+    constexpr int kPart = 2 * kBlk * kN / 4 / kJoinSplit;  // vectors of 4 a block
+    const int from = (int)(blockIdx.x % kJoinSplit) * kPart;
+#pragma unroll
+    for (int i = from + threadIdx.x; i < from + kPart; i += kJoinThreads) {
         const int which = i / (kBlk * kN / 4), e = (i % (kBlk * kN / 4)) * 4, r = e / kN, c = e % kN;
         if (r >= rows) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (long long x = x0; x <= x1; ++x) {
             // a CTA's first group sits in its slot 0, a later one (its last) in slot 1
             const int slot = it0 <= p.items * x / p.ctas ? 0 : 1;
@@ -1071,6 +1122,23 @@ int tc_sm_count() {
     return n;
 }
 
+// Segments of the state pass.  A CTA walks its chunks one after another, so a pass costs about
+// waves x (chunks a CTA + a start of two chunks' time).  More segments mean fewer chunks a CTA, but
+// the ends kernel then walks all but the last once more (without the stores: measured 0.8 of a
+// chunk's time), and each fold of an end costs about a quarter of a chunk.  The cheapest count wins.
+void plan_segments(int b, int H, int nc, int* nseg, int* cseg) {
+    const double sms = tc_sm_count(), units = 2.0 * b * H;
+    double best = 0.0;
+    *nseg = 1, *cseg = nc;
+    for (int n = 1; n <= std::min(nc, 64); ++n) {
+        const int len = (nc + n - 1) / n, m = (nc + len - 1) / len;
+        if (m != n) continue;
+        double cost = std::ceil(units * n / sms) * (len + 2.0);
+        if (n > 1) cost += std::ceil(units * (n - 1) / sms) * (0.8 * len + 2.0) + 0.25 * (n - 1) + 2.0;
+        if (n == 1 || cost < best) best = cost, *nseg = n, *cseg = len;
+    }
+}
+
 size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
     p->a = a;
     p->nc = (a.T + kBlk - 1) / kBlk;
@@ -1086,6 +1154,10 @@ size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
     p->terms = reinterpret_cast<float*>(take(n * kTermBytes));
     p->img_h = reinterpret_cast<uint8_t*>(take(n * kImage));
     p->img_g = reinterpret_cast<uint8_t*>(take(n * kImage));
+    plan_segments(a.b, a.H, p->nc, &p->nseg, &p->cseg);
+    const size_t ends = (size_t)a.b * a.H * 2 * (p->nseg - 1);
+    p->seg_end = reinterpret_cast<float*>(take(ends * kP * kN * 4));
+    p->seg_decay = reinterpret_cast<float*>(take(ends * 4));
     p->part = reinterpret_cast<float*>(take((size_t)p->ctas * 4 * kBlk * kN * 4));
     p->pA = reinterpret_cast<float*>(take(n * 4));
     p->pD = reinterpret_cast<float*>(take(n * 4));
@@ -1122,16 +1194,22 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     if ((st = make_map(&p.tm_B, a.B, kN, a.G, a.T, a.b)) != SSD_OK) return st;
     if ((st = make_map(&p.tm_C, a.C, kN, a.G, a.T, a.b)) != SSD_OK) return st;
     if ((st = make_map(&p.tm_dx, a.dx, kP, a.H, a.T, a.b)) != SSD_OK) return st;
-    if ((st = smem_limit_once((const void*)ssd_bwd_tc_state_kernel, (int)kSSmem)) != SSD_OK) return st;
+    if ((st = smem_limit_once((const void*)ssd_bwd_tc_state_kernel<false>, (int)kSSmem)) != SSD_OK) return st;
+    if ((st = smem_limit_once((const void*)ssd_bwd_tc_state_kernel<true>, (int)kSSmem)) != SSD_OK) return st;
     if ((st = smem_limit_once((const void*)ssd_bwd_tc_main_kernel, (int)kMSmem)) != SSD_OK) return st;
     {
         LaunchScope ls("ssd_bwd_tc_terms", s);
         ssd_bwd_tc_terms_kernel<<<dim3(a.b * p.nc, (a.H + 7) / 8), kTermThreads, 0, s>>>(p);
         SSD_CUDA_TRY(cudaGetLastError());
     }
+    if (p.nseg > 1) {
+        LaunchScope ls("ssd_bwd_tc_ends", s);
+        ssd_bwd_tc_state_kernel<true><<<dim3(a.b * a.H * (p.nseg - 1), 2), kSThreads, kSSmem, s>>>(p);
+        SSD_CUDA_TRY(cudaGetLastError());
+    }
     {
         LaunchScope ls("ssd_bwd_tc_state", s);
-        ssd_bwd_tc_state_kernel<<<dim3(a.b * a.H, 2), kSThreads, kSSmem, s>>>(p);
+        ssd_bwd_tc_state_kernel<false><<<dim3(a.b * a.H * p.nseg, 2), kSThreads, kSSmem, s>>>(p);
         SSD_CUDA_TRY(cudaGetLastError());
     }
     {
@@ -1141,7 +1219,7 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     }
     {
         LaunchScope ls("ssd_bwd_tc_join", s);
-        ssd_bwd_tc_join_kernel<<<(unsigned)((size_t)a.b * p.nc * a.G), kJoinThreads, 0, s>>>(p);
+        ssd_bwd_tc_join_kernel<<<(unsigned)((size_t)a.b * p.nc * a.G * kJoinSplit), kJoinThreads, 0, s>>>(p);
         SSD_CUDA_TRY(cudaGetLastError());
     }
     return launch_bwd_head_sums(p.pA, p.pD, p.pb, a.b * p.nc, a.H, a.dA, a.dD, a.dbias, s);
