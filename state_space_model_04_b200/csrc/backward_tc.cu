@@ -73,6 +73,39 @@ struct BwdTc {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// Waits.  Their slow side is one function each for a whole warp and for one thread, and all it needs
+// beside the barrier lies in shared memory: a wait costs its place in the code a few instructions.
+// On expiry the site goes to the status word and every other wait of the CTA gives up.
+__shared__ int s_stop;
+__shared__ int* s_status;
+__device__ __forceinline__ bool stopped() { return *reinterpret_cast<volatile int*>(&s_stop) != 0; }
+__device__ __forceinline__ bool wait_expired(unsigned long long t0, uint32_t site) {
+    if (stopped()) return true;
+    if (globaltimer() - t0 <= s_wait_ns) return false;
+    *reinterpret_cast<volatile int*>(&s_stop) = 1;
+    atomicCAS(s_status, 0, (int)(SSD_ERR_TIMEOUT | (site << 8)));
+    return true;
+}
+__device__ __noinline__ bool wait_slow_warp(uint32_t bar, uint32_t parity_site) {
+    const unsigned long long t0 = globaltimer();
+    while (!__all_sync(0xffffffffu, mbar_try_sleep(bar, parity_site & 1)))
+        if (__any_sync(0xffffffffu, wait_expired(t0, parity_site >> 1))) return false;
+    return true;
+}
+__device__ __noinline__ bool wait_slow_one(uint32_t bar, uint32_t parity_site) {
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_sleep(bar, parity_site & 1))
+        if (wait_expired(t0, parity_site >> 1)) return false;
+    return true;
+}
+// Phase `n` of a barrier (its parity counts).  wait_warp: all lanes together, with one result.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t n, uint32_t site) {
+    return __all_sync(0xffffffffu, mbar_try(bar, n & 1)) || wait_slow_warp(bar, (n & 1) | (site << 1));
+}
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t n, uint32_t site) {
+    return mbar_try(bar, n & 1) || wait_slow_one(bar, (n & 1) | (site << 1));
+}
+
 // ------------------------------------------------------------------ per-token terms
 // One warp per item, lane l holds tokens 32 q + l; prefix sums in fp64.
 constexpr int kTermThreads = 256;
@@ -152,25 +185,25 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
     auto chunk = [&](int k) { return dir ? nc - 1 - c0 - k : c0 + k; };
     uint8_t* small = smem + kSSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
-    volatile int* s_abort = reinterpret_cast<volatile int*>(small + 128);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 144);
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity & 1, s_abort, p.status, where); };
-    auto w1 = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity & 1, s_abort, p.status, where); };
+    auto wt = [&](int b, uint32_t n, uint32_t site) { return wait_warp(bar(b), n, site); };
+    auto w1 = [&](int b, uint32_t n, uint32_t site) { return wait_one(bar(b), n, site); };
 
     if (threadIdx.x == 0) {
         const bool misaligned = (sbase & 1023u) != 0;
         if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (5 << 8));
         for (int i = 0; i < SB_COUNT; ++i)
             mbar_init(bar(i), i == SB_XS || i == SB_XS + 1 || i == SB_ACCFREE || i == SB_ACCFREE + 1 ? 4 : 1);
-        *s_abort = misaligned ? 1 : 0;
+        s_stop = misaligned ? 1 : 0;
+        s_status = p.status;
         s_wait_ns = p.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, kSCols, warp == 1), 0);
     if (tmem == kTmemSentinel) {
-        *s_abort = 1;
+        s_stop = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (6 << 8));
     }
     // the product of the sequence's last chunk walked only feeds the adjoint of the initial state
@@ -178,7 +211,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
     const int products = final && !(dir && p.a.dh0) ? n - 1 : n;
 
     if (warp == 0) {
-        if (lane == 0 && !*s_abort && !p.starve) {
+        if (lane == 0 && !stopped() && !p.starve) {
             int issued = 0;
 #pragma unroll 1
             for (int k = 0; k < products; ++k) {
@@ -200,7 +233,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         if (elect_one()) {
             constexpr uint32_t id = idesc_bf16(128, 128, 1, 1);
             const uint64_t mB = sdesc(sbase + kRegion, kRegion, 1024), mX = sdesc(sbase + kSXs, kRegion, 1024);
-            bool ok = !*s_abort;
+            bool ok = !stopped();
 #pragma unroll 1
             for (int k = 0; k < products && ok; ++k) {
                 const int s = k & 1;
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             return dir ? t[kTermE * kBlk] : t[kTermW * kBlk] * t[kTermDt * kBlk];
         };
         float next = weight(0);
-        bool live = __all_sync(0xffffffffu, !*s_abort);
+        bool live = __all_sync(0xffffffffu, !stopped());
 #pragma unroll 1
         for (int k = 0; k < products && live; ++k) {
             const int s = k & 1;
@@ -289,7 +322,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         }
         float next = decay(0), total = 1.f;
         uint8_t* images = (dir ? p.img_g : p.img_h) + ((size_t)bi * nc * H + h) * kImage;
-        bool live = __all_sync(0xffffffffu, !*s_abort);
+        bool live = __all_sync(0xffffffffu, !stopped());
 #pragma unroll 1
         for (int k = 0; k < n && live; ++k) {
             const int s = k & 1;
@@ -347,7 +380,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             }
         }
         float* out = kEnds ? p.seg_end + (un * (p.nseg - 1) + seg) * kP * kN : final && dir ? p.a.dh0 : nullptr;
-        if (live && !*s_abort && out) {
+        if (live && !stopped() && out) {
             if (!kEnds) out += (size_t)u * kP * kN;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -372,7 +405,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
 }
 
 // ------------------------------------------------------------------ main pass
-// 18 warps; a warp's TMEM lane quadrant is q = warp % 4, and the work of the quadrants differs
+// 20 warps; a warp's TMEM lane quadrant is q = warp % 4, and the work of the quadrants differs
 // (tokens j of quadrant q meet tokens i of the 32-token groups c >= q only):
 //
 //   pair warps (q, c), q <= c: 10    S^T and the sum of dS^T of their 32 x 32 block in registers;
@@ -381,20 +414,23 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
 //   producer                         X, dY and the terms of an item (2-slot ring), the state halves
 //                                    (one slot), B and C of a group of heads
 //   issuer                           TMEM owner; every tcgen05.mma
-//   ddt                              ddt, the sums behind dA and dD; stores the dx tiles
-//   dot                              <h, dh>
+//   ddt                              ddt, the sums behind dA and dD
+//   store                            the dx tiles
+//   dot: 2                           <h, dh>, half of the entries each
 //
 // The roles' code runs at the same time and is fetched through one instruction cache: straight
 // FMA code measures 2.4 cycles an instruction up to 24 KB and 6 from 48 KB on (one warp a
 // scheduler), so loops stay rolled wherever registers need no constant index, and the slow side of
 // every wait is one call.
-constexpr int kWarps = 18, kThreads = 32 * kWarps;
-enum { ROLE_PAIR, ROLE_ROW, ROLE_ISSUER, ROLE_DDT, ROLE_PRODUCER, ROLE_DOT };
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+enum { ROLE_PAIR, ROLE_ROW, ROLE_ISSUER, ROLE_DDT, ROLE_STORE, ROLE_PRODUCER, ROLE_DOT };
 __device__ __forceinline__ int role_of(int warp) {
     const int q = warp & 3, j = warp >> 2;
     if (j < 4 - q) return ROLE_PAIR;  // c = q + j
     if (j == 4 - q) return ROLE_ROW;
-    return q == 1 ? ROLE_ISSUER : q == 2 ? ROLE_DDT : j == 2 ? ROLE_PRODUCER : ROLE_DOT;
+    if (q == 1) return ROLE_ISSUER;
+    if (q == 2) return j == 3 ? ROLE_DDT : ROLE_STORE;
+    return j == 2 ? ROLE_PRODUCER : ROLE_DOT;
 }
 
 constexpr uint32_t kMB = 0;                          // B: n 0..63, 64..127
@@ -421,7 +457,7 @@ enum {
     MB_EMPTYXY = 2,   // [2] row warps done with dY (4), dx tile read out (1)
     MB_EMPTYT = 4,    // [2] terms read: pair (10), row (4), ddt (1)
     MB_FULLST = 6,    // state halves landed
-    MB_EMPTYST = 7,   // every product that reads them done (1), <h, dh> done (1)
+    MB_EMPTYST = 7,   // every product that reads them done (1), <h, dh> done (2)
     MB_FULLBC = 8,    // B, C landed
     MB_SFULL = 9,     // S^T accumulated
     MB_SREAD = 10,    // pair warps read it (10)
@@ -437,7 +473,7 @@ enum {
     MB_DCDONE = 20,   // dC's product done: the tile is free
     MB_WXREADY = 21,  // row warps wrote w dt o X (4)
     MB_DBDONE = 22,   // dB's product done: the tile is free
-    MB_SUMFULL = 23,  // [2] sums written: pair (10), row (4), <h, dh> (1)
+    MB_SUMFULL = 23,  // [2] sums written: pair (10), row (4), <h, dh> (2)
     MB_SUMEMPTY = 25, // [2] sums read (1)
     MB_DXSTAGED = 27, // [2] dx tile written (4)
     MB_DSREADY = 29,  // pair warps wrote the dS^T tile (10)
@@ -450,8 +486,9 @@ static_assert(MB_COUNT * 8 <= 320, "barriers");
 __device__ __forceinline__ uint32_t main_bar_count(int i) {
     switch (i) {
         case MB_EMPTYXY: case MB_EMPTYXY + 1: return 5;
-        case MB_EMPTYT: case MB_EMPTYT + 1: case MB_SUMFULL: case MB_SUMFULL + 1: return 15;
-        case MB_EMPTYST: return 2;
+        case MB_EMPTYT: case MB_EMPTYT + 1: return 15;
+        case MB_SUMFULL: case MB_SUMFULL + 1: return 16;
+        case MB_EMPTYST: return 3;
         case MB_SREAD: case MB_MREADY: case MB_DSREADY: case MB_UNITFREE: return 10;
         case MB_VSCALED: case MB_UFREE: case MB_YFREE: case MB_EYREADY: case MB_WXREADY:
         case MB_DXSTAGED: case MB_DXSTAGED + 1: return 4;
@@ -459,11 +496,11 @@ __device__ __forceinline__ uint32_t main_bar_count(int i) {
     }
 }
 
-// v[i] of every lane summed over the lanes; lane l gets the sum of v[l % 8].  Halving exchange: 9
-// shuffles for 8 sums.
-__device__ __forceinline__ float transpose_sum(float (&v)[8], int lane) {
+// v[i] of every lane summed over the lanes; lane l gets the sum of v[l % 16].  Halving exchange: 16
+// shuffles for 16 sums.
+__device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
+    for (int o = 8; o > 0; o >>= 1) {
         const bool up = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -471,8 +508,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[8], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
-    const float a = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 8);
-    return a + __shfl_xor_sync(0xffffffffu, a, 16);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 // The items of one CTA, [lo, hi) of items = b nc H (< 2^31), in order: item (chunk bc of all
@@ -505,14 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
     const int lo = (int)(p.items * blockIdx.x / p.ctas), hi = (int)(p.items * (blockIdx.x + 1) / p.ctas);
     uint8_t* small = smem + kMSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
-    volatile int* s_abort = reinterpret_cast<volatile int*>(small + 320);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 336);
-    float* s_z = reinterpret_cast<float*>(small + 352);  // [2]
+    float* s_z = reinterpret_cast<float*>(small + 352);  // [2][2]
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     // waits of a whole warp, and of one thread
-    auto wt = [&](int b, uint32_t parity, int where) { return warp_wait(bar(b), parity & 1, s_abort, p.status, where); };
-    auto w1 = [&](int b, uint32_t parity, int where) { return mbar_wait(bar(b), parity & 1, s_abort, p.status, where); };
+    auto wt = [&](int b, uint32_t n, uint32_t site) { return wait_warp(bar(b), n, site); };
+    auto w1 = [&](int b, uint32_t n, uint32_t site) { return wait_one(bar(b), n, site); };
     // one arrival of the warp, once all its lanes are here
     auto arrive = [&](int b) {
         __syncwarp();
@@ -523,13 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
         const bool misaligned = (sbase & 1023u) != 0;
         if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (7 << 8));
         for (int i = 0; i < MB_COUNT; ++i) mbar_init(bar(i), main_bar_count(i));
-        *s_abort = misaligned ? 1 : 0;
+        s_stop = misaligned ? 1 : 0;
+        s_status = p.status;
         s_wait_ns = p.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_alloc_cta(s_tmem, 512, role == ROLE_ISSUER), 0);
     if (tmem == kTmemSentinel) {
-        *s_abort = 1;
+        s_stop = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (8 << 8));
     }
     // Every role walks the same items: i.k counts them (per-item barriers complete once each), n
@@ -543,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
         const int z0 = c - q, zstep = 4 - q;
         f32x2 S[16], dS[16];  // pairs of columns
         float sd = 0.f;       // S_jj
-        bool live = __all_sync(0xffffffffu, !*s_abort);
+        bool live = __all_sync(0xffffffffu, !stopped());
         int n = 0;
         for (Walk i(lo, hi, H, hg); i.more() && live; i.next()) {
             const int k = i.k, s = k & 1;
@@ -587,42 +623,40 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             f32x2 col2 = 0ull;
             float gd = 0.f;
 #pragma unroll
-            for (int o = 0; o < 4; ++o) {  // 8 columns at a time: few enough registers beside S and dS
-                uint32_t raw[8];
-                SSD_TMEM_LD8_WAIT(at + 8 * o, raw);
-                float w[8], e[8];
+            for (int half = 0; half < 2; ++half) {  // 16 columns at a time beside S and dS
+                uint32_t raw[16];
+                SSD_TMEM_LD16_WAIT(at + 16 * half, raw);
+                float w[16];
+                uint32_t pk[8];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(cs2 + 32 * c + 8 * o + 4 * j);
-                    unpack2(add2(pack2(v.x, v.y), d2), e[4 * j], e[4 * j + 1]);
-                    unpack2(add2(pack2(v.z, v.w), d2), e[4 * j + 2], e[4 * j + 3]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(raw[j]);
+                for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(raw[j]);
                 if (diagonal) {  // i < j counts for nothing, whatever G holds there
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int col = 8 * o + j;
-                        if (col < lane) e[j] = __int_as_float(0xff800000), w[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) {
+                        const int col = 16 * half + j;
+                        if (col < lane) w[j] = 0.f;
                         if (col == lane) gd = w[j];
                     }
                 }
-                uint32_t pk[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int m = 4 * o + j;
-                    const f32x2 l = pack2(ex2(e[2 * j]), ex2(e[2 * j + 1])), t = mul2(pack2(w[2 * j], w[2 * j + 1]), l);
+                for (int j = 0; j < 8; ++j) {
+                    const int m = 8 * half + j;
+                    const float2 v = *reinterpret_cast<const float2*>(cs2 + 32 * c + 2 * m);
+                    float l0, l1, a, b;
+                    unpack2(add2(pack2(v.x, v.y), d2), l0, l1);
+                    // (above the diagonal, where G and S are zero, only an infinity has to be kept off)
+                    const f32x2 l = pack2(ex2(fminf(l0, 126.f)), ex2(fminf(l1, 126.f)));
+                    const f32x2 t = mul2(pack2(w[2 * j], w[2 * j + 1]), l);
                     dS[m] = fma2(t, dt2, dS[m]);
-                    float a, b;
                     unpack2(mul2(S[m], l), a, b);
                     pk[j] = pack_bf16(a, b);
                     const f32x2 ww = mul2(S[m], t);
                     col2 = add2(col2, ww);
                     unpack2(mul2(ww, dt2), w[2 * j], w[2 * j + 1]);
                 }
-                SSD_TMEM_ST4_WAIT(at + 4 * o, pk);  // over the first 16 of the block's columns
+                SSD_TMEM_ST8_WAIT(at + 8 * half, pk);  // over the first 16 of the block's columns
                 const float row = transpose_sum(w, lane);
-                if (lane < 8) sums[(kSumRow + q) * kBlk + 32 * c + 8 * o + lane] = row;
+                if (lane < 16) sums[(kSumRow + q) * kBlk + 32 * c + 16 * half + lane] = row;
             }
             {
                 uint32_t zero[16] = {};
@@ -704,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
     } else if (role == ROLE_ROW) {
         const int r = q * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-        bool live = __all_sync(0xffffffffu, !*s_abort);
+        bool live = __all_sync(0xffffffffu, !stopped());
         float D_next = p.a.D[lo % H];
         for (Walk i(lo, hi, H, hg); i.more() && live; i.next()) {
             const int k = i.k, s = k & 1;
@@ -719,30 +753,31 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const uint8_t* ys = smem + kMY + s * kRegion;
             float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
             float F = 0.f, E = 0.f;
-            // Two rounds of the same steps: the row of dY weighted with e, then V against x;
-            // the row of X weighted with w dt, then Y against dy.  V is replaced by w o V on the way.
+            // the rows of dY weighted with e, then, once dC's product has read them, of X with w dt
 #pragma unroll 1
             for (int round = 0; round < 2; ++round) {
                 if (round) live = wt(MB_DCDONE, k, 112);
                 if (!live) break;
                 const uint8_t* src = round ? xs : ys;
                 const float weight = round ? wr * dtr : er;
-                const f32x2 w2 = pack2(weight, weight);
+                // x w in bf16 with one rounding that counts: x w_lo first, then fused x w_hi + that
+                const __nv_bfloat162 whi = __float2bfloat162_rn(weight);
+                const __nv_bfloat162 wlo = __float2bfloat162_rn(weight - __low2float(whi));
 #pragma unroll 2
                 for (int c = 0; c < 8; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c));
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[4];
+                    uint4 v = *reinterpret_cast<const uint4*>(src + swz(r, c));
+                    __nv_bfloat162* e = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, b;
-                        unpack2(mul2(pack2(bf_lo(in[j]), bf_hi(in[j])), w2), a, b);
-                        o[j] = pack_bf16(a, b);
-                    }
-                    *reinterpret_cast<uint4*>(smem + kMW + swz(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int j = 0; j < 4; ++j) e[j] = __hfma2(e[j], whi, __hmul2(e[j], wlo));
+                    *reinterpret_cast<uint4*>(smem + kMW + swz(r, c)) = v;
                 }
                 fence_proxy_async();
                 arrive(round ? MB_WXREADY : MB_EYREADY);
+            }
+            if (!live) break;
+            // V against x, with w o V in its place, then Y against dy
+#pragma unroll 1
+            for (int round = 0; round < 2; ++round) {
                 live = wt(round ? MB_YDONE : MB_VDONE, k, 113);
                 if (!live) break;
                 tc_fence_after();
@@ -814,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             arrive(MB_EMPTYXY + s);
         }
     } else if (role == ROLE_PRODUCER) {
-        if (lane == 0 && !*s_abort && !p.starve) {
+        if (lane == 0 && !stopped() && !p.starve) {
             int nxy = 0, nst = 0, nbc = 0, n = 0;
             for (Walk i(lo, hi, H, hg); i.more(); i.next()) {
                 const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
@@ -852,168 +887,175 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
         }
         __syncwarp();
     } else if (role == ROLE_ISSUER) {
-        // One lane issues everything, with constant descriptor steps: an address formed per
-        // instruction measured 190 cycles a product step against 40.
-                    if (elect_one()) {
-                        constexpr uint32_t id_nn = idesc_bf16(128, 128, 0, 0);   // both K-major
-                        constexpr uint32_t id_st = idesc_bf16(128, 64, 0, 1);    // state or dY [K rows][64]: MN-major
-                        constexpr uint32_t id_db = idesc_bf16(128, 128, 0, 1);
-                        constexpr uint32_t id_dc = idesc_bf16(128, 128, 1, 1);
-                        // K-major operands step 16 elements along a row (32 bytes, regions of 64 columns),
-                        // MN-major ones 16 rows
-                        auto k_major = [](uint32_t a) { return sdesc(a, 16, 1024); };
-                        auto mn_major = [](uint32_t a) { return sdesc(a, kRegion, 1024); };
-                        auto koff = [](int kk) { return (uint32_t)((kk >> 2) * (kRegion >> 4) + (kk & 3) * 2); };
-                        constexpr uint32_t kRowStep = 128;
-                        const uint64_t kB = k_major(sbase + kMB), kC = k_major(sbase + kMC), kW = k_major(sbase + kMW);
-                        const uint64_t kX0 = k_major(sbase + kMX), kY0 = k_major(sbase + kMY), mY0 = mn_major(sbase + kMY);
-                        const uint64_t kH = k_major(sbase + kMH), kG = k_major(sbase + kMG);
-                        const uint64_t mH = mn_major(sbase + kMH), mG = mn_major(sbase + kMG);
-                        bool ok = !*s_abort;
-                        int n = -1;
-                        for (Walk i(lo, hi, H, hg); i.more() && ok; i.next()) {
-                            const int k = i.k, s = k & 1;
-                            const bool fresh = i.first();
-                            const uint32_t stage = s * (kRegion >> 4);
-                            // G^T's columns: U of the item before has read M^T there
-                            ok = k < 1 || w1(MB_UDONE, k - 1, 70);
-                            if (!ok) break;
-                            if (fresh) {
-                                ++n;
-                                ok = w1(MB_FULLBC, n, 71);
-                                if (!ok) break;
-                                tc_fence_after();
-        #pragma unroll
-                                for (int kk = 0; kk < kN / 16; ++kk)
-                                    mma_ss(tmem + kColG, kB + koff(kk), kC + koff(kk), id_nn, kk > 0);
-                                mma_commit(bar(MB_SFULL));
-                                ok = w1(MB_SREAD, n, 72);
-                                if (!ok) break;
-                            }
-                            ok = w1(MB_FULLXY + s, k >> 1, 73);
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < kP / 16; ++kk)
-                                mma_ss(tmem + kColG, kX0 + stage + kk * 2, kY0 + stage + kk * 2, id_nn, kk > 0);
-                            mma_commit(bar(MB_GFULL));
-                            // V = B dh^T, Y = C h^T, hi then lo
-                            ok = w1(MB_FULLST, k, 74) && (k < 1 || w1(MB_UFREE, k - 1, 75));
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < 2 * kN / 16; ++kk)
-                                mma_ss(tmem + kColV, kB + koff(kk & 7), mG + (kk >> 3) * (kRegion >> 4) + (kk & 7) * kRowStep, id_st, kk > 0);
-                            mma_commit(bar(MB_VDONE));
-                            ok = k < 1 || w1(MB_YFREE, k - 1, 76);
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < 2 * kN / 16; ++kk)
-                                mma_ss(tmem + kColY, kC + koff(kk & 7), mH + (kk >> 3) * (kRegion >> 4) + (kk & 7) * kRowStep, id_st, kk > 0);
-                            mma_commit(bar(MB_YDONE));
-                            // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
-                            ok = w1(MB_EYREADY, k, 77);
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < kP / 16; ++kk)
-                                mma_ss(tmem + kColC, kW + kk * 2, kH + kk * 2, id_nn, !fresh || kk > 0);
-                            mma_commit(bar(MB_DCDONE));
-                            ok = w1(MB_WXREADY, k, 78);
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < kP / 16; ++kk)
-                                mma_ss(tmem + kColB, kW + kk * 2, kG + kk * 2, id_nn, !fresh || kk > 0);
-                            mma_commit(bar(MB_DBDONE));
-                            mma_commit(bar(MB_EMPTYST));
-                            // U = w o V + M^T dY
-                            ok = w1(MB_VSCALED, k, 79) && w1(MB_MREADY, k, 80);
-                            if (!ok) break;
-                            tc_fence_after();
-        #pragma unroll
-                            for (int kk = 0; kk < kBlk / 16; ++kk)
-                                mma_ts(tmem + kColV, tmem + kColG + (kk >> 1) * 32 + (kk & 1) * 8, mY0 + stage + kk * kRowStep, id_st, 1);
-                            mma_commit(bar(MB_UDONE));
-                            if (i.last()) {  // dB += dS^T C, dC += dS B
-                                ok = w1(MB_DSREADY, n, 81);
-                                if (!ok) break;
-                                tc_fence_after();
-                                const uint64_t mB = mn_major(sbase + kMB), mC = mn_major(sbase + kMC);
-        #pragma unroll
-                                for (int kk = 0; kk < kBlk / 16; ++kk)
-                                    mma_ss(tmem + kColB, kH + koff(kk), mC + kk * kRowStep, id_db, 1);
-        #pragma unroll
-                                for (int kk = 0; kk < kBlk / 16; ++kk)
-                                    mma_ss(tmem + kColC, mH + kk * kRowStep, mB + kk * kRowStep, id_dc, 1);
-                                mma_commit(bar(MB_ACCDONE));
-                            }
-                        }
-                        mma_commit(bar(MB_DONE));
-                        mbar_drain(bar(MB_DONE), 0);
-                    }
+        // One lane issues everything, in small rolled loops whose descriptors advance by constants.  (A
+        // loop over products with their layouts as data took 190 cycles an instruction; unrolled, the
+        // code crowds the instruction cache.)
+        if (elect_one()) {
+            constexpr uint32_t id_nn = idesc_bf16(128, 128, 0, 0);   // both K-major
+            constexpr uint32_t id_st = idesc_bf16(128, 64, 0, 1);    // state or dY [K rows][64]: MN-major
+            constexpr uint32_t id_db = idesc_bf16(128, 128, 0, 1);
+            constexpr uint32_t id_dc = idesc_bf16(128, 128, 1, 1);
+            // K-major operands step 16 elements along a row (32 bytes), and every 64 a region; MN-major
+            // ones step 16 rows
+            auto k_major = [](uint32_t a) { return sdesc(a, 16, 1024); };
+            auto mn_major = [](uint32_t a) { return sdesc(a, kRegion, 1024); };
+            constexpr uint32_t kCol = 2, kRow = 128, kReg = kRegion >> 4;
+            auto run4 = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {  // K = 64, both K-major
+#pragma unroll 1
+                for (int kk = 0; kk < 4; ++kk, a += kCol, b += kCol) mma_ss(d, a, b, id, acc | kk);
+            };
+            // K = 128, a K-major over two regions, b MN-major
+            auto run8 = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+#pragma unroll 1
+                for (int kk = 0; kk < 8; ++kk, b += kRow) {
+                    mma_ss(d, a, b, id, acc | kk);
+                    a += kk == 3 ? kReg - 3 * kCol : kCol;
+                }
+            };
+            const uint64_t kB = k_major(sbase + kMB), kC = k_major(sbase + kMC), kW = k_major(sbase + kMW);
+            const uint64_t kX0 = k_major(sbase + kMX), kY0 = k_major(sbase + kMY), mY0 = mn_major(sbase + kMY);
+            bool ok = !stopped();
+            int n = -1;
+#pragma unroll 1
+            for (Walk i(lo, hi, H, hg); i.more() && ok; i.next()) {
+                const int k = i.k, s = k & 1;
+                const bool fresh = i.first();
+                const uint32_t stage = s * kReg;
+                // G^T's columns: U of the item before has read M^T there
+                ok = k < 1 || w1(MB_UDONE, k - 1, 70);
+                if (!ok) break;
+                if (fresh) {
+                    ++n;
+                    ok = w1(MB_FULLBC, n, 71);
+                    if (!ok) break;
+                    tc_fence_after();
+                    run4(tmem + kColG, kB, kC, id_nn, 0);
+                    run4(tmem + kColG, kB + kReg, kC + kReg, id_nn, 1);
+                    mma_commit(bar(MB_SFULL));
+                    ok = w1(MB_SREAD, n, 72);
+                    if (!ok) break;
+                }
+                ok = w1(MB_FULLXY + s, k >> 1, 73);
+                if (!ok) break;
+                tc_fence_after();
+                run4(tmem + kColG, kX0 + stage, kY0 + stage, id_nn, 0);
+                mma_commit(bar(MB_GFULL));
+                // V = B dh^T, then Y = C h^T, each from both halves
+                ok = w1(MB_FULLST, k, 74) && (k < 1 || w1(MB_UFREE, k - 1, 75));
+                if (!ok) break;
+                tc_fence_after();
+                run8(tmem + kColV, kB, mn_major(sbase + kMG), id_st, 0);
+                run8(tmem + kColV, kB, mn_major(sbase + kMG + kRegion), id_st, 1);
+                mma_commit(bar(MB_VDONE));
+                // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
+                ok = w1(MB_EYREADY, k, 77);
+                if (!ok) break;
+                tc_fence_after();
+                run4(tmem + kColC, kW, k_major(sbase + kMH), id_nn, !fresh);
+                mma_commit(bar(MB_DCDONE));
+                ok = k < 1 || w1(MB_YFREE, k - 1, 76);
+                if (!ok) break;
+                tc_fence_after();
+                run8(tmem + kColY, kC, mn_major(sbase + kMH), id_st, 0);
+                run8(tmem + kColY, kC, mn_major(sbase + kMH + kRegion), id_st, 1);
+                mma_commit(bar(MB_YDONE));
+                ok = w1(MB_WXREADY, k, 78);
+                if (!ok) break;
+                tc_fence_after();
+                run4(tmem + kColB, kW, k_major(sbase + kMG), id_nn, !fresh);
+                mma_commit(bar(MB_DBDONE));
+                mma_commit(bar(MB_EMPTYST));
+                // U = w o V + M^T dY
+                ok = w1(MB_VSCALED, k, 79) && w1(MB_MREADY, k, 80);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    uint64_t b = mY0 + stage;
+                    uint32_t a = tmem + kColG;  // M^T: 16 columns of 32 hold 32 of K
+#pragma unroll 1
+                    for (int kk = 0; kk < 8; ++kk, b += kRow, a += kk & 1 ? 8 : 24) mma_ts(tmem + kColV, a, b, id_st, 1);
+                }
+                mma_commit(bar(MB_UDONE));
+                if (i.last()) {  // dB += dS^T C, dC += dS B
+                    ok = w1(MB_DSREADY, n, 81);
+                    if (!ok) break;
+                    tc_fence_after();
+                    run8(tmem + kColB, k_major(sbase + kMH), mn_major(sbase + kMC), id_db, 1);
+                    uint64_t a = mn_major(sbase + kMH), b = mn_major(sbase + kMB);
+#pragma unroll 1
+                    for (int kk = 0; kk < 8; ++kk, a += kRow, b += kRow) mma_ss(tmem + kColC, a, b, id_dc, 1);
+                    mma_commit(bar(MB_ACCDONE));
+                }
+            }
+            mma_commit(bar(MB_DONE));
+            mbar_drain(bar(MB_DONE), 0);
+        }
         __syncwarp();
     } else if (role == ROLE_DDT) {
-        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        bool ok = __all_sync(0xffffffffu, !stopped());
         float A_next = p.a.A[lo % H];
         for (Walk i(lo, hi, H, hg); i.more() && ok; i.next()) {
             const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
-            ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
-            if (!ok) break;
-            float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes) + lane;
-            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + lane;
-            // da_t adds a prefix of F (exclusive) and a suffix of E + rows - columns; 32 tokens a step
-            const float zz = s_z[s] * (terms - lane)[kTermE * kBlk + kBlk - 1];
             const float Ah = A_next;
             A_next = p.a.A[i.next_head()];
-            float sA = 0.f, sD = 0.f, sb = 0.f, carry = 0.f;
-#pragma unroll 1
+            ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
+            if (!ok) break;
+            const float* sums = reinterpret_cast<const float*>(smem + kMSums + s * kSumBytes) + lane;
+            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + lane;
+            // da_t adds a prefix of F (exclusive) and a suffix of E + rows - columns.  Lane l holds
+            // tokens 32 g + l; the four groups' scans run side by side
+            float f[4], dt[4], suf[4], dir[4], slope[4], sD = 0.f;
+#pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int t = 32 * g;
-                const float f = sums[kSumF * kBlk + t] * terms[kTermDt * kBlk + t];
-                float v = f;
+                dt[g] = terms[kTermDt * kBlk + 32 * g];
+                slope[g] = terms[kTermSlope * kBlk + 32 * g];
+                const float fj = sums[kSumF * kBlk + 32 * g], gd = sums[kSumGd * kBlk + 32 * g];
+                float row = sums[kSumE * kBlk + 32 * g], col = 0.f;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o) v += a;
+                for (int j = 0; j < 4; ++j) {
+                    if (j <= g) row += sums[(kSumRow + j) * kBlk + 32 * g];
+                    if (j >= g) col += sums[(kSumCol + j) * kBlk + 32 * g];
                 }
-                float row = sums[kSumE * kBlk + t];
-#pragma unroll 1
-                for (int j = 0; j <= g; ++j) row += sums[(kSumRow + j) * kBlk + t];
-                sums[kSumE * kBlk + t] = row;
-                sums[kSumRow * kBlk + t] = carry + v - f;  // the prefix, in a place its token has done with
-                carry += __shfl_sync(0xffffffffu, v, 31);
-            }
-            carry = zz;
-            size_t at = ((size_t)bi * T + t0 + 96 + lane) * H + h;
-#pragma unroll 1
-            for (int g = 3; g >= 0; --g) {
-                const int t = 32 * g;
-                const float dt = terms[kTermDt * kBlk + t];
-                float col = 0.f;
-#pragma unroll 1
-                for (int j = g; j < 4; ++j) col += sums[(kSumCol + j) * kBlk + t];
-                float v = fmaf(-col, dt, sums[kSumE * kBlk + t]);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_down_sync(0xffffffffu, v, o);
-                    if (lane + o < 32) v += a;
-                }
-                const float da = carry + v + sums[kSumRow * kBlk + t];
-                carry += __shfl_sync(0xffffffffu, v, 0);
-                const float gd = sums[kSumGd * kBlk + t];
-                const float ddt = fmaf(Ah, da, fmaf(gd, sums[kSumSd * kBlk + t], col + sums[kSumF * kBlk + t])) *
-                                  terms[kTermSlope * kBlk + t];
+                f[g] = fj * dt[g];
+                suf[g] = fmaf(-col, dt[g], row);
+                dir[g] = fmaf(gd, sums[kSumSd * kBlk + 32 * g], col + fj);
                 sD += gd;
-                if (t0 + t + lane < T) {
-                    p.a.ddt[at] = ddt;
-                    sA = fmaf(dt, da, sA);
+            }
+            float da = (s_z[2 * s] + s_z[2 * s + 1]) * (terms - lane)[kTermE * kBlk + kBlk - 1];
+            arrive(MB_SUMEMPTY + s);
+            arrive(MB_EMPTYT + s);
+            float pre[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) pre[g] = f[g];
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float a = __shfl_up_sync(0xffffffffu, pre[g], o), b = __shfl_down_sync(0xffffffffu, suf[g], o);
+                    if (lane >= o) pre[g] += a;
+                    if (lane + o < 32) suf[g] += b;
+                }
+            }
+            float sA = 0.f, sb = 0.f, carry[4], run = da;
+#pragma unroll
+            for (int g = 3; g >= 0; --g) {
+                carry[g] = run;  // <h, dh> and the suffix behind group g
+                run += __shfl_sync(0xffffffffu, suf[g], 0);
+            }
+            run = 0.f;
+            float* out = p.a.ddt + ((size_t)bi * T + t0 + lane) * H + h;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                da = carry[g] + suf[g] + (run + pre[g] - f[g]);
+                run += __shfl_sync(0xffffffffu, pre[g], 31);
+                const float ddt = fmaf(Ah, da, dir[g]) * slope[g];
+                if (t0 + 32 * g + lane < T) {
+                    out[(size_t)(32 * g) * H] = ddt;
+                    sA = fmaf(dt[g], da, sA);
                     sb += ddt;
                 }
-                at -= (size_t)32 * H;
             }
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) {
                 sA += __shfl_xor_sync(0xffffffffu, sA, o);
                 sD += __shfl_xor_sync(0xffffffffu, sD, o);
@@ -1024,47 +1066,56 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 p.pD[lo + k] = sD;
                 if (p.pb) p.pb[lo + k] = sb;
             }
-            arrive(MB_SUMEMPTY + s);
-            arrive(MB_EMPTYT + s);
-            ok = wt(MB_DXSTAGED + s, k >> 1, 92);
-            if (!ok) break;
-            if (lane == 0) {
-                tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, h, t0, bi);
+            __syncwarp();
+        }
+    } else if (role == ROLE_STORE) {
+        if (lane == 0 && !stopped()) {
+            for (Walk i(lo, hi, H, hg); i.more(); i.next()) {
+                const int k = i.k, s = k & 1, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
+                if (!w1(MB_DXSTAGED + s, k >> 1, 92)) break;
+                tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, i.h, t0, bi);
                 bulk_commit();
                 bulk_wait_read0();
                 mbar_arrive(bar(MB_EMPTYXY + s));
             }
-            __syncwarp();
+            bulk_wait0();
         }
-        if (lane == 0) bulk_wait0();
         __syncwarp();
     } else {
-        bool ok = __all_sync(0xffffffffu, !*s_abort);
+        // <h, dh>, half of the entries a warp.  hi hi' in fp32; the cross terms, 2^-8 of that, in packed
+        // bf16 over the 8 entries of a vector (their error 2^-8 of them again); lo lo' is below both
+        const int mine = (warp >> 2) - 3;
+        bool ok = __all_sync(0xffffffffu, !stopped());
         for (int k = 0; k < hi - lo && ok; ++k) {
             const int s = k & 1;
             ok = wt(MB_FULLST, k, 95);
             if (!ok) break;
             const uint4 *h4 = reinterpret_cast<const uint4*>(smem + kMH), *g4 = reinterpret_cast<const uint4*>(smem + kMG);
-            f32x2 z2 = 0ull;
+            f32x2 z2 = 0ull, c2 = 0ull;
 #pragma unroll 2
-            for (int i = lane; i < (int)(kRegion / 16); i += 32) {
+            for (int i = mine * 32 + lane; i < (int)(kRegion / 16); i += 64) {
                 const uint4 a = h4[i], al = h4[i + kRegion / 16], b = g4[i], bl = g4[i + kRegion / 16];
                 const uint32_t ah[4] = {a.x, a.y, a.z, a.w}, ao[4] = {al.x, al.y, al.z, al.w};
                 const uint32_t bh[4] = {b.x, b.y, b.z, b.w}, bo[4] = {bl.x, bl.y, bl.z, bl.w};
+                __nv_bfloat162 t = __float2bfloat162_rn(0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    z2 = fma2(add2(pack2(bf_lo(ah[j]), bf_hi(ah[j])), pack2(bf_lo(ao[j]), bf_hi(ao[j]))),
-                              add2(pack2(bf_lo(bh[j]), bf_hi(bh[j])), pack2(bf_lo(bo[j]), bf_hi(bo[j]))), z2);
+                for (int j = 0; j < 4; ++j) {
+                    auto v = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+                    z2 = fma2(pack2(bf_lo(ah[j]), bf_hi(ah[j])), pack2(bf_lo(bh[j]), bf_hi(bh[j])), z2);
+                    t = __hfma2(v(ah[j]), v(bo[j]), __hfma2(v(ao[j]), v(bh[j]), t));
+                }
+                const uint32_t tu = *reinterpret_cast<const uint32_t*>(&t);
+                c2 = add2(c2, pack2(bf_lo(tu), bf_hi(tu)));
             }
             arrive(MB_EMPTYST);
             float z, z1;
-            unpack2(z2, z, z1);
+            unpack2(add2(z2, c2), z, z1);
             z += z1;
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            ok = k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 96);
+            ok = k < 2 || wt(MB_SUMEMPTY + s, k / 2 - 1, 96);
             if (!ok) break;
-            if (lane == 0) s_z[s] = z;
+            if (lane == 0) s_z[2 * s + mine] = z;
             arrive(MB_SUMFULL + s);
         }
     }

@@ -294,16 +294,6 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
         : "r"(taddr) \
         : "memory"); \
     } while (0)
-#define SSD_TMEM_LD8_WAIT(taddr, r) \
-    do { \
-    __syncwarp(); \
-    asm volatile( \
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t" \
-        "tcgen05.wait::ld.sync.aligned;" \
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) \
-        : "r"(taddr) \
-        : "memory"); \
-    } while (0)
 #define SSD_TMEM_LD16_WAIT(taddr, r) \
     do { \
     __syncwarp(); \
@@ -354,14 +344,14 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
         : "r"(ta), kind(off) \
         : "memory"); \
     } while (0)
-#define SSD_TMEM_ST4_WAIT(ta, ra) \
+#define SSD_TMEM_ST8_WAIT(ta, ra) \
     do { \
     __syncwarp(); \
     asm volatile( \
-        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t" \
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t" \
         "tcgen05.wait::st.sync.aligned;" \
         : \
-        : "r"(ta), "r"(ra[0]), "r"(ra[1]), "r"(ra[2]), "r"(ra[3]) \
+        : "r"(ta), "r"(ra[0]), "r"(ra[1]), "r"(ra[2]), "r"(ra[3]), "r"(ra[4]), "r"(ra[5]), "r"(ra[6]), "r"(ra[7]) \
         : "memory"); \
     } while (0)
 #define SSD_TMEM_ST16_WAIT(ta, ra) \
