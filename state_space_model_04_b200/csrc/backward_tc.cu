@@ -912,6 +912,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                     a += kk == 3 ? kReg - 3 * kCol : kCol;
                 }
             };
+            // the same against both halves of a state image
+            auto run8_state = [&](uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll 1
+                for (int kk = 0; kk < 8; ++kk, b += kRow) {
+                    mma_ss_pair(d, a, b, b + kReg, id_st, kk);
+                    a += kk == 3 ? kReg - 3 * kCol : kCol;
+                }
+            };
             const uint64_t kB = k_major(sbase + kMB), kC = k_major(sbase + kMC), kW = k_major(sbase + kMW);
             const uint64_t kX0 = k_major(sbase + kMX), kY0 = k_major(sbase + kMY), mY0 = mn_major(sbase + kMY);
             bool ok = !stopped();
@@ -944,8 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 ok = w1(MB_FULLST, k, 74) && (k < 1 || w1(MB_UFREE, k - 1, 75));
                 if (!ok) break;
                 tc_fence_after();
-                run8(tmem + kColV, kB, mn_major(sbase + kMG), id_st, 0);
-                run8(tmem + kColV, kB, mn_major(sbase + kMG + kRegion), id_st, 1);
+                run8_state(tmem + kColV, kB, mn_major(sbase + kMG));
                 mma_commit(bar(MB_VDONE));
                 // dC += (e o dY) h, dB += (w dt o X) dh: the images as K-major [n][p]
                 ok = w1(MB_EYREADY, k, 77);
@@ -956,8 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 ok = k < 1 || w1(MB_YFREE, k - 1, 76);
                 if (!ok) break;
                 tc_fence_after();
-                run8(tmem + kColY, kC, mn_major(sbase + kMH), id_st, 0);
-                run8(tmem + kColY, kC, mn_major(sbase + kMH + kRegion), id_st, 1);
+                run8_state(tmem + kColY, kC, mn_major(sbase + kMH));
                 mma_commit(bar(MB_YDONE));
                 ok = w1(MB_WXREADY, k, 78);
                 if (!ok) break;

@@ -234,6 +234,18 @@ __device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint64_t a, uint64_t b, 
         ::"r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// Two products with the same A in a row: the first keeps A's slice in the tensor core's collector
+// buffer, the second takes it from there instead of reading shared memory again.
+__device__ __forceinline__ void mma_ss_pair(uint32_t tmem_d, uint64_t a, uint64_t b0, uint64_t b1, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %4, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %3, %4, q;\n\t}\n"
+        ::"r"(tmem_d), "l"(a), "l"(b0), "l"(b1), "r"(idesc), "r"(acc)
+        : "memory");
+}
 __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
