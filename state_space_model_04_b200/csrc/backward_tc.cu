@@ -630,13 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 uint32_t pk[8];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(raw[j]);
-                if (diagonal) {  // i < j counts for nothing, whatever G holds there
+                if (diagonal) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int col = 16 * half + j;
-                        if (col < lane) w[j] = 0.f;
-                        if (col == lane) gd = w[j];
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        if (16 * half + j == lane) gd = w[j];
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -644,8 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                     const float2 v = *reinterpret_cast<const float2*>(cs2 + 32 * c + 2 * m);
                     float l0, l1, a, b;
                     unpack2(add2(pack2(v.x, v.y), d2), l0, l1);
-                    // (above the diagonal, where G and S are zero, only an infinity has to be kept off)
-                    const f32x2 l = pack2(ex2(fminf(l0, 126.f)), ex2(fminf(l1, 126.f)));
+                    // above the diagonal S is zero and dS is dropped in the end; the bound keeps L finite
+                    // there (below it L <= 1)
+                    const f32x2 l = pack2(ex2(fminf(l0, 64.f)), ex2(fminf(l1, 64.f)));
                     const f32x2 t = mul2(pack2(w[2 * j], w[2 * j + 1]), l);
                     dS[m] = fma2(t, dt2, dS[m]);
                     unpack2(mul2(S[m], l), a, b);
@@ -679,6 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 live = wt(MB_EMPTYST, k, 104);
                 if (!live) break;
                 uint8_t* tile = smem + kMH;
+                if (diagonal) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        unpack2(dS[j], a, b);
+                        dS[j] = pack2(2 * j >= lane ? a : 0.f, 2 * j + 1 >= lane ? b : 0.f);
+                    }
+                }
 #pragma unroll
                 for (int c4 = 0; c4 < 4; ++c4) {
                     uint32_t o[4];
@@ -784,20 +790,21 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 const uint8_t* other = round ? ys : xs;
                 const uint32_t from = lanes + (round ? kColY : kColV);
                 const f32x2 wr2 = pack2(wr, wr);
-                f32x2 dot2 = 0ull;
+                f32x2 dots[2] = {0ull, 0ull};
 #pragma unroll 1
                 for (int o = 0; o < 4; ++o) {
+                    const uint4 rows[2] = {*reinterpret_cast<const uint4*>(other + swz(r, 2 * o)),
+                                           *reinterpret_cast<const uint4*>(other + swz(r, 2 * o + 1))};
                     uint32_t raw[16];
                     SSD_TMEM_LD16_WAIT(from + 16 * o, raw);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(other + swz(r, 2 * o + c));
-                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                        const uint32_t in[4] = {rows[c].x, rows[c].y, rows[c].z, rows[c].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t &ra = raw[8 * c + 2 * j], &rb = raw[8 * c + 2 * j + 1];
                             const f32x2 t = pack2(__uint_as_float(ra), __uint_as_float(rb));
-                            dot2 = fma2(pack2(bf_lo(in[j]), bf_hi(in[j])), t, dot2);
+                            dots[c] = fma2(pack2(bf_lo(in[j]), bf_hi(in[j])), t, dots[c]);
                             float a, b;
                             unpack2(mul2(t, wr2), a, b);
                             ra = __float_as_uint(a), rb = __float_as_uint(b);
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 tc_fence_before();
                 arrive(round ? MB_YFREE : MB_VSCALED);
                 float a, b;
-                unpack2(dot2, a, b);
+                unpack2(add2(dots[0], dots[1]), a, b);
                 if (round) E = a + b;  // E_i = e_i dy_i . Y_i
                 else F = a + b;        // F_j / dt_j = w_j x_j . V_j
             }
@@ -825,12 +832,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const f32x2 dy2 = pack2(dyw, dyw), dt2 = pack2(dtr, dtr);
 #pragma unroll 1
             for (int o = 0; o < 4; ++o) {
+                const uint4 rows[2] = {*reinterpret_cast<const uint4*>(ys + swz(r, 2 * o)),
+                                       *reinterpret_cast<const uint4*>(ys + swz(r, 2 * o + 1))};
                 uint32_t raw[16];
                 SSD_TMEM_LD16_WAIT(lanes + kColV + 16 * o, raw);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(ys + swz(r, 2 * o + c));
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t in[4] = {rows[c].x, rows[c].y, rows[c].z, rows[c].w};
                     uint32_t out[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
