@@ -152,25 +152,28 @@ __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __
 }
 
 // ------------------------------------------------------------------ state pass
-//   warp 0      TMA producer: X (or dY) and the two boxes of B (or C) of a chunk, 2-slot ring
+//   warp 0      TMA producer: X (or dY) and the two boxes of B (or C) of a chunk, 3-slot ring
 //   warp 1      TMEM owner and MMA issuer: D[n][hi p | lo p] = B^T [wX_hi | wX_lo], one product of
 //               N = 128 (the halves in products of their own would read B from shared memory twice)
-//   warps 2-5   one token row a thread: weighted into hi and lo tiles, a chunk ahead
-//   warps 6-9   one state row n a thread, 64 fp32 entries in registers: stores the entering state's
-//               halves, then h <- exp(cs_last) h + D_hi + D_lo.  A warp's 32 rows are a contiguous
-//               piece of the image, so it stores them on its own
+//   warp 2      stores the images, one bulk copy each
+//   warps 4-11  half a token row a thread: weighted into hi and lo tiles, a chunk ahead
+//   warps 12-19 half a state row n a thread, 32 fp32 entries in registers: writes the entering state's
+//               halves to an image, then h <- exp(cs_last) h + D_hi + D_lo
 // A sequence may be cut into segments of whole chunks to fill the SMs: the ends kernel runs all but
 // the last segment from zero for their end states, and the state kernel's segments start from the
 // fold of the ends before them.
-constexpr int kSThreads = 320;
+constexpr int kSThreads = 640;
 constexpr uint32_t kSSlot = 3 * kRegion;            // X, B (n 0..63), B (n 64..127)
-constexpr uint32_t kSXs = 2 * kSSlot;               // [2] hi, lo tiles of the weighted rows
-constexpr uint32_t kSImg = kSXs + 2 * kImage;       // [2] state images
-constexpr uint32_t kSSmall = kSImg + 2 * kImage;
+constexpr int kSSlots = 3;
+constexpr uint32_t kSXs = kSSlots * kSSlot;         // hi, lo tiles of the weighted rows
+constexpr uint32_t kSImg = kSXs + kImage;           // state image
+constexpr uint32_t kSSmall = kSImg + kImage;
 constexpr uint32_t kSSmem = kSSmall + 256;
 static_assert(kSSmem <= 232448 - 1024, "state pass shared memory");
 constexpr uint32_t kSCols = 256;                    // two accumulators of 128 columns
-enum { SB_FULL = 0, SB_EMPTY = 2, SB_XS = 4, SB_ACC = 6, SB_ACCFREE = 8, SB_DONE = 10, SB_COUNT };
+enum {
+    SB_FULL = 0, SB_EMPTY = 3, SB_XS = 6, SB_IMG = 7, SB_IMGFREE = 8, SB_DONE = 9, SB_ACC = 10, SB_ACCFREE = 12, SB_COUNT = 14
+};
 
 template <bool kEnds>
 __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __grid_constant__ BwdTc p) {
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         const bool misaligned = (sbase & 1023u) != 0;
         if (misaligned) report_status(p.status, SSD_ERR_INTERNAL | (5 << 8));
         for (int i = 0; i < SB_COUNT; ++i)
-            mbar_init(bar(i), i == SB_XS || i == SB_XS + 1 || i == SB_ACCFREE || i == SB_ACCFREE + 1 ? 4 : 1);
+            mbar_init(bar(i), i == SB_XS || i == SB_IMG || (i & ~1) == SB_ACCFREE ? 8 : 1);
         s_stop = misaligned ? 1 : 0;
         s_status = p.status;
         s_wait_ns = p.wait_ns;
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             int issued = 0;
 #pragma unroll 1
             for (int k = 0; k < products; ++k) {
-                const int s = k & 1;
-                if (k >= 2 && !w1(SB_EMPTY + s, (k - 2) >> 1, 50)) break;
+                const int s = k % kSSlots;
+                if (k >= kSSlots && !w1(SB_EMPTY + s, k / kSSlots - 1, 50)) break;
                 const uint32_t f = bar(SB_FULL + s), slot = sbase + s * kSSlot;
                 const int t0 = chunk(k) * kBlk;
                 mbar_expect_tx(f, kSSlot);
@@ -225,8 +228,8 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
                 tma_load_4d(slot + 2 * kRegion, dir ? &p.tm_C : &p.tm_B, f, 64, g, t0, bi);
                 issued = k + 1;
             }
-            for (int k = issued - 2; k < issued; ++k)
-                if (k >= 0) mbar_drain(bar(SB_FULL + (k & 1)), (k >> 1) & 1);
+            for (int k = issued - kSSlots; k < issued; ++k)
+                if (k >= 0) mbar_drain(bar(SB_FULL + k % kSSlots), (k / kSSlots) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -236,23 +239,37 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             bool ok = !stopped();
 #pragma unroll 1
             for (int k = 0; k < products && ok; ++k) {
-                const int s = k & 1;
-                ok = w1(SB_FULL + s, k >> 1, 51) && w1(SB_XS + s, k >> 1, 52) &&
+                const int s = k & 1, slot = k % kSSlots;
+                ok = w1(SB_FULL + slot, k / kSSlots, 51) && w1(SB_XS, k, 52) &&
                      (k < 2 || w1(SB_ACCFREE + s, (k - 2) >> 1, 53));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t a = mB + s * (kSSlot >> 4), b = mX + s * (kImage >> 4);
+                const uint64_t a = mB + slot * (kSSlot >> 4), b = mX;
 #pragma unroll
                 for (int kk = 0; kk < kBlk / 16; ++kk) mma_ss(tmem + s * 128, a + kk * 128, b + kk * 128, id, kk > 0);
-                mma_commit(bar(SB_EMPTY + s));
+                mma_commit(bar(SB_EMPTY + slot));
                 mma_commit(bar(SB_ACC + s));
             }
             mma_commit(bar(SB_DONE));
             mbar_drain(bar(SB_DONE), 0);
         }
         __syncwarp();
-    } else if (warp < 6) {
-        const int r = (warp - 2) * 32 + lane;  // token
+    } else if (warp == 2) {
+        if (!kEnds && lane == 0 && !stopped()) {
+            uint8_t* images = (dir ? p.img_g : p.img_h) + ((size_t)bi * nc * H + h) * kImage;
+#pragma unroll 1
+            for (int k = 0; k < n; ++k) {
+                if (!w1(SB_IMG, k, 57)) break;
+                bulk_store(images + (size_t)chunk(k) * H * kImage, sbase + kSImg, kImage);
+                bulk_commit();
+                bulk_wait_read0();
+                mbar_arrive(bar(SB_IMGFREE));
+            }
+            bulk_wait0();  // the stores are complete before the shared memory goes away
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        const int r = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;  // token, 32 of its columns
         const float* tm = p.terms + ((size_t)bi * nc * H + h) * kTerms * kBlk + r;
         auto weight = [&](int k) {
             if (k >= products) return 0.f;
@@ -263,15 +280,16 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         bool live = __all_sync(0xffffffffu, !stopped());
 #pragma unroll 1
         for (int k = 0; k < products && live; ++k) {
-            const int s = k & 1;
+            const int s = k % kSSlots;
             const f32x2 w2 = pack2(next, next), minus = pack2(-1.f, -1.f);
             next = weight(k + 1);
-            live = (k < 2 || wt(SB_EMPTY + s, (k - 2) >> 1, 54)) && wt(SB_FULL + s, k >> 1, 55);
+            // the product of the chunk before has read the tiles
+            live = (k < 1 || wt(SB_EMPTY + (k - 1) % kSSlots, (k - 1) / kSSlots, 54)) && wt(SB_FULL + s, k / kSSlots, 55);
             if (!live) break;
             const uint8_t* src = smem + s * kSSlot;
-            uint8_t* dst = smem + kSXs + s * kImage;
+            uint8_t* dst = smem + kSXs;
 #pragma unroll 2
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 4 * half; c < 4 * half + 4; ++c) {
                 const uint32_t o = swz(r, c);
                 const uint4 v = *reinterpret_cast<const uint4*>(src + o);
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -290,21 +308,21 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SB_XS + s));
+            if (lane == 0) mbar_arrive(bar(SB_XS));
         }
-    } else {
-        const int q = warp & 3, r = q * 32 + lane;  // state row n
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-        const size_t un = (size_t)u * 2 + dir;      // (sequence, head, direction)
+    } else if (warp >= 12) {
+        const int q = warp & 3, r = q * 32 + lane, half = (warp - 12) >> 2, p0 = 32 * half;  // state row n, columns p0 ..
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + p0;
+        const size_t un = (size_t)u * 2 + dir;  // (sequence, head, direction)
+        const size_t at = (size_t)p0 * kN + r;  // [p][n]
         const float* init = dir ? p.a.dhf : p.a.h0;
-        f32x2 st[32];
+        f32x2 st[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[i] = 0ull;
         if (init && seg == 0) {
+            const float* v = init + (size_t)u * kP * kN + at;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                st[i] = pack2(init[(size_t)u * kP * kN + (size_t)(2 * i) * kN + r], init[(size_t)u * kP * kN + (size_t)(2 * i + 1) * kN + r]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) st[i] = 0ull;
+            for (int i = 0; i < 16; ++i) st[i] = pack2(v[(2 * i) * kN], v[(2 * i + 1) * kN]);
         }
         const float* gp = p.terms + (((size_t)bi * nc * H + h) * kTerms + kTermE) * kBlk + kBlk - 1;
         auto decay = [&](int k) { return k < n ? gp[(size_t)chunk(k) * H * kTerms * kBlk] : 0.f; };
@@ -312,16 +330,14 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             // the ends of the segments before, in order; the first already starts from the initial state
 #pragma unroll 1
             for (int s = 0; s < seg; ++s) {
-                const float* e = p.seg_end + (un * (p.nseg - 1) + s) * kP * kN + r;
+                const float* e = p.seg_end + (un * (p.nseg - 1) + s) * kP * kN + at;
                 const float d = s ? p.seg_decay[un * (p.nseg - 1) + s] : 0.f;
                 const f32x2 d2 = pack2(d, d);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    st[i] = fma2(d2, s ? st[i] : 0ull, pack2(e[(size_t)(2 * i) * kN], e[(size_t)(2 * i + 1) * kN]));
+                for (int i = 0; i < 16; ++i) st[i] = fma2(d2, s ? st[i] : 0ull, pack2(e[(2 * i) * kN], e[(2 * i + 1) * kN]));
             }
         }
         float next = decay(0), total = 1.f;
-        uint8_t* images = (dir ? p.img_g : p.img_h) + ((size_t)bi * nc * H + h) * kImage;
         bool live = __all_sync(0xffffffffu, !stopped());
 #pragma unroll 1
         for (int k = 0; k < n && live; ++k) {
@@ -330,13 +346,13 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
             next = decay(k + 1);
             total *= gam;
             if constexpr (!kEnds) {
-                // the state as two bf16 halves; the warp's store of two chunks ago has read the buffer
-                uint8_t* img = smem + kSImg + s * kImage;
-                if (lane == 0) bulk_wait_read1();
-                __syncwarp();
+                // the state as two bf16 halves
+                live = k < 1 || wt(SB_IMGFREE, k - 1, 58);
+                if (!live) break;
+                uint8_t* img = smem + kSImg;
                 const f32x2 minus = pack2(-1.f, -1.f);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -346,18 +362,13 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
                         unpack2(fma2(pack2(bf_lo(hi[j]), bf_hi(hi[j])), minus, st[4 * c + j]), a, b);
                         lo[j] = pack_bf16(a, b);
                     }
-                    *reinterpret_cast<uint4*>(img + swz(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(img + kRegion + swz(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const uint32_t o = swz(r, 4 * half + c);
+                    *reinterpret_cast<uint4*>(img + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(img + kRegion + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) {
-                    uint8_t* dst = images + (size_t)chunk(k) * H * kImage + q * 4096;
-                    const uint32_t from = smem_u32(img) + q * 4096;
-                    bulk_store(dst, from, 4096);
-                    bulk_store(dst + kRegion, from + kRegion, 4096);
-                    bulk_commit();
-                }
+                if (lane == 0) mbar_arrive(bar(SB_IMG));
             }
             if (k < products) {
                 live = wt(SB_ACC + s, k >> 1, 56);
@@ -365,9 +376,9 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
                 tc_fence_after();
                 const f32x2 g2 = pack2(gam, gam);
 #pragma unroll
-                for (int o = 0; o < 4; ++o) {
+                for (int o = 0; o < 2; ++o) {
                     uint32_t hi[16], lo[16];
-                    SSD_TMEM_LD16x2_WAIT(lanes + s * 128 + 16 * o, 64, hi, lo);
+                    SSD_TMEM_LD16x2_WAIT(acc + s * 128 + 16 * o, 64, hi, lo);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         st[8 * o + j] = fma2(g2, st[8 * o + j],
@@ -383,16 +394,14 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         if (live && !stopped() && out) {
             if (!kEnds) out += (size_t)u * kP * kN;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 float a, b;
                 unpack2(st[i], a, b);
-                out[(size_t)(2 * i) * kN + r] = a;
-                out[(size_t)(2 * i + 1) * kN + r] = b;
+                out[at + (2 * i) * kN] = a;
+                out[at + (2 * i + 1) * kN] = b;
             }
-            if (kEnds && r == 0) p.seg_decay[un * (p.nseg - 1) + seg] = total;
+            if (kEnds && r == 0 && half == 0) p.seg_decay[un * (p.nseg - 1) + seg] = total;
         }
-        if (lane == 0) bulk_wait0();  // the stores are complete before the shared memory goes away
-        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
