@@ -14,24 +14,28 @@
 //                dz = dout y k w silu'(z),  dw = sum of t y k
 // Everything is computed in fp32 from the stored operands and rounded once, on the store.
 //
-// Bound: device memory.  Each operand is read once and each result written once; a segment
-// (a row, or one group of a row) stays in registers between its reductions and its results.
-// A segment belongs to `tps` threads of a block (blockDim.x), blockDim.y segments side by
-// side; the block then walks rows by a grid stride with its weights held in registers.  In the
-// backward pass the thread owns the same columns of every row it sees, so dw is summed in
-// registers over the rows, stored once per block to the workspace, and a second kernel adds
-// the blocks' sums in a fixed order (no atomics: the same call gives the same bits).
+// Bound: device memory, with the issue of instructions close behind in the gated backward pass.
+// Each operand is read once and each result written once; a segment (a row, or one group of a row)
+// stays in registers, as stored, between its reductions and its results.  A segment belongs to
+// `tps` threads of a block (blockDim.x), 8 elements a thread up to 1024 threads, blockDim.y
+// segments side by side; the block walks rows by a grid stride with its weights in registers.
+// Copies to shared memory some rows ahead (cp.async) measured slower than loads by more threads
+// (residual backward of 32768 x 2560: 246 us against 227 us).  In the backward pass the thread
+// owns the same columns of every row it sees, so dw is summed in registers over the rows, stored
+// once per block to the workspace, and a second kernel adds the blocks' sums in a fixed order (no
+// atomics: the same call gives the same bits).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include "common.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kMaxThreads = 512;
-// rows a block walks in the backward pass are spread over at most this many blocks an SM
-constexpr int kBwdBlocksPerSM = 6;
-constexpr int kSumRows = 32;  // threads along the parts in the dw sum kernel
+constexpr int kMaxThreads = 1024;
+constexpr int kPairThreads = 640;   // blocks up to here are built with more registers a thread
+constexpr int kMaxBlocksPerSM = 8;
+constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
 
 int norm_sm_count() {
     static const int n = [] {
@@ -42,79 +46,111 @@ int norm_sm_count() {
     return n;
 }
 
-// ---- V consecutive elements as fp32 (V = 8: 16-byte accesses; V = 1: one element)
-template <int V>
-__device__ __forceinline__ void loadv(const float* p, float (&o)[V]) {
-    if constexpr (V == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-    } else {
-        o[0] = *p;
-    }
+// Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register
+// pair; here they cost more in registers and moves than they saved: gated forward of 16384 x 5120
+// took 156 us with them against 117 us.)
+struct f2 { float x, y; };
+__device__ __forceinline__ f2 pk(float a, float b) { return {a, b}; }
+__device__ __forceinline__ f2 pk(float a) { return {a, a}; }
+__device__ __forceinline__ void un(f2 v, float& a, float& b) { a = v.x, b = v.y; }
+__device__ __forceinline__ f2 mul(f2 a, f2 b) { return {a.x * b.x, a.y * b.y}; }
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return {fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+
+// ---- a thread's V elements of an operand as stored (V = 8: 16-byte accesses; V = 2: two elements,
+// one by one), and as pairs of fp32
+template <typename T, int V> struct Raw;
+template <> struct Raw<float, 8> { float4 a, b; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 a; };
+template <typename T> struct Raw<T, 2> { T a, b; };
+
+__device__ __forceinline__ void load(Raw<float, 8>& r, const float* p, int) {
+    r.a = *reinterpret_cast<const float4*>(p), r.b = *reinterpret_cast<const float4*>(p + 4);
 }
-template <int V>
-__device__ __forceinline__ void loadv(const __nv_bfloat16* p, float (&o)[V]) {
-    if constexpr (V == 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void load(Raw<__nv_bfloat16, 8>& r, const __nv_bfloat16* p, int) {
+    r.a = *reinterpret_cast<const uint4*>(p);
+}
+template <typename T> __device__ __forceinline__ void load(Raw<T, 2>& r, const T* p, int n) {  // n: elements there are
+    r.a = p[0];
+    r.b = n > 1 ? p[1] : T(0.f);
+}
+__device__ __forceinline__ float f32(float v) { return v; }
+__device__ __forceinline__ float f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ f2 pair(const Raw<float, 8>& r, int j) {
+    return j == 0 ? pk(r.a.x, r.a.y) : j == 1 ? pk(r.a.z, r.a.w) : j == 2 ? pk(r.b.x, r.b.y) : pk(r.b.z, r.b.w);
+}
+__device__ __forceinline__ f2 pair(const Raw<__nv_bfloat16, 8>& r, int j) {
+    const uint32_t u = j == 0 ? r.a.x : j == 1 ? r.a.y : j == 2 ? r.a.z : r.a.w;
+    return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ f2 pair(const Raw<T, 2>& r, int) { return pk(f32(r.a), f32(r.b)); }
+
+// Keeps the compiler from carrying the unpacked values of a bf16 operand across a reduction beside
+// the stored ones: they are unpacked again behind it, for half the registers.
+__device__ __forceinline__ void repack(Raw<__nv_bfloat16, 8>& r) {
+    asm volatile("" : "+r"(r.a.x), "+r"(r.a.y), "+r"(r.a.z), "+r"(r.a.w));
+}
+template <typename R> __device__ __forceinline__ void repack(R&) {}
+
+__device__ __forceinline__ void store(float* p, const f2 (&v)[4], int) {
+    float4 a, b;
+    un(v[0], a.x, a.y), un(v[1], a.z, a.w), un(v[2], b.x, b.y), un(v[3], b.z, b.w);
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + 4) = b;
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const f2 (&v)[4], int) {
+    uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(u[i] << 16);
-            o[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    } else {
-        o[0] = __bfloat162float(*p);
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        un(v[i], a, b);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+        u[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-template <int V>
-__device__ __forceinline__ void storev(float* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *p = v[0];
-    }
-}
-template <int V>
-__device__ __forceinline__ void storev(__nv_bfloat16* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&t);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-        *p = __float2bfloat16_rn(v[0]);
-    }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <typename T> __device__ __forceinline__ void store(T* p, const f2 (&v)[1], int n) {
+    float a, b;
+    un(v[0], a, b);
+    put(p, a);
+    if (n > 1) put(p + 1, b);
 }
 
 // Sum of a (and b) over the threads of one segment.  A segment of at most 32 threads is one
-// warp; longer ones meet in shared memory.  `red` holds 2 x [blockDim.y][warps] pairs used in
+// warp; longer ones meet in shared memory.  `red` holds 2 x [blockDim.y][32] pairs used in
 // turn (`flip`), so one barrier a row is enough: a block can be at most one row ahead of its
 // slowest warp.  Every thread of the block calls this the same number of times.
+template <bool kTwo>
 __device__ __forceinline__ float2 segment_sum(float a, float b, float2* red, int flip) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+        if (kTwo) b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if (blockDim.x == 32) return make_float2(a, b);
-    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5;
-    float2* mine = red + (flip * blockDim.y + threadIdx.y) * nw;
-    if ((threadIdx.x & 31) == 0) mine[w] = make_float2(a, b);
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    float2* mine = red + (flip * blockDim.y + threadIdx.y) * 32;
+    if (lane == 0) mine[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    float2 t = make_float2(0.f, 0.f);
-    for (int i = 0; i < nw; ++i) {
-        const float2 m = mine[i];
-        t.x += m.x;
-        t.y += m.y;
+    float2 t = lane < nw ? mine[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+        if (kTwo) t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
     }
     return t;
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + 2^(-z log2 e)), both approximations within 2 ulp
+__device__ __forceinline__ float sigmoid1(float z) {
+    float a = z * -1.4426950408889634f;
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    a += 1.f;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    return a;
+}
+__device__ __forceinline__ f2 sigmoid2(f2 z) { return {sigmoid1(z.x), sigmoid1(z.y)}; }
 
 struct ResFwd {
     const void* x;
@@ -160,228 +196,317 @@ struct GateBwd {
     float eps;
 };
 
-#define SSD_NORM_PROLOGUE(LEN)                                                                   \
-    extern __shared__ float2 red[];                                                              \
-    const int tps = blockDim.x;                                                                  \
-    const long long row_step = (long long)gridDim.x * blockDim.y;                                \
-    const long long row_end = (p.rows + row_step - 1) / row_step * row_step;                     \
-    const float inv_len = 1.f / (float)(LEN);                                                    \
-    int col[VPT];                                                                                \
-    bool has[VPT];                                                                               \
-    _Pragma("unroll") for (int i = 0; i < VPT; ++i) {                                            \
-        col[i] = (i * tps + (int)threadIdx.x) * V;                                               \
-        has[i] = col[i] < (LEN);                                                                 \
-    }                                                                                            \
+// Common to the kernels below.  V elements an access; a thread's accesses of a segment lie V tps
+// elements apart.  col: element of an access, left: elements the segment has there (<= 0: none).
+// An element's address is the operand's place at the block's row, the same for all threads and so
+// held in uniform registers, and a 32-bit byte offset of the thread.
+#define SSD_NORM_PROLOGUE(LEN)                                                                            \
+    extern __shared__ float2 red[];                                                                       \
+    constexpr int kPairs = V / 2;                                                                         \
+    const int tps = blockDim.x;                                                                           \
+    const float inv_len = 1.f / (float)(LEN);                                                             \
+    int col[VPT], left[VPT];                                                                              \
+    _Pragma("unroll") for (int i = 0; i < VPT; ++i) {                                                     \
+        col[i] = (i * tps + (int)threadIdx.x) * V;                                                        \
+        left[i] = (LEN) - col[i];                                                                         \
+    }                                                                                                     \
     int flip = 0;
+#define SSD_NORM_ROWS                                                                                     \
+    for (long long row = (long long)blockIdx.x * blockDim.y; row < p.rows; row += (long long)gridDim.x * blockDim.y)
+// an operand: its first element, row stride, and the thread's offset
+template <typename T> struct At {
+    T* p;
+    long long ld;
+    uint32_t off;
+    __device__ __forceinline__ At(T* p_, long long ld_) : p(p_), ld(ld_), off((uint32_t)(threadIdx.y * ld_ * sizeof(T))) {}
+    __device__ __forceinline__ T* operator()(long long row, int col) const {
+        using C = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+        return reinterpret_cast<T*>(reinterpret_cast<C*>(p + row * ld) + (off + (uint32_t)col * (uint32_t)sizeof(T)));
+    }
+};
+// The operands of a row: loaded DEPTH rows ahead where the registers allow, so that memory is busy
+// through a row's reduction and stores.
+#define SSD_NORM_FIRST(DEPTH)                                                                             \
+    constexpr int kAhead = VPT == 1 && kThr == kPairThreads ? (DEPTH) : 0;                                \
+    const long long step = (long long)gridDim.x * blockDim.y;                                             \
+    Row cur = {}, next[kAhead > 0 ? kAhead : 1] = {};                                                     \
+    _Pragma("unroll") for (int d = 0; d < kAhead; ++d) fetch(next[d], (long long)blockIdx.x * blockDim.y + d * step);
+#define SSD_NORM_NEXT                                                                                     \
+    if constexpr (kAhead > 0) {                                                                           \
+        cur = next[0];                                                                                    \
+        _Pragma("unroll") for (int d = 0; d + 1 < kAhead; ++d) next[d] = next[d + 1];                     \
+        fetch(next[kAhead - 1], row + kAhead * step);                                                     \
+    } else {                                                                                              \
+        fetch(cur, row);                                                                                  \
+    }
+// The weights: in registers, or where a thread has none to spare (kLean: blocks above kPairThreads,
+// and several accesses a thread) read again for every row, from the L1 cache.
+#define SSD_NORM_WEIGHT(SRC)                                                                              \
+    constexpr bool kLean = kThr > kPairThreads;                                                           \
+    const float* const wsrc = (SRC);                                                                      \
+    f2 wreg[kLean ? 1 : VPT][kLean ? 1 : kPairs];                                                         \
+    if constexpr (!kLean) {                                                                               \
+        _Pragma("unroll") for (int i = 0; i < VPT; ++i) {                                                 \
+            Raw<float, V> raw = {};                                                                       \
+            if (left[i] > 0) load(raw, wsrc + col[i], left[i]);                                           \
+            _Pragma("unroll") for (int j = 0; j < kPairs; ++j) wreg[i][j] = pair(raw, j);                 \
+        }                                                                                                 \
+    }                                                                                                     \
+    /* weights of pair j of access i, which the segment has */                                            \
+    auto w = [&](int i, int j) -> f2 {                                                                    \
+        if constexpr (!kLean) return wreg[i][j];                                                          \
+        else if constexpr (V == 8) {                                                                      \
+            const float2 v = __ldg(reinterpret_cast<const float2*>(wsrc + col[i]) + j);                   \
+            return {v.x, v.y};                                                                            \
+        } else return {__ldg(wsrc + col[i]), left[i] > 1 ? __ldg(wsrc + col[i] + 1) : 0.f};               \
+    };
+#define SSD_NORM_DW                                                                                       \
+    f2 dw[VPT][kPairs];                                                                                   \
+    _Pragma("unroll") for (int i = 0; i < VPT; ++i)                                                       \
+        _Pragma("unroll") for (int j = 0; j < kPairs; ++j) dw[i][j] = {};
+#define SSD_NORM_DW_STORE(BASE)                                                                           \
+    if (p.part) {                                                                                         \
+        float* part = p.part + (size_t)(blockIdx.x * blockDim.y + threadIdx.y) * p.D + (BASE);            \
+        _Pragma("unroll") for (int i = 0; i < VPT; ++i)                                                   \
+            if (left[i] > 0) store(part + col[i], dw[i], left[i]);                                        \
+    }
+__device__ __forceinline__ float hsum(f2 v) {
+    float a, b;
+    un(v, a, b);
+    return a + b;
+}
 
-template <typename TIO, typename TRES, int V, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) ssd_residual_norm_kernel(const ResFwd p) {
+template <typename TIO, typename TRES, int V, int VPT, int kThr>
+__global__ void __launch_bounds__(kThr, kThr == kPairThreads ? 2 : 1) ssd_residual_norm_kernel(const ResFwd p) {
     SSD_NORM_PROLOGUE(p.D)
-    float w[VPT][V];
+    SSD_NORM_WEIGHT(p.w)
+    const f2 scale2 = pk(p.scale);
+    const At<const TIO> px(static_cast<const TIO*>(p.x), p.ld_x);
+    const At<const TRES> pres(static_cast<const TRES*>(p.res), p.ld_res);
+    const At<TIO> pout(static_cast<TIO*>(p.out), p.ld_out);
+    const At<TRES> pr(static_cast<TRES*>(p.r), p.ld_r);
+    SSD_NORM_ROWS {
+        const bool in = row + threadIdx.y < p.rows;
+        f2 r[VPT][kPairs], ss = {};
+        Raw<TIO, V> x[VPT] = {};
+        Raw<TRES, V> res[VPT] = {};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        if (has[i]) loadv<V>(p.w + col[i], w[i]);
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < row_end; row += row_step) {
-        const bool in = row < p.rows;
-        float r[VPT][V], ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) r[i][v] = 0.f;
-            if (in && has[i]) {
-                float xv[V];
-                if (p.res) loadv<V>(static_cast<const TRES*>(p.res) + row * p.ld_res + col[i], r[i]);
-                loadv<V>(static_cast<const TIO*>(p.x) + row * p.ld_x + col[i], xv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) r[i][v] = fmaf(p.scale, xv[v], r[i][v]);
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
+                load(x[i], px(row, col[i]), left[i]);
+                if (p.res) load(res[i], pres(row, col[i]), left[i]);
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) ss = fmaf(r[i][v], r[i][v], ss);
-        }
-        const float k = rsqrtf(segment_sum(ss, 0.f, red, flip).x * inv_len + p.eps);
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                r[i][j] = fma(scale2, pair(x[i], j), pair(res[i], j));
+                ss = fma(r[i][j], r[i][j], ss);
+            }
+        const float k = rsqrtf(segment_sum<false>(hsum(ss), 0.f, red, flip).x * inv_len + p.eps);
         flip ^= 1;
+        const f2 k2 = pk(k);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (in && has[i]) {
-                if (p.r) storev<V>(static_cast<TRES*>(p.r) + row * p.ld_r + col[i], r[i]);
-                float o[V];
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
+                if (p.r) store(pr(row, col[i]), r[i], left[i]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = r[i][v] * k * w[i][v];
-                storev<V>(static_cast<TIO*>(p.out) + row * p.ld_out + col[i], o);
+                for (int j = 0; j < kPairs; ++j) r[i][j] = mul(mul(r[i][j], k2), w(i, j));
+                store(pout(row, col[i]), r[i], left[i]);
             }
-        }
     }
 }
 
-template <typename TIO, typename TRES, int V, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) ssd_residual_norm_backward_kernel(const ResBwd p) {
+template <typename TIO, typename TRES, int V, int VPT, int kThr>
+__global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const ResBwd p) {
     SSD_NORM_PROLOGUE(p.D)
-    float w[VPT][V], dw[VPT][V];
+    SSD_NORM_WEIGHT(p.w)
+    SSD_NORM_DW
+    const f2 scale2 = pk(p.scale);
+    const At<const TIO> pg(static_cast<const TIO*>(p.dout), p.ld_dout);
+    const At<const TRES> pr(static_cast<const TRES*>(p.r), p.ld_r), pd(static_cast<const TRES*>(p.dr_out), p.ld_dro);
+    const At<TIO> pdx(static_cast<TIO*>(p.dx), p.ld_dx);
+    const At<TRES> pdres(static_cast<TRES*>(p.dres), p.ld_dres);
+    struct Row {
+        Raw<TRES, V> r[VPT], d[VPT];
+        Raw<TIO, V> g[VPT];
+    };
+    auto fetch = [&](Row& o, long long row) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (has[i]) loadv<V>(p.w + col[i], w[i]);
+        for (int i = 0; i < VPT; ++i)
+            if (row + threadIdx.y < p.rows && left[i] > 0) {
+                load(o.r[i], pr(row, col[i]), left[i]);
+                load(o.g[i], pg(row, col[i]), left[i]);
+                if (p.dr_out) load(o.d[i], pd(row, col[i]), left[i]);
+            }
+    };
+    SSD_NORM_FIRST(1)
+    SSD_NORM_ROWS {
+        const bool in = row + threadIdx.y < p.rows;
+        f2 ss = {}, gr = {};
+        SSD_NORM_NEXT
+        auto &r = cur.r, &d = cur.d;
+        auto& g = cur.g;
 #pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = 0.f;
-    }
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < row_end; row += row_step) {
-        const bool in = row < p.rows;
-        float r[VPT][V], g[VPT][V], d[VPT][V], ss = 0.f, gr = 0.f;
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) r[i][v] = g[i][v] = d[i][v] = 0.f;
-            if (in && has[i]) {
-                loadv<V>(static_cast<const TRES*>(p.r) + row * p.ld_r + col[i], r[i]);
-                loadv<V>(static_cast<const TIO*>(p.dout) + row * p.ld_dout + col[i], g[i]);
-                if (p.dr_out) loadv<V>(static_cast<const TRES*>(p.dr_out) + row * p.ld_dro + col[i], d[i]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    ss = fmaf(r[i][v], r[i][v], ss);
-                    gr = fmaf(g[i][v] * w[i][v], r[i][v], gr);
+                for (int j = 0; j < kPairs; ++j) {
+                    const f2 rv = pair(r[i], j);
+                    ss = fma(rv, rv, ss);
+                    gr = fma(mul(pair(g[i], j), w(i, j)), rv, gr);
                 }
             }
-        }
-        const float2 sum = segment_sum(ss, gr, red, flip);
+        const float2 sum = segment_sum<true>(hsum(ss), hsum(gr), red, flip);
         flip ^= 1;
         const float k = rsqrtf(sum.x * inv_len + p.eps);
-        const float m = sum.y * inv_len * k * k;
+        const f2 k2 = pk(k), m2 = pk(-sum.y * inv_len * k * k);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (in && has[i]) {
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
+                f2 o[kPairs];
+                repack(r[i]), repack(g[i]), repack(d[i]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    dw[i][v] = fmaf(g[i][v], r[i][v] * k, dw[i][v]);
-                    d[i][v] = fmaf(k, g[i][v] * w[i][v] - r[i][v] * m, d[i][v]);
+                for (int j = 0; j < kPairs; ++j) {
+                    const f2 rv = pair(r[i], j), gv = pair(g[i], j);
+                    dw[i][j] = fma(gv, mul(rv, k2), dw[i][j]);
+                    o[j] = fma(k2, fma(rv, m2, mul(gv, w(i, j))), pair(d[i], j));
                 }
-                if (p.dres) storev<V>(static_cast<TRES*>(p.dres) + row * p.ld_dres + col[i], d[i]);
+                if (p.dres) store(pdres(row, col[i]), o, left[i]);
                 if (p.dx) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) d[i][v] *= p.scale;
-                    storev<V>(static_cast<TIO*>(p.dx) + row * p.ld_dx + col[i], d[i]);
+                    for (int j = 0; j < kPairs; ++j) o[j] = mul(o[j], scale2);
+                    store(pdx(row, col[i]), o, left[i]);
                 }
             }
-        }
     }
-    if (p.part) {
-        float* part = p.part + (size_t)(blockIdx.x * blockDim.y + threadIdx.y) * p.D;
+    SSD_NORM_DW_STORE(0)
+}
+
+template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
+__global__ void __launch_bounds__(kThr) ssd_gated_norm_kernel(const GateFwd p) {
+    SSD_NORM_PROLOGUE(p.L)
+    const int base = blockIdx.y * p.L;
+    SSD_NORM_WEIGHT(p.w + base)
+    const At<const TIO> py(static_cast<const TIO*>(p.y) + base, p.ld_y), pz(static_cast<const TIO*>(p.z) + base, p.ld_z);
+    const At<TIO> pout(static_cast<TIO*>(p.out) + base, p.ld_out);
+    struct Row {
+        Raw<TIO, V> y[VPT], z[VPT];
+    };
+    auto fetch = [&](Row& o, long long row) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (has[i]) storev<V>(part + col[i], dw[i]);
-    }
-}
-
-template <typename TIO, bool kNormFirst, int V, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) ssd_gated_norm_kernel(const GateFwd p) {
-    SSD_NORM_PROLOGUE(p.L)
-    const int base = blockIdx.y * p.L;
-    float w[VPT][V];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        if (has[i]) loadv<V>(p.w + base + col[i], w[i]);
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < row_end; row += row_step) {
-        const bool in = row < p.rows;
-        float a[VPT][V], gt[VPT][V], ss = 0.f;  // a: what is normalised; gt: silu(z) where it follows the norm
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[i][v] = gt[i][v] = 0.f;
-            if (in && has[i]) {
-                loadv<V>(static_cast<const TIO*>(p.y) + row * p.ld_y + base + col[i], a[i]);
-                loadv<V>(static_cast<const TIO*>(p.z) + row * p.ld_z + base + col[i], gt[i]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    gt[i][v] *= sigmoid_f(gt[i][v]);
-                    if (!kNormFirst) a[i][v] *= gt[i][v];
-                }
+            if (row + threadIdx.y < p.rows && left[i] > 0) {
+                load(o.y[i], py(row, col[i]), left[i]);
+                load(o.z[i], pz(row, col[i]), left[i]);
             }
+    };
+    SSD_NORM_FIRST(1)
+    SSD_NORM_ROWS {
+        const bool in = row + threadIdx.y < p.rows;
+        f2 a[VPT][kPairs], gt[VPT][kPairs], ss = {};  // a: what is normalised; gt: silu(z)
+        SSD_NORM_NEXT
+        auto &y = cur.y, &z = cur.z;
 #pragma unroll
-            for (int v = 0; v < V; ++v) ss = fmaf(a[i][v], a[i][v], ss);
-        }
-        const float k = rsqrtf(segment_sum(ss, 0.f, red, flip).x * inv_len + p.eps);
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const f2 zv = pair(z[i], j);
+                gt[i][j] = mul(zv, sigmoid2(zv));
+                a[i][j] = kNormFirst ? pair(y[i], j) : mul(pair(y[i], j), gt[i][j]);
+                ss = fma(a[i][j], a[i][j], ss);
+            }
+        const float k = rsqrtf(segment_sum<false>(hsum(ss), 0.f, red, flip).x * inv_len + p.eps);
         flip ^= 1;
+        const f2 k2 = pk(k);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (in && has[i]) {
-                float o[V];
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    o[v] = a[i][v] * k * w[i][v];
-                    if (kNormFirst) o[v] *= gt[i][v];
+                for (int j = 0; j < kPairs; ++j) {
+                    a[i][j] = mul(mul(a[i][j], k2), w(i, j));
+                    if (kNormFirst) a[i][j] = mul(a[i][j], gt[i][j]);
                 }
-                storev<V>(static_cast<TIO*>(p.out) + row * p.ld_out + base + col[i], o);
+                store(pout(row, col[i]), a[i], left[i]);
             }
-        }
     }
 }
 
-template <typename TIO, bool kNormFirst, int V, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) ssd_gated_norm_backward_kernel(const GateBwd p) {
+template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
+__global__ void __launch_bounds__(kThr) ssd_gated_norm_backward_kernel(const GateBwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
-    float w[VPT][V], dw[VPT][V];
+    SSD_NORM_WEIGHT(p.w + base)
+    SSD_NORM_DW
+    const At<const TIO> pg(static_cast<const TIO*>(p.dout) + base, p.ld_dout), py(static_cast<const TIO*>(p.y) + base, p.ld_y),
+        pz(static_cast<const TIO*>(p.z) + base, p.ld_z);
+    const At<TIO> pdy(static_cast<TIO*>(p.dy) + base, p.ld_dy), pdz(static_cast<TIO*>(p.dz) + base, p.ld_dz);
+    struct Row {
+        Raw<TIO, V> y[VPT], z[VPT], g[VPT];
+    };
+    auto fetch = [&](Row& o, long long row) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (has[i]) loadv<V>(p.w + base + col[i], w[i]);
+        for (int i = 0; i < VPT; ++i)
+            if (row + threadIdx.y < p.rows && left[i] > 0) {
+                load(o.z[i], pz(row, col[i]), left[i]);
+                load(o.y[i], py(row, col[i]), left[i]);
+                load(o.g[i], pg(row, col[i]), left[i]);
+            }
+    };
+    SSD_NORM_FIRST(1)
+    SSD_NORM_ROWS {
+        const bool in = row + threadIdx.y < p.rows;
+        f2 ss = {}, gv = {}, sg[kLean ? 1 : VPT][kLean ? 1 : kPairs];
+        SSD_NORM_NEXT
+        auto &y = cur.y, &z = cur.z, &g = cur.g;
 #pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = 0.f;
-    }
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < row_end; row += row_step) {
-        const bool in = row < p.rows;
-        float y[VPT][V], z[VPT][V], g[VPT][V], ss = 0.f, gv = 0.f;
+        for (int i = 0; i < VPT; ++i)
+            if (in && left[i] > 0) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[i][v] = z[i][v] = g[i][v] = 0.f;
-            if (in && has[i]) {
-                loadv<V>(static_cast<const TIO*>(p.y) + row * p.ld_y + base + col[i], y[i]);
-                loadv<V>(static_cast<const TIO*>(p.z) + row * p.ld_z + base + col[i], z[i]);
-                loadv<V>(static_cast<const TIO*>(p.dout) + row * p.ld_dout + base + col[i], g[i]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float gate = z[i][v] * sigmoid_f(z[i][v]);
-                    const float n = kNormFirst ? y[i][v] : y[i][v] * gate;  // what is normalised
-                    const float t = kNormFirst ? g[i][v] * gate : g[i][v];  // gradient behind the weight
-                    ss = fmaf(n, n, ss);
-                    gv = fmaf(t * w[i][v], n, gv);
+                for (int j = 0; j < kPairs; ++j) {
+                    const f2 zv = pair(z[i], j), s1 = sigmoid2(zv), gate = mul(zv, s1);
+                    if constexpr (!kLean) sg[i][j] = s1;
+                    const f2 n = kNormFirst ? pair(y[i], j) : mul(pair(y[i], j), gate);              // what is normalised
+                    const f2 t = mul(kNormFirst ? mul(pair(g[i], j), gate) : pair(g[i], j), w(i, j));  // its gradient over k
+                    ss = fma(n, n, ss);
+                    gv = fma(t, n, gv);
                 }
             }
-        }
-        const float2 sum = segment_sum(ss, gv, red, flip);
+        const float2 sum = segment_sum<true>(hsum(ss), hsum(gv), red, flip);
         flip ^= 1;
         const float k = rsqrtf(sum.x * inv_len + p.eps);
-        const float m = sum.y * inv_len * k * k;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (in && has[i]) {
-                float dy[V], dz[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float sg = sigmoid_f(z[i][v]), gate = z[i][v] * sg;
-                    const float dgate = fmaf(gate, 1.f - sg, sg);  // silu'(z)
-                    if (kNormFirst) {
-                        const float n = y[i][v] * k, t = g[i][v] * gate;
-                        dw[i][v] = fmaf(t, n, dw[i][v]);
-                        dy[v] = k * (t * w[i][v] - y[i][v] * m);
-                        dz[v] = g[i][v] * n * w[i][v] * dgate;
-                    } else {
-                        const float n = y[i][v] * gate;
-                        dw[i][v] = fmaf(g[i][v], n * k, dw[i][v]);
-                        const float dn = k * (g[i][v] * w[i][v] - n * m);
-                        dy[v] = dn * gate;
-                        dz[v] = dn * y[i][v] * dgate;
-                    }
-                }
-                storev<V>(static_cast<TIO*>(p.dy) + row * p.ld_dy + base + col[i], dy);
-                storev<V>(static_cast<TIO*>(p.dz) + row * p.ld_dz + base + col[i], dz);
-            }
-        }
-    }
-    if (p.part) {
-        float* part = p.part + (size_t)(blockIdx.x * blockDim.y + threadIdx.y) * p.D + base;
+        const f2 k2 = pk(k), m2 = pk(-sum.y * inv_len * k * k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (has[i]) storev<V>(part + col[i], dw[i]);
+            if (in && left[i] > 0) {
+                f2 dy[kPairs], dz[kPairs];
+                repack(y[i]), repack(z[i]), repack(g[i]);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    const f2 zv = pair(z[i], j), yv = pair(y[i], j), go = pair(g[i], j);
+                    f2 s1;
+                    if constexpr (kLean) s1 = sigmoid2(zv);
+                    else s1 = sg[i][j];
+                    const f2 gate = mul(zv, s1);
+                    const f2 dgate = fma(gate, fma(s1, pk(-1.f), pk(1.f)), s1);  // silu'(z)
+                    if (kNormFirst) {
+                        const f2 n = mul(yv, k2), t = mul(go, gate);
+                        dw[i][j] = fma(t, n, dw[i][j]);
+                        dy[j] = mul(k2, fma(yv, m2, mul(t, w(i, j))));
+                        dz[j] = mul(mul(go, n), mul(w(i, j), dgate));
+                    } else {
+                        const f2 n = mul(yv, gate);
+                        dw[i][j] = fma(go, mul(n, k2), dw[i][j]);
+                        const f2 dn = mul(k2, fma(n, m2, mul(go, w(i, j))));
+                        dy[j] = mul(dn, gate);
+                        dz[j] = mul(mul(dn, yv), dgate);
+                    }
+                }
+                store(pdy(row, col[i]), dy, left[i]);
+                store(pdz(row, col[i]), dz, left[i]);
+            }
     }
+    SSD_NORM_DW_STORE(base)
 }
 
 // dw[c] = sum over the parts, in part order per thread row and then over the thread rows.
@@ -407,24 +532,29 @@ struct Shape {
     size_t smem;
 };
 
+// Threads an SM holds of the one-vector kernels: their registers are 48 in the residual forward pass, 56
+// in the gated one, 96 in the backward passes (which hold dw and a row ahead); 48 element by element.
+constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
+
 // Vector accesses need every operand's row starts on 16 bytes and segments of whole vectors
-// (`vec`); otherwise elements are read one by one.  A thread takes one access of a segment
-// while that leaves at most 384 threads a segment, two up to 768 and four beyond: few accesses
-// keep the registers low and several blocks on an SM.
-Shape norm_shape(long long rows, int groups, int L, bool vec, bool backward) {
+// (`vec`); otherwise elements are read one by one, in pairs.  A thread takes one vector of a segment
+// up to 1024 threads and two beyond: more threads with one vector each measured faster than fewer
+// with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
+Shape norm_shape(long long rows, int groups, int L, bool vec, int resident) {
     Shape s;
-    s.V = vec ? 8 : 1;
+    s.V = vec ? 8 : 2;
     const int n = (L + s.V - 1) / s.V;
-    if (vec) s.vpt = n <= 384 ? 1 : n <= 768 ? 2 : 4;
-    else s.vpt = n <= 4 * kMaxThreads ? 4 : 32;
+    s.vpt = n <= kMaxThreads ? 1 : vec ? 2 : n <= 4 * kMaxThreads ? 4 : 8;
     s.tps = ((n + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.seg = s.tps >= 256 ? 1 : std::max(1, 256 / s.tps);
-    s.smem = 2 * sizeof(float2) * s.seg * (s.tps / 32);
+    const int thr = s.tps * s.seg;
+    s.smem = 2 * sizeof(float2) * s.seg * 32;
+    // one wave of blocks: each holds its weights, and in the backward pass stores a part of dw
+    if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
+    else if (!vec) resident = kFwdThreads;
+    const int per_sm = std::max(1, std::min(kMaxBlocksPerSM, resident / thr));
     const long long want = (rows + s.seg - 1) / s.seg;
-    // forward: a few waves of blocks; backward: one wave, since each block stores a part of dw
-    const int per_sm = backward ? kBwdBlocksPerSM : 4 * std::max(1, 2048 / (s.tps * s.seg));
-    const long long cap = std::max<long long>(1, (long long)norm_sm_count() * per_sm / groups);
-    s.blocks = (int)std::min(want, cap);
+    s.blocks = (int)std::min(want, std::max<long long>(1, (long long)norm_sm_count() * per_sm / groups));
     return s;
 }
 
@@ -443,10 +573,14 @@ int launch_dweight(const float* part, float* dw, int parts, int D, cudaStream_t 
     return SSD_OK;
 }
 
-// the kernel of a shape among the five (V, VPT) instances
-#define SSD_NORM_PICK(kernel, A, B)                                                         \
-    (sh.V == 8 ? (sh.vpt == 1 ? kernel<A, B, 8, 1> : sh.vpt == 2 ? kernel<A, B, 8, 2> : kernel<A, B, 8, 4>) \
-               : (sh.vpt == 4 ? kernel<A, B, 1, 4> : kernel<A, B, 1, 32>))
+// the kernel of a shape among its instances
+#define SSD_NORM_PICK(kernel, A, B)                                                                                    \
+    (sh.vpt == 1 ? (sh.tps * sh.seg <= kPairThreads ? (sh.V == 8 ? kernel<A, B, 8, 1, kPairThreads>                    \
+                                                                 : kernel<A, B, 2, 1, kPairThreads>)                   \
+                                                    : (sh.V == 8 ? kernel<A, B, 8, 1, kMaxThreads>                     \
+                                                                 : kernel<A, B, 2, 1, kMaxThreads>))                   \
+     : sh.V == 8 ? kernel<A, B, 8, 2, kMaxThreads>                                                                     \
+     : sh.vpt == 4 ? kernel<A, B, 2, 4, kMaxThreads> : kernel<A, B, 2, 8, kMaxThreads>)
 
 bool vec_ok(const void* p, long long ld, int elem) {
     return !p || (aligned16(p) && (ld * elem) % 16 == 0);
@@ -461,7 +595,7 @@ size_t norm_workspace_bytes(long long rows, int D, int groups) {
     size_t parts = 0;
     for (int v = 0; v < 2; ++v) {
         if (v && L % 8) continue;
-        const Shape s = norm_shape(rows, groups, L, v != 0, true);
+        const Shape s = norm_shape(rows, groups, L, v != 0, kBwdThreads);
         parts = std::max(parts, (size_t)s.blocks * s.seg);
     }
     return round_up(parts * D * sizeof(float), 256);
@@ -473,7 +607,7 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, false);
+    const Shape sh = norm_shape(rows, 1, D, vec, kFwdThreads);
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -489,7 +623,7 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(r, ld_r, rb) && vec_ok(dro, ld_dro, rb) &&
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, true);
+    const Shape sh = norm_shape(rows, 1, D, vec, kBwdThreads);
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
     const char* name = "ssd_residual_norm_backward";
@@ -510,7 +644,7 @@ int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first,
                       cudaStream_t s) {
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) && vec_ok(out, ld_out, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, false);
+    const Shape sh = norm_shape(rows, groups, L, vec, kGatedThreads);
     const GateFwd p{y, z, w, out, rows, ld_y, ld_z, ld_out, D, L, eps};
     const char* name = "ssd_gated_norm";
     if (io == SSD_F32)
@@ -527,7 +661,7 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, true);
+    const Shape sh = norm_shape(rows, groups, L, vec, kBwdThreads);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
     const char* name = "ssd_gated_norm_backward";
