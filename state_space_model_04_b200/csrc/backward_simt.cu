@@ -63,9 +63,9 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
 }
 
 // A [kQ][W] tile from rows `stride` elements apart; rows from `valid` on are zero.
-template <int W, typename T>
+template <int W, int kThr, typename T>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, size_t stride, int valid) {
-    for (int i = threadIdx.x; i < kQ * (W / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < kQ * (W / 4); i += kThr) {
         const int r = i / (W / 4), c = i % (W / 4);
         const float4 v = r < valid ? ld4(src + r * stride + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4*>(dst + at<W>(r, c)) = v;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) ssd_bwd_chunk_states_kernel(const Si
     const size_t tok = (size_t)bi * p.a.T + t0;
     const TIO* xs = static_cast<const TIO*>(dir ? p.a.dy : p.a.x) + (tok * p.a.H + h) * kP;
     const TIO* bs = static_cast<const TIO*>(dir ? p.a.C : p.a.B) + (tok * p.a.G + g) * N;
-    load_tile<N>(sb, bs, (size_t)p.a.G * N, valid);
+    load_tile<N, kThreads>(sb, bs, (size_t)p.a.G * N, valid);
     const size_t o = (size_t)blockIdx.x * kQ;
     for (int i = threadIdx.x; i < kQ * (kP / 4); i += kThreads) {
         const int r = i / (kP / 4), c = i % (kP / 4);
@@ -244,12 +244,19 @@ __global__ void __launch_bounds__(kThreads) ssd_bwd_state_scan_kernel(const Simt
 template <int N> struct MainSmem {
     static constexpr int kB = 0, kC = kB + kQ * N, kH = kC + kQ * N, kG = kH + kP * N, kX = kG + kP * N,
                          kY = kX + kQ * kP, kS = kY + kQ * kP, kM = kS + kQ * kQ, kTerms = kM + kQ * kQ;
-    // per-token: dt, e, w, cs (double), row sums, column parts [8], E, direct, F; 8 warp sums x 2
-    static constexpr int kFloats = kTerms + kQ * (3 + 2 + 1 + 8 + 8 + 3) + 32;
+    // per-token: cs (double), dt, e, w, row sums, column parts [8], Gm S and Gm on the diagonal, E, F;
+    // then the warps' sums of <h, dh>
+    static constexpr int kFloats = kTerms + kQ * (2 + 3 + 1 + 8 + 2 + 2) + 16;
 };
 
 template <typename TIO, int N>
-__global__ void __launch_bounds__(kThreads, 1) ssd_bwd_chunk_kernel(const SimtBwd p) {
+// Two groups of 256 threads, a 4 x 4 tile of a 64 x 64 product each, work side by side on an item:
+//   pairs   Gm, M, dS and W's sums, then U, V, dx and F
+//   states  E from C h^T, then the states' parts of dC and dB, held in registers over the heads
+// One group doing both in turn took 361 us against 321 us for 4096 tokens, 24 heads, N = 64, and 35
+// against 34 us for 512 tokens, 4 heads; at N = 128 the two are level (4 x 2048 tokens, 48 heads:
+// 1.60 and 1.62 ms).
+__global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const SimtBwd p) {
     using SM = MainSmem<N>;
     extern __shared__ float sm[];
     float *sB = sm + SM::kB, *sC = sm + SM::kC, *sH = sm + SM::kH, *sG = sm + SM::kG, *sX = sm + SM::kX,
@@ -261,34 +268,37 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_chunk_kernel(const SimtBw
     float* s_dia = s_col + 8 * kQ;  // [kQ] Gm_jj S_jj, and [kQ] Gm_jj behind it
     float* s_E = s_dia + 2 * kQ;    // [kQ] E_i
     float* s_F = s_E + kQ;          // [kQ] F_j / dt_j
-    float* s_z = s_F + kQ;          // [8] warp sums of <h, dh>
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+    float* s_z = s_F + kQ;          // [16] warp sums of <h, dh>
+    const int tid = threadIdx.x, ty = (tid & 255) >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+    const bool pairs = tid < kThreads;
     const int H = p.a.H, G = p.a.G, T = p.a.T, hg = H / G;
     const int split = blockIdx.x % p.splits, ug = blockIdx.x / p.splits, g = ug % G, bc = ug / G;
     const int bi = bc / p.nc, t0 = (bc % p.nc) * kQ, valid = min(kQ, T - t0);
     const size_t tok = (size_t)bi * T + t0;
     const int h_lo = (int)((long long)split * hg / p.splits), h_hi = (int)((long long)(split + 1) * hg / p.splits);
 
-    load_tile<N>(sB, static_cast<const TIO*>(p.a.B) + (tok * G + g) * N, (size_t)G * N, valid);
-    load_tile<N>(sC, static_cast<const TIO*>(p.a.C) + (tok * G + g) * N, (size_t)G * N, valid);
+    load_tile<N, 2 * kThreads>(sB, static_cast<const TIO*>(p.a.B) + (tok * G + g) * N, (size_t)G * N, valid);
+    load_tile<N, 2 * kThreads>(sC, static_cast<const TIO*>(p.a.C) + (tok * G + g) * N, (size_t)G * N, valid);
     __syncthreads();
-    {
+    if (pairs) {
         float s[4][4] = {};
         mm_nt<N>(sC, sB, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float4*>(sS + at<64>(4 * ty + i, tx)) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     }
-    float dS[4][4] = {}, dC[4][N / 16] = {}, dB[4][N / 16] = {};
+    // over the heads: the pairs' group holds dS in the first four columns of dC's registers
+    float dC[4][N / 16] = {}, dB[4][N / 16] = {};
+    auto& dS = dC;
 
     for (int hh = h_lo; hh < h_hi; ++hh) {
         const int h = g * hg + hh;
         const size_t u = (size_t)bc * H + h;
         __syncthreads();  // the head before has been read
-        load_tile<kP>(sX, static_cast<const TIO*>(p.a.x) + (tok * H + h) * kP, (size_t)H * kP, valid);
-        load_tile<kP>(sY, static_cast<const TIO*>(p.a.dy) + (tok * H + h) * kP, (size_t)H * kP, valid);
+        load_tile<kP, 2 * kThreads>(sX, static_cast<const TIO*>(p.a.x) + (tok * H + h) * kP, (size_t)H * kP, valid);
+        load_tile<kP, 2 * kThreads>(sY, static_cast<const TIO*>(p.a.dy) + (tok * H + h) * kP, (size_t)H * kP, valid);
         float z = 0.f;
-        for (int i = tid; i < kP * (N / 4); i += kThreads) {
+        for (int i = tid; i < kP * (N / 4); i += 2 * kThreads) {
             const int r = i / (N / 4), c = i % (N / 4);
             const float4 a = ld4(p.hs + u * kP * N + 4 * i), d = ld4(p.gs + u * kP * N + 4 * i);
             *reinterpret_cast<float4*>(sH + at<N>(r, c)) = a;
@@ -305,95 +315,98 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_chunk_kernel(const SimtBw
             s_w[tid] = p.w[u * kQ + tid];
         }
         __syncthreads();
-        // ---- Gm, M = S L, dS, W's sums (rows i = 4 ty + a, columns j = 4 tx + b)
-        {
-            float gm[4][4] = {}, row[4] = {}, colp[4] = {};
-            mm_nt<kP>(sY, sX, ty, tx, gm);
+        if (pairs) {
+            // ---- Gm, M = S L, dS, W's sums (rows i = 4 ty + a, columns j = 4 tx + b)
+            {
+                float gm[4][4] = {}, row[4] = {}, colp[4] = {};
+                mm_nt<kP>(sY, sX, ty, tx, gm);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int i = 4 * ty + a;
-                const float4 s4 = ld4(sS + at<64>(i, tx));
-                const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
-                float m[4];
+                for (int a = 0; a < 4; ++a) {
+                    const int i = 4 * ty + a;
+                    const float4 s4 = ld4(sS + at<64>(i, tx));
+                    const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+                    float m[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int j = 4 * tx + c;
-                    const float l = i >= j ? expf((float)(s_cs[i] - s_cs[j])) : 0.f;
-                    m[c] = sv[c] * l;
-                    const float wv = gm[a][c] * m[c];
-                    dS[a][c] = fmaf(gm[a][c] * l, s_dt[j], dS[a][c]);
-                    if (i == j) {
-                        s_dia[j] = wv;
-                        s_dia[kQ + j] = gm[a][c];
-                    } else {
-                        row[a] = fmaf(wv, s_dt[j], row[a]);
-                        colp[c] += wv;
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = 4 * tx + c;
+                        const float l = i >= j ? expf((float)(s_cs[i] - s_cs[j])) : 0.f;
+                        m[c] = sv[c] * l;
+                        const float wv = gm[a][c] * m[c];
+                        dS[a][c] = fmaf(gm[a][c] * l, s_dt[j], dS[a][c]);
+                        if (i == j) {
+                            s_dia[j] = wv;
+                            s_dia[kQ + j] = gm[a][c];
+                        } else {
+                            row[a] = fmaf(wv, s_dt[j], row[a]);
+                            colp[c] += wv;
+                        }
                     }
+                    *reinterpret_cast<float4*>(sM + at<64>(i, tx)) = make_float4(m[0], m[1], m[2], m[3]);
                 }
-                *reinterpret_cast<float4*>(sM + at<64>(i, tx)) = make_float4(m[0], m[1], m[2], m[3]);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) row[a] += __shfl_xor_sync(0xffffffffu, row[a], o);
+                    if (tx == 0) s_row[4 * ty + a] = row[a];
+                    colp[a] += __shfl_xor_sync(0xffffffffu, colp[a], 16);
+                    if (lane < 16) s_col[warp * kQ + 4 * tx + a] = colp[a];
+                }
             }
+            asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+            // ---- dx and F (rows j = 4 ty + a, columns p = 4 tx + b)
+            {
+                float v[4][4] = {}, uu[4][4] = {};
+                mm_nt<N>(sB, sG, ty, tx, v);
+                mm_tn<kP>(sM, sY, ty, tx, uu);
+                const float Dh = p.a.D[h];
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+                for (int a = 0; a < 4; ++a) {
+                    const int j = 4 * ty + a;
+                    const float4 x4 = ld4(sX + at<64>(j, tx)), y4 = ld4(sY + at<64>(j, tx));
+                    const float wj = s_w[j], dtj = s_dt[j];
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) row[a] += __shfl_xor_sync(0xffffffffu, row[a], o);
-                if (tx == 0) s_row[4 * ty + a] = row[a];
-                colp[a] += __shfl_xor_sync(0xffffffffu, colp[a], 16);
-                if (lane < 16) s_col[warp * kQ + 4 * tx + a] = colp[a];
+                    for (int c = 0; c < 4; ++c) v[a][c] *= wj;
+                    float f = x4.x * v[a][0] + x4.y * v[a][1] + x4.z * v[a][2] + x4.w * v[a][3];
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+                    if (tx == 0) s_F[j] = f;
+                    const float4 o4 = make_float4(fmaf(dtj, uu[a][0] + v[a][0], Dh * y4.x),
+                                                  fmaf(dtj, uu[a][1] + v[a][1], Dh * y4.y),
+                                                  fmaf(dtj, uu[a][2] + v[a][2], Dh * y4.z),
+                                                  fmaf(dtj, uu[a][3] + v[a][3], Dh * y4.w));
+                    if (j < valid) st4(static_cast<TIO*>(p.a.dx) + ((tok + j) * H + h) * kP + 4 * tx, o4);
+                }
             }
-        }
-        __syncthreads();
-        // ---- dx and F (rows j = 4 ty + a, columns p = 4 tx + b)
-        {
-            float v[4][4] = {}, uu[4][4] = {};
-            mm_nt<N>(sB, sG, ty, tx, v);
-            mm_tn<kP>(sM, sY, ty, tx, uu);
-            const float Dh = p.a.D[h];
+        } else {
+            // ---- E
+            {
+                float v[4][4] = {};
+                mm_nt<N>(sC, sH, ty, tx, v);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int j = 4 * ty + a;
-                const float4 x4 = ld4(sX + at<64>(j, tx)), y4 = ld4(sY + at<64>(j, tx));
-                const float wj = s_w[j], dtj = s_dt[j];
+                for (int a = 0; a < 4; ++a) {
+                    const int i = 4 * ty + a;
+                    const float4 y4 = ld4(sY + at<64>(i, tx));
+                    float f = y4.x * v[a][0] + y4.y * v[a][1] + y4.z * v[a][2] + y4.w * v[a][3];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[a][c] *= wj;
-                float f = x4.x * v[a][0] + x4.y * v[a][1] + x4.z * v[a][2] + x4.w * v[a][3];
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-                if (tx == 0) s_F[j] = f;
-                const float4 o4 = make_float4(fmaf(dtj, uu[a][0] + v[a][0], Dh * y4.x),
-                                              fmaf(dtj, uu[a][1] + v[a][1], Dh * y4.y),
-                                              fmaf(dtj, uu[a][2] + v[a][2], Dh * y4.z),
-                                              fmaf(dtj, uu[a][3] + v[a][3], Dh * y4.w));
-                if (j < valid) st4(static_cast<TIO*>(p.a.dx) + ((tok + j) * H + h) * kP + 4 * tx, o4);
+                    for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+                    if (tx == 0) s_E[i] = f * s_e[i];
+                }
             }
-        }
-        // ---- E
-        {
-            float v[4][4] = {};
-            mm_nt<N>(sC, sH, ty, tx, v);
+            // ---- the states' parts of dC and dB
+            {
+                float sc[4], sb[4];
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int i = 4 * ty + a;
-                const float4 y4 = ld4(sY + at<64>(i, tx));
-                float f = y4.x * v[a][0] + y4.y * v[a][1] + y4.z * v[a][2] + y4.w * v[a][3];
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-                if (tx == 0) s_E[i] = f * s_e[i];
+                for (int a = 0; a < 4; ++a) sc[a] = s_e[4 * ty + a], sb[a] = s_w[4 * ty + a] * s_dt[4 * ty + a];
+                mm_nn<N>(sY, sH, ty, tx, sc, dC);
+                mm_nn<N>(sX, sG, ty, tx, sb, dB);
             }
-        }
-        // ---- the states' parts of dC and dB
-        {
-            float sc[4], sb[4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) sc[a] = s_e[4 * ty + a], sb[a] = s_w[4 * ty + a] * s_dt[4 * ty + a];
-            mm_nn<N>(sY, sH, ty, tx, sc, dC);
-            mm_nn<N>(sX, sG, ty, tx, sb, dB);
         }
         __syncthreads();
         // ---- ddt, two tokens a lane of warp 0
         if (warp == 0) {
             float zz = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) zz += s_z[k];
+            for (int k = 0; k < 16; ++k) zz += s_z[k];
             zz *= s_e[kQ - 1];
             float col[2], rc[2], f[2], dtv[2];
 #pragma unroll
@@ -446,10 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_chunk_kernel(const SimtBw
     }
     // ---- the pairs' parts of dC and dB, from the sum of dS over the heads
     __syncthreads();
+    if (pairs) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-        *reinterpret_cast<float4*>(sM + at<64>(4 * ty + a, tx)) = make_float4(dS[a][0], dS[a][1], dS[a][2], dS[a][3]);
+        for (int a = 0; a < 4; ++a)
+            *reinterpret_cast<float4*>(sM + at<64>(4 * ty + a, tx)) = make_float4(dS[a][0], dS[a][1], dS[a][2], dS[a][3]);
+    }
     __syncthreads();
+    if (pairs) return;
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     mm_nn<N>(sM, sB, ty, tx, one, dC);
     mm_tn<N>(sM, sC, ty, tx, dB);
@@ -507,10 +523,13 @@ ssd_bwd_head_sums_kernel(const float* pA, const float* pD, const float* pb, int 
     }
 }
 
+// once, thread-safely
 int bwd_sm_count() {
     static const int n = [] {
-        int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess || v < 1) v = 148;
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            v <= 0)
+            v = 148;
         return v;
     }();
     return n;
@@ -568,7 +587,7 @@ int run_simt(const SimtBwd& p, cudaStream_t s) {
         const int smem = MainSmem<N>::kFloats * 4;
         if (const int st = smem_limit_once((const void*)ssd_bwd_chunk_kernel<TIO, N>, smem)) return st;
         LaunchScope ls("ssd_bwd_chunk", s);
-        ssd_bwd_chunk_kernel<TIO, N><<<(unsigned)((size_t)p.a.b * p.nc * p.a.G * p.splits), kThreads, smem, s>>>(p);
+        ssd_bwd_chunk_kernel<TIO, N><<<(unsigned)((size_t)p.a.b * p.nc * p.a.G * p.splits), 2 * kThreads, smem, s>>>(p);
         SSD_CUDA_TRY(cudaGetLastError());
     }
     if (p.splits > 1) {
