@@ -737,6 +737,17 @@ static Range norm_range(const NormMat& m, long long rows, int D) {
     return {m.p, ((size_t)(rows - 1) * (size_t)m.ld + (size_t)D) * m.elem};
 }
 
+// Do two matrices share an element?  Rows of the same stride in bytes may lie side by side, as two
+// column slices of one buffer do.
+static bool mats_overlap(const NormMat& a, const NormMat& b, long long rows, int D) {
+    if (!overlaps(norm_range(a, rows, D), norm_range(b, rows, D))) return false;
+    const size_t ld = (size_t)a.ld * a.elem, na = (size_t)D * a.elem, nb = (size_t)D * b.elem;
+    if (ld != (size_t)b.ld * b.elem) return true;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const size_t d = pb >= pa ? (pb - pa) % ld : (ld - (pa - pb) % ld) % ld;  // b's column in a's rows
+    return d < na || d + nb > ld;
+}
+
 // Shapes, pointers and overlaps of a norm call.  `inplace` names a pair (input, output) that may
 // be the same memory with the same stride.
 static int check_norm(long long rows, int D, int groups, int io, int res_dtype, float eps, const NormMat* mats, int n,
@@ -762,6 +773,8 @@ static int check_norm(long long rows, int D, int groups, int io, int res_dtype, 
         }
         if ((uintptr_t)m.p % m.elem) return set_error(SSD_ERR_INVALID_ARG, "%s is not aligned to its elements", m.name);
         if (m.ld < D) return set_error(SSD_ERR_INVALID_ARG, "%s has a row stride of %lld, below D=%d", m.name, m.ld, D);
+        if (m.ld > (1LL << 56) / rows)
+            return set_error(SSD_ERR_INVALID_ARG, "%s: %lld rows %lld apart pass the address space", m.name, rows, m.ld);
     }
     const Range rw{weight, (size_t)D * 4}, rdw{dweight, dweight ? (size_t)D * 4 : 0};
     if (overlaps(rdw, rw)) return set_error(SSD_ERR_INVALID_ARG, "dweight overlaps weight");
@@ -773,7 +786,7 @@ static int check_norm(long long rows, int D, int groups, int io, int res_dtype, 
         for (int j = 0; j < n; ++j) {
             if (j == i || (mats[j].written && j < i)) continue;
             if (i == inplace_out && j == inplace_in && mats[i].p == mats[j].p && mats[i].ld == mats[j].ld) continue;
-            if (overlaps(ri, norm_range(mats[j], rows, D)))
+            if (mats_overlap(mats[i], mats[j], rows, D))
                 return set_error(SSD_ERR_INVALID_ARG, "%s overlaps %s", mats[i].name, mats[j].name);
         }
     }

@@ -1187,10 +1187,13 @@ __global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __g
     }
 }
 
+// once, thread-safely
 int tc_sm_count() {
     static const int n = [] {
-        int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess || v < 1) v = 148;
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            v <= 0)
+            v = 148;
         return v;
     }();
     return n;

@@ -37,10 +37,13 @@ constexpr int kPairThreads = 640;   // blocks up to here are built with more reg
 constexpr int kMaxBlocksPerSM = 8;
 constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
 
+// once, thread-safely
 int norm_sm_count() {
     static const int n = [] {
-        int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess || v < 1) v = 148;
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            v <= 0)
+            v = 148;
         return v;
     }();
     return n;
@@ -540,7 +543,9 @@ constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
 // (`vec`); otherwise elements are read one by one, in pairs.  A thread takes one vector of a segment
 // up to 1024 threads and two beyond: more threads with one vector each measured faster than fewer
 // with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
-Shape norm_shape(long long rows, int groups, int L, bool vec, int resident) {
+// `ld`: the longest row stride in bytes.  The rows of a block's segments start within 2^32 bytes of
+// its first one's (a thread's offset has 32 bits), or the block takes one segment at a time.
+Shape norm_shape(long long rows, int groups, int L, bool vec, int resident, long long ld) {
     Shape s;
     s.V = vec ? 8 : 2;
     const int n = (L + s.V - 1) / s.V;
@@ -553,6 +558,10 @@ Shape norm_shape(long long rows, int groups, int L, bool vec, int resident) {
     if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
     else if (!vec) resident = kFwdThreads;
     const int per_sm = std::max(1, std::min(kMaxBlocksPerSM, resident / thr));
+    if (s.seg > 1 && ld > ((1LL << 32) - 4LL * L) / (s.seg - 1)) {
+        s.seg = 1;
+        s.smem = 2 * sizeof(float2) * 32;
+    }
     const long long want = (rows + s.seg - 1) / s.seg;
     s.blocks = (int)std::min(want, std::max<long long>(1, (long long)norm_sm_count() * per_sm / groups));
     return s;
@@ -595,7 +604,7 @@ size_t norm_workspace_bytes(long long rows, int D, int groups) {
     size_t parts = 0;
     for (int v = 0; v < 2; ++v) {
         if (v && L % 8) continue;
-        const Shape s = norm_shape(rows, groups, L, v != 0, kBwdThreads);
+        const Shape s = norm_shape(rows, groups, L, v != 0, kBwdThreads, 0);
         parts = std::max(parts, (size_t)s.blocks * s.seg);
     }
     return round_up(parts * D * sizeof(float), 256);
@@ -607,7 +616,7 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, kFwdThreads);
+    const Shape sh = norm_shape(rows, 1, D, vec, kFwdThreads, std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0}));
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -623,7 +632,8 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(r, ld_r, rb) && vec_ok(dro, ld_dro, rb) &&
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, kBwdThreads);
+    const Shape sh = norm_shape(rows, 1, D, vec, kBwdThreads, std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0,
+                                                                      dres ? ld_dres * rb : 0}));
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
     const char* name = "ssd_residual_norm_backward";
@@ -644,7 +654,7 @@ int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first,
                       cudaStream_t s) {
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) && vec_ok(out, ld_out, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, kGatedThreads);
+    const Shape sh = norm_shape(rows, groups, L, vec, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
     const GateFwd p{y, z, w, out, rows, ld_y, ld_z, ld_out, D, L, eps};
     const char* name = "ssd_gated_norm";
     if (io == SSD_F32)
@@ -661,7 +671,7 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, kBwdThreads);
+    const Shape sh = norm_shape(rows, groups, L, vec, kBwdThreads, std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
     const char* name = "ssd_gated_norm_backward";

@@ -61,6 +61,22 @@ def test_norm_refusals(call, kw, status):
     assert ssd.last_error() != ""
 
 
+def test_norm_refuses_rows_beyond_the_address_space():
+    for call in (lambda: fwd(rows=1 << 40, lx=1 << 40), lambda: fwd(rows=1 << 62, lx=64),
+                 lambda: gate(rows=1 << 33, lo=1 << 33), lambda: bwd(rows=1 << 31, ld=1 << 31)):
+        assert call() == INVALID
+        assert "address space" in ssd.last_error()
+
+
+def test_norm_overlap_of_column_slices():
+    """Slices of one buffer that share a row's columns are refused, whichever starts first."""
+    a, b = ctypes.c_void_p(0x10000000 + 96), ctypes.c_void_p(0x10000000)
+    for y, out in ((a, b), (b, a)):
+        assert gate(y=y, ly=128, out=out, lo=128) == INVALID  # 64 columns of 2 bytes, 48 apart
+        assert "overlaps" in ssd.last_error()
+    assert gate(y=b, ly=256, out=ctypes.c_void_p(0x10000000 + 128), lo=128) == INVALID  # other strides
+
+
 def test_norm_no_rows_needs_no_matrices():
     assert fwd(rows=0, x=None, out=None, ro=None, r=None) == OK
     assert gate(rows=0, y=None, z=None, out=None) == OK

@@ -173,6 +173,46 @@ def test_strided_operands(io, offset):
     close(out, oo, omag, "out")
 
 
+def test_side_by_side_in_one_buffer():
+    """Both gradients as column slices of one buffer, and a result beside its operand."""
+    g = gen(21)
+    rows, D = 45, 320
+    y, z, dout = (rand(g, rows, D, dtype=BF) for _ in range(3))
+    w = 1 + 0.1 * rand(g, D)
+    want = ssd.gated_norm_backward(dout, y, z, w)
+    buf = torch.zeros(rows, 2 * D + 16, dtype=BF, device="cuda")
+    dy, dz, dw = ssd.gated_norm_backward(dout, y, z, w, dy=buf[:, :D], dz=buf[:, D + 8:2 * D + 8])
+    assert torch.equal(dy, want[0]) and torch.equal(dz, want[1]) and torch.equal(dw, want[2])
+    assert (buf[:, D:D + 8] == 0).all() and (buf[:, 2 * D + 8:] == 0).all()
+    pair = torch.cat([y, y], 1)
+    ssd.gated_norm(pair[:, :D], z, w, out=pair[:, D:])
+    assert torch.equal(pair[:, D:], ssd.gated_norm(y, z, w)) and torch.equal(pair[:, :D], y)
+
+
+@pytest.mark.parametrize("D,offset", [(32, 0), (31, 1)])
+def test_rows_beyond_32_bit_offsets(D, offset):
+    """Short rows so far apart that those side by side in a block pass 2^32 bytes; the same values
+    packed give the same bits (the sums of a row do not depend on its place)."""
+    g = gen(22)
+    rows, ld = 11, (1 << 29) + 8  # bf16: 1 GiB and 16 bytes apart
+    store = torch.empty((rows - 1) * ld + 64, dtype=BF, device="cuda")
+    far = store.as_strided((rows, D), (ld, 1), offset)
+    x, res, dout, w = rand(g, rows, D, dtype=BF), rand(g, rows, D), rand(g, rows, D, dtype=BF), 1 + 0.1 * rand(g, D)
+    far.copy_(x)
+    for a, b in zip(ssd.residual_norm(x, w, res), ssd.residual_norm(far, w, res)):
+        assert torch.equal(a, b)
+    assert torch.equal(ssd.gated_norm(dout, x, w), ssd.gated_norm(dout, far, w))
+    ref = ssd.gated_norm_backward(dout, x, x, w)
+    got = ssd.gated_norm_backward(dout, far, far, w)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    mag = gated_backward_ref(dout, x, x, w, 1, 1e-5, False)[5]  # the same 11 terms, added in two orders
+    assert ((ref[2] - got[2]).double().abs() <= 2 * 10 * U * mag).all()
+    r = res.to(BF)
+    ref = ssd.residual_norm_backward(x, r, w)
+    got = ssd.residual_norm_backward(far, r, w)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
 def test_in_place_residual_and_gradient():
     g = gen(3)
     x, res, w = rand(g, 65, 2560, dtype=BF), rand(g, 65, 2560), 1 + 0.1 * rand(g, 2560)
