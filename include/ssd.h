@@ -420,8 +420,9 @@ SSD_API int ssd_debug_starve_next_prefill_backward(unsigned long long wait_limit
  * dweight sums over the rows in an order fixed by the shape and the device: the same call gives
  * bitwise the same result.  It needs a workspace of ssd_norm_backward_workspace_size(rows, D,
  * groups) bytes (groups = 1 for the residual norm); without dweight the workspace may be NULL.
- * Written buffers must overlap nothing else, apart from the in-place pairs named above (same
- * pointer and stride); a strided buffer counts from its first element to its last.
+ * Written buffers must share no element with another, apart from the in-place pairs named above
+ * (same pointer and stride).  Column slices of one buffer may stand side by side where their rows
+ * are equally many bytes apart; otherwise a strided buffer counts from its first element to its last.
  * Errors: SSD_ERR_INVALID_ARG (null or misaligned pointer, a negative size, D % groups, a stride
  * below D, eps negative or not finite, scale not finite, a bad enum, an overlap),
  * SSD_ERR_UNSUPPORTED (a norm above 16384 elements, groups above 65535, a bf16 residual beside
