@@ -15,13 +15,14 @@
 // sums over i > j: both sums are of the same fp32 numbers, so what has to cancel does, and no
 // term of the whole sequence's length enters.
 //
-// Launches: per-token decay terms; the chunks' own states in both directions; a scan over the
-// chunks (in place: slot c ends up with the state entering chunk c, or the adjoint of the state
-// leaving it); the gradients per chunk, a block walking heads of one B/C group with dB and dC
-// in registers; sums.  Bound by the fp32 pipes: per token and head about 57,000 multiply-adds
+// Launches: decay terms and the chunks' own states in both directions; a scan over the chunks (in
+// place: slot c ends up with the state entering chunk c, or the adjoint of the state leaving
+// it); the gradients per chunk, a block walking heads of one B/C group with dB and dC in
+// registers; sums.  Bound by the fp32 pipes: per token and head about 57,000 multiply-adds
 // at N = 128 against 6 KB of state traffic.
 #include <algorithm>
 #include "backward.cuh"
+#include "tc.cuh"
 
 namespace ssd {
 namespace {
@@ -65,6 +66,7 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
 // A [kQ][W] tile from rows `stride` elements apart; rows from `valid` on are zero.
 template <int W, int kThr, typename T>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, size_t stride, int valid) {
+#pragma unroll 2
     for (int i = threadIdx.x; i < kQ * (W / 4); i += kThr) {
         const int r = i / (W / 4), c = i % (W / 4);
         const float4 v = r < valid ? ld4(src + r * stride + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -75,7 +77,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, size_t strid
 // acc[a][b] += sum_k A[4 ty + a][k] B[4 tx + b][k]  (both along rows)
 template <int K>
 __device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
-#pragma unroll 4
+#pragma unroll 1
     for (int k = 0; k < K / 4; ++k) {
         float4 av[4], bv[4];
 #pragma unroll
@@ -101,7 +103,7 @@ __device__ __forceinline__ void axpy4(float s, float4 v, float* acc) {
 template <int W>
 __device__ __forceinline__ void mm_nn(const float* A, const float* B, int ty, int tx, const float (&s)[4],
                                       float (&acc)[4][W / 16]) {
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < 16; ++k) {
         float4 av[4];
 #pragma unroll
@@ -125,7 +127,7 @@ __device__ __forceinline__ void mm_nn(const float* A, const float* B, int ty, in
 // acc[a][...] += sum_k A[k][4 ty + a] B[k][columns 4 tx .. and 64 + 4 tx ..]   (A [64][64], B [64][W])
 template <int W>
 __device__ __forceinline__ void mm_tn(const float* A, const float* B, int ty, int tx, float (&acc)[4][W / 16]) {
-#pragma unroll 4
+#pragma unroll (W == 64 ? 4 : 2)
     for (int k = 0; k < 64; ++k) {
         const float4 av = ld4(A + at<64>(k, ty));
 #pragma unroll
@@ -139,59 +141,62 @@ __device__ __forceinline__ void mm_tn(const float* A, const float* B, int ty, in
     }
 }
 
-// ---- per-token decay terms: one warp per (chunk, head), two tokens a lane
-__global__ void __launch_bounds__(kThreads) ssd_bwd_terms_kernel(const SimtBwd p) {
-    const int lane = threadIdx.x & 31, h = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
-    if (h >= p.a.H) return;
-    const int bc = blockIdx.x, bi = bc / p.nc, t0 = (bc % p.nc) * kQ;
-    const double Ah = p.a.A[h];
-    float dt[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int t = t0 + 2 * lane + k;
-        dt[k] = t < p.a.T ? dt_value(p.a.dt[((size_t)bi * p.a.T + t) * p.a.H + h], p.a.dtm, h) : 0.f;
-    }
-    const double a0 = dt[0] * Ah, a1 = dt[1] * Ah;
-    double s = a0 + a1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-    }
-    const double tot = __shfl_sync(0xffffffffu, s, 31);
-    const size_t o = ((size_t)bc * p.a.H + h) * kQ + 2 * lane;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const double c = k ? s : s - a1;
-        p.dtv[o + k] = dt[k];
-        p.cs[o + k] = c;
-        p.e[o + k] = expf((float)c);
-        p.w[o + k] = expf((float)(tot - c));
-    }
-}
-
-// ---- the chunk's own states: z = 0: sum_j dt_j w_j x_j B_j^T, z = 1: sum_i e_i dy_i C_i^T
+// ---- the chunk's decay terms and its own states: z = 0: sum_j dt_j w_j x_j B_j^T, z = 1:
+// sum_i e_i dy_i C_i^T.  Both directions need the terms; one stores them.
 template <typename TIO, int N>
 __global__ void __launch_bounds__(kThreads) ssd_bwd_chunk_states_kernel(const SimtBwd p) {
+    griddep_launch();
     extern __shared__ float sm[];
-    float *sx = sm, *sb = sm + kQ * kP;
+    float *sx = sm, *sb = sm + kQ * kP, *s_scale = sb + kQ * N;
     const int h = blockIdx.x % p.a.H, bc = blockIdx.x / p.a.H, dir = blockIdx.y;
     const int bi = bc / p.nc, t0 = (bc % p.nc) * kQ, g = h / (p.a.H / p.a.G);
     const int valid = min(kQ, p.a.T - t0);
     const size_t tok = (size_t)bi * p.a.T + t0;
+    const int lane = threadIdx.x;
+    float dt[2] = {};
+    if (lane < 32) {  // two tokens a lane
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * lane + k < valid) dt[k] = p.a.dt[(tok + 2 * lane + k) * p.a.H + h];
+    }
     const TIO* xs = static_cast<const TIO*>(dir ? p.a.dy : p.a.x) + (tok * p.a.H + h) * kP;
-    const TIO* bs = static_cast<const TIO*>(dir ? p.a.C : p.a.B) + (tok * p.a.G + g) * N;
-    load_tile<N, kThreads>(sb, bs, (size_t)p.a.G * N, valid);
-    const size_t o = (size_t)blockIdx.x * kQ;
-    for (int i = threadIdx.x; i < kQ * (kP / 4); i += kThreads) {
-        const int r = i / (kP / 4), c = i % (kP / 4);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < valid) {
-            v = ld4(xs + (size_t)r * p.a.H * kP + 4 * c);
-            const float s = dir ? p.e[o + r] : p.w[o + r] * p.dtv[o + r];
-            v.x *= s, v.y *= s, v.z *= s, v.w *= s;
+    constexpr int kRows = kThreads / (kP / 4);  // rows of x the block reads at once
+    const int xr = threadIdx.x / (kP / 4), xc = threadIdx.x % (kP / 4);
+    float4 x[kQ / kRows];
+#pragma unroll
+    for (int i = 0; i < kQ / kRows; ++i) {
+        const int r = i * kRows + xr;
+        x[i] = r < valid ? ld4(xs + (size_t)r * p.a.H * kP + 4 * xc) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    load_tile<N, kThreads>(sb, static_cast<const TIO*>(dir ? p.a.C : p.a.B) + (tok * p.a.G + g) * N, (size_t)p.a.G * N, valid);
+    if (lane < 32) {
+        const double Ah = p.a.A[h];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) dt[k] = 2 * lane + k < valid ? dt_value(dt[k], p.a.dtm, h) : 0.f;
+        const double a0 = dt[0] * Ah, a1 = dt[1] * Ah;
+        double s = a0 + a1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double v = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += v;
         }
-        *reinterpret_cast<float4*>(sx + at<64>(r, c)) = v;
+        const double tot = __shfl_sync(0xffffffffu, s, 31);
+        const size_t o = (size_t)blockIdx.x * kQ + 2 * lane;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const double c = k ? s : s - a1;
+            const float e = expf((float)c), w = expf((float)(tot - c));
+            s_scale[2 * lane + k] = dir ? e : w * dt[k];
+            if (!dir) p.dtv[o + k] = dt[k], p.cs[o + k] = c, p.e[o + k] = e, p.w[o + k] = w;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQ / kRows; ++i) {
+        const int r = i * kRows + xr;
+        const float f = s_scale[r];
+        x[i].x *= f, x[i].y *= f, x[i].z *= f, x[i].w *= f;
+        *reinterpret_cast<float4*>(sx + at<64>(r, xc)) = x[i];
     }
     __syncthreads();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -209,6 +214,8 @@ __global__ void __launch_bounds__(kThreads) ssd_bwd_chunk_states_kernel(const Si
 // ---- scan over the chunks, four state entries a thread; z = 0 forwards, z = 1 backwards
 constexpr int kAhead = 8;  // chunks loaded ahead of the dependent updates
 __global__ void __launch_bounds__(kThreads) ssd_bwd_state_scan_kernel(const SimtBwd p) {
+    griddep_launch();
+    griddep_wait();
     const int pn = kP * p.a.N, per = pn / (4 * kThreads);
     const int u = blockIdx.x / per, el = ((blockIdx.x % per) * kThreads + threadIdx.x) * 4;
     const int h = u % p.a.H, bi = u / p.a.H, dir = blockIdx.y;
@@ -240,11 +247,18 @@ __global__ void __launch_bounds__(kThreads) ssd_bwd_state_scan_kernel(const Simt
     if (dir && p.a.dh0) st4(p.a.dh0 + (size_t)u * pn + el, run);
 }
 
+// 2^v, within 2 ulp
+__device__ __forceinline__ float exp2_approx(float v) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v));
+    return v;
+}
+__device__ __noinline__ float raw_slope(float z, float lo, float hi) { return dt_slope(z, DtMap{nullptr, lo, hi, 1}); }
+
 // ---- gradients of a chunk
 template <int N> struct MainSmem {
     static constexpr int kB = 0, kC = kB + kQ * N, kH = kC + kQ * N, kG = kH + kP * N, kX = kG + kP * N,
                          kY = kX + kQ * kP, kS = kY + kQ * kP, kM = kS + kQ * kQ, kTerms = kM + kQ * kQ;
-    // per-token: cs (double), dt, e, w, row sums, column parts [8], Gm S and Gm on the diagonal, E, F;
+    // per-token: cs (two floats), dt, e, w, row sums, column parts [8], Gm S and Gm on the diagonal, E, F;
     // then the warps' sums of <h, dh>
     static constexpr int kFloats = kTerms + kQ * (2 + 3 + 1 + 8 + 2 + 2) + 16;
 };
@@ -261,7 +275,7 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
     extern __shared__ float sm[];
     float *sB = sm + SM::kB, *sC = sm + SM::kC, *sH = sm + SM::kH, *sG = sm + SM::kG, *sX = sm + SM::kX,
           *sY = sm + SM::kY, *sS = sm + SM::kS, *sM = sm + SM::kM;
-    double* s_cs = reinterpret_cast<double*>(sm + SM::kTerms);
+    float2* s_cs = reinterpret_cast<float2*>(sm + SM::kTerms);  // log2(e) cs in two parts
     float *s_dt = sm + SM::kTerms + 2 * kQ, *s_e = s_dt + kQ, *s_w = s_e + kQ;
     float* s_row = s_w + kQ;        // [kQ] sum_j W_ij
     float* s_col = s_row + kQ;      // [8 warps][kQ] parts of sum_i Gm S L (i > j)
@@ -275,7 +289,8 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
     const int split = blockIdx.x % p.splits, ug = blockIdx.x / p.splits, g = ug % G, bc = ug / G;
     const int bi = bc / p.nc, t0 = (bc % p.nc) * kQ, valid = min(kQ, T - t0);
     const size_t tok = (size_t)bi * T + t0;
-    const int h_lo = (int)((long long)split * hg / p.splits), h_hi = (int)((long long)(split + 1) * hg / p.splits);
+    const int per = hg / p.splits, more = hg % p.splits;  // heads of a split; the first `more` have one more
+    const int h_lo = split * per + min(split, more), h_hi = h_lo + per + (split < more);
 
     load_tile<N, 2 * kThreads>(sB, static_cast<const TIO*>(p.a.B) + (tok * G + g) * N, (size_t)G * N, valid);
     load_tile<N, 2 * kThreads>(sC, static_cast<const TIO*>(p.a.C) + (tok * G + g) * N, (size_t)G * N, valid);
@@ -287,6 +302,8 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float4*>(sS + at<64>(4 * ty + i, tx)) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     }
+    griddep_launch();
+    griddep_wait();  // the states; B, C and S above need none of the launches ahead
     // over the heads: the pairs' group holds dS in the first four columns of dC's registers
     float dC[4][N / 16] = {}, dB[4][N / 16] = {};
     auto& dS = dC;
@@ -298,6 +315,7 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
         load_tile<kP, 2 * kThreads>(sX, static_cast<const TIO*>(p.a.x) + (tok * H + h) * kP, (size_t)H * kP, valid);
         load_tile<kP, 2 * kThreads>(sY, static_cast<const TIO*>(p.a.dy) + (tok * H + h) * kP, (size_t)H * kP, valid);
         float z = 0.f;
+#pragma unroll 2
         for (int i = tid; i < kP * (N / 4); i += 2 * kThreads) {
             const int r = i / (N / 4), c = i % (N / 4);
             const float4 a = ld4(p.hs + u * kP * N + 4 * i), d = ld4(p.gs + u * kP * N + 4 * i);
@@ -309,7 +327,8 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) s_z[warp] = z;
         if (tid < kQ) {
-            s_cs[tid] = p.cs[u * kQ + tid];
+            const double c = p.cs[u * kQ + tid] * 1.4426950408889634;
+            s_cs[tid] = make_float2((float)c, (float)(c - (double)(float)c));
             s_dt[tid] = p.dtv[u * kQ + tid];
             s_e[tid] = p.e[u * kQ + tid];
             s_w[tid] = p.w[u * kQ + tid];
@@ -318,29 +337,29 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
         if (pairs) {
             // ---- Gm, M = S L, dS, W's sums (rows i = 4 ty + a, columns j = 4 tx + b)
             {
-                float gm[4][4] = {}, row[4] = {}, colp[4] = {};
+                float gm[4][4] = {}, row[4] = {}, colp[4] = {}, dtj[4];
+                float2 cj[4];
                 mm_nt<kP>(sY, sX, ty, tx, gm);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cj[c] = s_cs[4 * tx + c], dtj[c] = s_dt[4 * tx + c];
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     const int i = 4 * ty + a;
                     const float4 s4 = ld4(sS + at<64>(i, tx));
                     const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+                    const float2 ci = s_cs[i];
                     float m[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int j = 4 * tx + c;
-                        const float l = i >= j ? expf((float)(s_cs[i] - s_cs[j])) : 0.f;
+                        const bool low = ty > tx || (ty == tx && a >= c);  // i >= j
+                        const float l = low ? exp2_approx((ci.x - cj[c].x) + (ci.y - cj[c].y)) : 0.f;
                         m[c] = sv[c] * l;
-                        const float wv = gm[a][c] * m[c];
-                        dS[a][c] = fmaf(gm[a][c] * l, s_dt[j], dS[a][c]);
-                        if (i == j) {
-                            s_dia[j] = wv;
-                            s_dia[kQ + j] = gm[a][c];
-                        } else {
-                            row[a] = fmaf(wv, s_dt[j], row[a]);
-                            colp[c] += wv;
-                        }
+                        const float wv = a == c && ty == tx ? 0.f : gm[a][c] * m[c];  // i > j
+                        dS[a][c] = fmaf(gm[a][c] * l, dtj[c], dS[a][c]);
+                        row[a] = fmaf(wv, dtj[c], row[a]);
+                        colp[c] += wv;
                     }
+                    if (ty == tx) s_dia[i] = gm[a][a] * m[a], s_dia[kQ + i] = gm[a][a];
                     *reinterpret_cast<float4*>(sM + at<64>(i, tx)) = make_float4(m[0], m[1], m[2], m[3]);
                 }
 #pragma unroll
@@ -437,7 +456,7 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
                 float ddt = fmaf(Ah, da, s_dia[t] + col[k] + s_F[t]);
                 if (t < valid) {
                     const size_t o = (tok + t) * H + h;
-                    if (p.a.dtm.raw) ddt *= dt_slope(p.a.dt[o] + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm);
+                    if (p.a.dtm.raw) ddt *= raw_slope(p.a.dt[o] + (p.a.dtm.bias ? p.a.dtm.bias[h] : 0.f), p.a.dtm.lo, p.a.dtm.hi);
                     p.a.ddt[o] = ddt;
                     sA = fmaf(dtv[k], da, sA);
                     sD += s_dia[kQ + t];
@@ -490,37 +509,24 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
     }
 }
 
-// dB and dC from the blocks' sums, in block order
+// dB and dC from the blocks' sums, in block order (none where a group's heads are not split), and
+// the sums over the chunks
 template <typename TIO>
-__global__ void __launch_bounds__(kThreads) ssd_bwd_group_sums_kernel(const SimtBwd p) {
-    const size_t all = (size_t)p.a.b * p.a.T * p.a.G * p.a.N;
-    const size_t i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-    if (i >= all) return;
-    const float* src = p.part + (size_t)blockIdx.y * p.splits * all + i;
+__global__ void __launch_bounds__(kThreads) ssd_bwd_sums_kernel(const SimtBwd p, const HeadSums hs, int group_blocks) {
+    griddep_wait();
+    if ((int)blockIdx.x >= group_blocks) return head_sum<kThreads>(hs, blockIdx.x - group_blocks);
+    const size_t all = (size_t)p.a.b * p.a.T * p.a.G * p.a.N, i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= 2 * all) return;
+    const int which = i >= all;
+    const size_t at = i - which * all;
+    const float* src = p.part + (size_t)which * p.splits * all + at;
     float4 s = ld4(src);
+#pragma unroll 4
     for (int k = 1; k < p.splits; ++k) {
         const float4 v = ld4(src + k * all);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    st4(static_cast<TIO*>(blockIdx.y ? p.a.dC : p.a.dB) + i, s);
-}
-
-constexpr int kSumThreads = 128;
-__global__ void __launch_bounds__(kSumThreads)
-ssd_bwd_head_sums_kernel(const float* pA, const float* pD, const float* pb, int n, int H, float* dA, float* dD, float* db) {
-    __shared__ double s[kSumThreads / 32];
-    const int h = blockIdx.x, which = blockIdx.y;
-    const float* src = which == 0 ? pA : which == 1 ? pD : pb;
-    double a = 0.0;
-    for (int i = threadIdx.x; i < n; i += kSumThreads) a += src[(size_t)i * H + h];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kSumThreads / 32; ++i) a += s[i];
-        (which == 0 ? dA : which == 1 ? dD : db)[h] = (float)a;
-    }
+    st4(static_cast<TIO*>(which ? p.a.dC : p.a.dB) + at, s);
 }
 
 // once, thread-safely
@@ -567,12 +573,7 @@ template <typename TIO, int N>
 int run_simt(const SimtBwd& p, cudaStream_t s) {
     const size_t u = (size_t)p.a.b * p.nc * p.a.H;
     {
-        LaunchScope ls("ssd_bwd_terms", s);
-        ssd_bwd_terms_kernel<<<dim3(p.a.b * p.nc, (p.a.H + 7) / 8), kThreads, 0, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
-    }
-    {
-        const int smem = (kQ * kP + kQ * N) * 4;
+        const int smem = (kQ * kP + kQ * N + kQ) * 4;
         if (const int st = smem_limit_once((const void*)ssd_bwd_chunk_states_kernel<TIO, N>, smem)) return st;
         LaunchScope ls("ssd_bwd_chunk_states", s);
         ssd_bwd_chunk_states_kernel<TIO, N><<<dim3((unsigned)u, 2), kThreads, smem, s>>>(p);
@@ -580,34 +581,27 @@ int run_simt(const SimtBwd& p, cudaStream_t s) {
     }
     {
         LaunchScope ls("ssd_bwd_state_scan", s);
-        ssd_bwd_state_scan_kernel<<<dim3(p.a.b * p.a.H * (kP * N / (4 * kThreads)), 2), kThreads, 0, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_state_scan_kernel, dim3(p.a.b * p.a.H * (kP * N / (4 * kThreads)), 2), kThreads, 0, s, p));
     }
     {
         const int smem = MainSmem<N>::kFloats * 4;
         if (const int st = smem_limit_once((const void*)ssd_bwd_chunk_kernel<TIO, N>, smem)) return st;
         LaunchScope ls("ssd_bwd_chunk", s);
-        ssd_bwd_chunk_kernel<TIO, N><<<(unsigned)((size_t)p.a.b * p.nc * p.a.G * p.splits), 2 * kThreads, smem, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_chunk_kernel<TIO, N>, dim3((unsigned)((size_t)p.a.b * p.nc * p.a.G * p.splits)),
+                                2 * kThreads, smem, s, p));
     }
-    if (p.splits > 1) {
+    {
         const size_t all = (size_t)p.a.b * p.a.T * p.a.G * N;
-        LaunchScope ls("ssd_bwd_group_sums", s);
-        ssd_bwd_group_sums_kernel<TIO><<<dim3((unsigned)((all / 4 + kThreads - 1) / kThreads), 2), kThreads, 0, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        const int group_blocks = p.splits > 1 ? (int)((all / 2 + kThreads - 1) / kThreads) : 0;
+        const HeadSums hs{p.pA, p.pD, p.pb, p.a.b * p.nc, p.a.H, p.a.dA, p.a.dD, p.a.dbias};
+        LaunchScope ls("ssd_bwd_sums", s);
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_sums_kernel<TIO>, dim3((unsigned)(group_blocks + hs.blocks())), kThreads, 0, s, p, hs,
+                                group_blocks));
     }
-    return launch_bwd_head_sums(p.pA, p.pD, p.pb, p.a.b * p.nc, p.a.H, p.a.dA, p.a.dD, p.a.dbias, s);
+    return SSD_OK;
 }
 
 }  // namespace
-
-int launch_bwd_head_sums(const float* pA, const float* pD, const float* pb, int n, int H, float* dA, float* dD,
-                         float* db, cudaStream_t s) {
-    LaunchScope ls("ssd_bwd_head_sums", s);
-    ssd_bwd_head_sums_kernel<<<dim3(H, db ? 3 : 2), kSumThreads, 0, s>>>(pA, pD, pb, n, H, dA, dD, db);
-    SSD_CUDA_TRY(cudaGetLastError());
-    return SSD_OK;
-}
 
 size_t backward_simt_workspace_bytes(const BwdArgs& a) {
     SimtBwd p;
@@ -619,7 +613,7 @@ size_t backward_simt_workspace_bytes(const BwdArgs& a) {
 bool backward_simt_fits(const BwdArgs& a) {
     const unsigned long long u = (unsigned long long)a.b * ((a.T + kQ - 1) / kQ) * a.H;
     return u < (1ull << 31) && (unsigned long long)a.b * a.H * 8 < (1ull << 31) &&
-           (unsigned long long)a.b * a.T * a.G * a.N / 4 / kThreads < (1ull << 31);
+           (unsigned long long)a.b * a.T * a.G * a.N / 2 / kThreads + 3ull * a.H < (1ull << 31) - 1;
 }
 
 int launch_backward_simt(const BwdArgs& a, void* ws, cudaStream_t s) {

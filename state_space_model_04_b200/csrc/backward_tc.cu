@@ -111,6 +111,7 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t n, uint32_t site
 constexpr int kTermThreads = 256;
 __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __grid_constant__ BwdTc p) {
     const int lane = threadIdx.x & 31, h = blockIdx.y * (kTermThreads / 32) + (threadIdx.x >> 5);
+    griddep_launch();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
     if (h >= p.a.H) return;
     const int bc = blockIdx.x, bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
@@ -209,6 +210,8 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
         s_stop = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (6 << 8));
     }
+    griddep_launch();
+    griddep_wait();  // what the launches ahead wrote
     // the product of the sequence's last chunk walked only feeds the adjoint of the initial state
     const bool final = !kEnds && c0 + n == nc;
     const int products = final && !(dir && p.a.dh0) ? n - 1 : n;
@@ -577,6 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
         s_stop = 1;
         report_status(p.status, SSD_ERR_INTERNAL | (8 << 8));
     }
+    griddep_launch();
+    griddep_wait();  // what the launches ahead wrote
     // Every role walks the same items: i.k counts them (per-item barriers complete once each), n
     // the groups begun.
     if (role == ROLE_PAIR) {
@@ -1155,7 +1160,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
 // ------------------------------------------------------------------ dB, dC of split groups
 // kJoinSplit blocks per (chunk, group); a group whose heads lie in one CTA has been stored already.
 constexpr int kJoinThreads = 256, kJoinSplit = 16;
-__global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __grid_constant__ BwdTc p) {
+__global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __grid_constant__ BwdTc p, const HeadSums hs,
+                                                                       unsigned join_blocks) {
+    griddep_wait();
+    if (blockIdx.x >= join_blocks) return head_sum<kJoinThreads>(hs, (int)(blockIdx.x - join_blocks));
     const long long unit = blockIdx.x / kJoinSplit, hg = p.a.H / p.a.G, it0 = unit * hg, it1 = it0 + hg;
     // CTA x holds items [items x / ctas, items (x + 1) / ctas): the CTA of an item by that rule
     auto owner = [&](long long it) {
@@ -1281,25 +1289,23 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     }
     if (p.nseg > 1) {
         LaunchScope ls("ssd_bwd_tc_ends", s);
-        ssd_bwd_tc_state_kernel<true><<<dim3(a.b * a.H * (p.nseg - 1), 2), kSThreads, kSSmem, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<true>, dim3(a.b * a.H * (p.nseg - 1), 2), kSThreads, kSSmem, s, p));
     }
     {
         LaunchScope ls("ssd_bwd_tc_state", s);
-        ssd_bwd_tc_state_kernel<false><<<dim3(a.b * a.H * p.nseg, 2), kSThreads, kSSmem, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<false>, dim3(a.b * a.H * p.nseg, 2), kSThreads, kSSmem, s, p));
     }
     {
         LaunchScope ls("ssd_bwd_tc_main", s);
-        ssd_bwd_tc_main_kernel<<<p.ctas, kThreads, kMSmem, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_main_kernel, dim3(p.ctas), kThreads, kMSmem, s, p));
     }
     {
+        const unsigned join_blocks = (unsigned)((size_t)a.b * p.nc * a.G * kJoinSplit);
+        const HeadSums hs{p.pA, p.pD, p.pb, a.b * p.nc, a.H, a.dA, a.dD, a.dbias};
         LaunchScope ls("ssd_bwd_tc_join", s);
-        ssd_bwd_tc_join_kernel<<<(unsigned)((size_t)a.b * p.nc * a.G * kJoinSplit), kJoinThreads, 0, s>>>(p);
-        SSD_CUDA_TRY(cudaGetLastError());
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_join_kernel, dim3(join_blocks + hs.blocks()), kJoinThreads, 0, s, p, hs, join_blocks));
     }
-    return launch_bwd_head_sums(p.pA, p.pD, p.pb, a.b * p.nc, a.H, a.dA, a.dD, a.dbias, s);
+    return SSD_OK;
 }
 
 }  // namespace ssd
