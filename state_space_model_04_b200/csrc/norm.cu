@@ -33,6 +33,7 @@ namespace ssd {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kWarpThreads = 256, kWarpVectors = 4;  // blocks of a warp a segment, and its vectors a thread
 constexpr int kPairThreads = 640;   // blocks up to here are built with more registers a thread
 constexpr int kMaxBlocksPerSM = 8;
 constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
 }
 
 template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
-__global__ void __launch_bounds__(kThr) ssd_gated_norm_kernel(const GateFwd p) {
+__global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : 0) ssd_gated_norm_kernel(const GateFwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThr) ssd_gated_norm_kernel(const GateFwd p) {
 }
 
 template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
-__global__ void __launch_bounds__(kThr) ssd_gated_norm_backward_kernel(const GateBwd p) {
+__global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : kThr == kPairThreads ? 1 : 0) ssd_gated_norm_backward_kernel(const GateBwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(32 * kSumRows) ssd_norm_dweight_kernel(const f
 // threads a segment, seg segments a block, and blocks along the rows.
 struct Shape {
     int V, vpt, tps, seg, blocks;
+    bool warps;  // a warp a segment
     size_t smem;
 };
 
@@ -568,17 +570,19 @@ constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
 // with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
 // `ld`: the longest row stride in bytes.  The rows of a block's segments start within 2^32 bytes of
 // its first one's (a thread's offset has 32 bits), or the block takes one segment at a time.
-Shape norm_shape(long long rows, int groups, int L, bool vec, int resident, long long ld) {
+Shape norm_shape(long long rows, int groups, int L, bool vec, bool warps, int resident, long long ld) {
     Shape s;
     s.V = vec ? 8 : 2;
     const int n = (L + s.V - 1) / s.V;
-    s.vpt = n <= kMaxThreads ? 1 : vec ? 2 : n <= 4 * kMaxThreads ? 4 : 8;
+    s.warps = warps && vec && n > 32 && n <= 32 * kWarpVectors;
+    s.vpt = s.warps ? (n + 31) / 32 : n <= kMaxThreads ? 1 : vec ? 2 : n <= 4 * kMaxThreads ? 4 : 8;
     s.tps = ((n + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.seg = s.tps >= 256 ? 1 : std::max(1, 256 / s.tps);
     const int thr = s.tps * s.seg;
     s.smem = 2 * sizeof(float2) * s.seg * 32;
     // one wave of blocks: each holds its weights, and in the backward pass stores a part of dw
-    if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
+    if (s.warps) resident = 2 * kWarpThreads;
+    else if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
     else if (!vec) resident = kFwdThreads;
     const int per_sm = std::max(1, std::min(kMaxBlocksPerSM, resident / thr));
     if (s.seg > 1 && ld > ((1LL << 32) - 4LL * L) / (s.seg - 1)) {
@@ -613,6 +617,9 @@ int launch_dweight(const float* part, float* dw, int parts, int D, cudaStream_t 
                                                                  : kernel<A, B, 2, 1, kMaxThreads>))                   \
      : sh.V == 8 ? kernel<A, B, 8, 2, kMaxThreads>                                                                     \
      : sh.vpt == 4 ? kernel<A, B, 2, 4, kMaxThreads> : kernel<A, B, 2, 8, kMaxThreads>)
+#define SSD_NORM_PICK_GATED(kernel, A, B)                                                                              \
+    (!sh.warps ? SSD_NORM_PICK(kernel, A, B) : sh.vpt == 2 ? kernel<A, B, 8, 2, kWarpThreads>                          \
+     : sh.vpt == 3 ? kernel<A, B, 8, 3, kWarpThreads> : kernel<A, B, 8, 4, kWarpThreads>)
 
 bool vec_ok(const void* p, long long ld, int elem) {
     return !p || (aligned16(p) && (ld * elem) % 16 == 0);
@@ -625,9 +632,9 @@ bool vec_ok(const void* p, long long ld, int elem) {
 size_t norm_workspace_bytes(long long rows, int D, int groups) {
     const int L = D / groups;
     size_t parts = 0;
-    for (int v = 0; v < 2; ++v) {
+    for (int v = 0; v < 3; ++v) {
         if (v && L % 8) continue;
-        const Shape s = norm_shape(rows, groups, L, v != 0, kBwdThreads, 0);
+        const Shape s = norm_shape(rows, groups, L, v != 0, v == 2, kBwdThreads, 0);
         parts = std::max(parts, (size_t)s.blocks * s.seg);
     }
     return round_up(parts * D * sizeof(float), 256);
@@ -639,7 +646,7 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, kFwdThreads, std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0}));
+    const Shape sh = norm_shape(rows, 1, D, vec, false, kFwdThreads, std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0}));
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -655,7 +662,7 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(r, ld_r, rb) && vec_ok(dro, ld_dro, rb) &&
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, kBwdThreads, std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0,
+    const Shape sh = norm_shape(rows, 1, D, vec, false, kBwdThreads, std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0,
                                                                       dres ? ld_dres * rb : 0}));
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
@@ -677,14 +684,14 @@ int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first,
                       cudaStream_t s) {
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) && vec_ok(out, ld_out, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
+    const Shape sh = norm_shape(rows, groups, L, vec, true, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
     const GateFwd p{y, z, w, out, rows, ld_y, ld_z, ld_out, D, L, eps};
     const char* name = "ssd_gated_norm";
     if (io == SSD_F32)
-        return norm_first ? launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_kernel, float, true), sh, groups, p, s)
-                          : launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_kernel, float, false), sh, groups, p, s);
-    return norm_first ? launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_kernel, __nv_bfloat16, true), sh, groups, p, s)
-                      : launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_kernel, __nv_bfloat16, false), sh, groups, p, s);
+        return norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, true), sh, groups, p, s)
+                          : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, false), sh, groups, p, s);
+    return norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, true), sh, groups, p, s)
+                      : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, false), sh, groups, p, s);
 }
 
 int launch_gated_norm_backward(long long rows, int D, int groups, int io, int norm_first, const void* dout,
@@ -694,18 +701,18 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, kBwdThreads, std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
+    const Shape sh = norm_shape(rows, groups, L, vec, true, kBwdThreads, std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
     const char* name = "ssd_gated_norm_backward";
     int st;
     if (io == SSD_F32)
-        st = norm_first ? launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_backward_kernel, float, true), sh, groups, p, s)
-                        : launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_backward_kernel, float, false), sh, groups, p, s);
+        st = norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, true), sh, groups, p, s)
+                        : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, false), sh, groups, p, s);
     else
         st = norm_first
-                 ? launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_backward_kernel, __nv_bfloat16, true), sh, groups, p, s)
-                 : launch_norm(name, SSD_NORM_PICK(ssd_gated_norm_backward_kernel, __nv_bfloat16, false), sh, groups, p, s);
+                 ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, true), sh, groups, p, s)
+                 : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, false), sh, groups, p, s);
     if (st != SSD_OK || !dw) return st;
     return launch_dweight(static_cast<float*>(ws), dw, sh.blocks * sh.seg, D, s);
 }
