@@ -13,12 +13,16 @@
  *     depthwise conv over k-1 cached inputs, then one recurrence step
  *     h <- exp(dt*A) h + dt * x B^T, y = h C + D x (O(1) caching section), looped on the
  *     device with no host round trip per token ("Compiled on-device loops").
+ *   - ssd_prefill_backward: the gradients of the prefill.
+ *   - ssd_residual_norm, ssd_gated_norm and their backward passes: the RMS norms of the block
+ *     around the SSD.
  *
  * Conventions shared by every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library never
  *     frees or retains them past the call (a decode plan retains the pointers it was
  *     created with until it is destroyed).  Layouts are row-major (last index
- *     contiguous), densely packed, and every pointer must be 16-byte aligned.
+ *     contiguous), densely packed, and every pointer must be 16-byte aligned (the norms' matrices
+ *     excepted: strided rows, the alignment of their elements).
  *   - Scalars per head (dt, A, D), states (h0, h_final, h, conv_state) and conv
  *     parameters are fp32.  x, B, C, y (prefill) and xbc, y (decode) use the io dtype
  *     (SSD_BF16: bfloat16 payloads; SSD_F32: float).
@@ -179,11 +183,11 @@ SSD_API int ssd_prefill_context_scan(int world, int rank, int b, int H, int P, i
                                      const float* log_decay_all, float* h_in, void* stream);
 
 /* Synchronises `stream` and returns the device-side status recorded by the most recent
- * ssd_prefill or ssd_prefill_backward that used `workspace` (SSD_OK, or SSD_ERR_TIMEOUT if a bounded wait inside
- * the tensor-core kernel expired, or SSD_ERR_INTERNAL for a failed device consistency
+ * ssd_prefill or ssd_prefill_backward that used `workspace` (SSD_OK, or SSD_ERR_TIMEOUT if a
+ * bounded wait inside a tensor-core kernel expired, or SSD_ERR_INTERNAL for a failed device consistency
  * check: a dynamic shared-memory base that is not 1024-byte aligned, or a tensor-memory
  * allocation whose address never reached the CTA), then clears it; ssd_last_error names
- * the wait site or the check.  Each ssd_prefill call resets the status word first. */
+ * the wait site or the check.  Each of those calls resets the status word first. */
 SSD_API int ssd_prefill_check(void* workspace, void* stream);
 
 /* Failure-detection test hook.  Arms a one-shot fault for the next ssd_prefill in this
@@ -215,7 +219,8 @@ SSD_API int ssd_debug_force_prefill_split(int n_full, int nseg);
 /* Test and measurement hook: with on = 1, every following ssd_prefill / ssd_prefill_dt_raw
  * in this process (and ssd_prefill_workspace_size, ssd_prefill_segments,
  * ssd_prefill_whole_units) takes the fp32-FMA path even for shapes the tensor-core kernel
- * takes (and so do ssd_prefill_backward and its workspace query).  That path evaluates the chunked dual form with chunks of exactly `chunk` tokens,
+ * takes, and so do ssd_prefill_backward(_dt_raw) and their workspace query.  The prefill's fp32-FMA
+ * path evaluates the chunked dual form with chunks of exactly `chunk` tokens,
  * so it serves the literal chunk-length sweep ([CF-SSD] "Chunked recurrence": the chunk
  * size trades arithmetic intensity against sequential overhead) at any shape; it is an
  * order of magnitude slower than the tensor-core kernel.  on = 0 restores the default.

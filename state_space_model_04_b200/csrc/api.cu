@@ -758,7 +758,8 @@ static int check_norm(long long rows, int D, int groups, int io, int res_dtype, 
     if (io == SSD_F32 && res_dtype == SSD_BF16)
         return set_error(SSD_ERR_UNSUPPORTED, "a bf16 residual beside fp32 io is not implemented");
     if (rows < 0) return set_error(SSD_ERR_INVALID_ARG, "negative size rows=%lld", rows);
-    if (D < 1 || groups < 1 || D % groups) return set_error(SSD_ERR_INVALID_ARG, "D=%d groups=%d: D must be a positive multiple of groups", D, groups);
+    if (D < 1 || groups < 1 || D % groups)
+        return set_error(SSD_ERR_INVALID_ARG, "D=%d groups=%d: D must be a positive multiple of groups", D, groups);
     if (D / groups > kNormMaxLen) return set_error(SSD_ERR_UNSUPPORTED, "a norm over %d elements (at most %d)", D / groups, kNormMaxLen);
     if (groups > kMaxGridYZ) return set_error(SSD_ERR_UNSUPPORTED, "groups=%d above 65535", groups);
     if (!(eps >= 0.f) || std::isinf(eps)) return set_error(SSD_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", (double)eps);

@@ -18,8 +18,9 @@
 // Launches: decay terms and the chunks' own states in both directions; a scan over the chunks (in
 // place: slot c ends up with the state entering chunk c, or the adjoint of the state leaving
 // it); the gradients per chunk, a block walking heads of one B/C group with dB and dC in
-// registers; sums.  Bound by the fp32 pipes: per token and head about 57,000 multiply-adds
-// at N = 128 against 6 KB of state traffic.
+// registers; sums.  Bound by the fp32 pipes and the shared memory that feeds them: per token and
+// head about 57,000 multiply-adds at N = 128 against 6 KB of state traffic.  4 x 2048 tokens, 48
+// heads, N = 128, fp32: 1.89 ms, 24 TFLOP/s, a third of the fp32 pipes' rate.
 #include <algorithm>
 #include "backward.cuh"
 #include "tc.cuh"
@@ -267,9 +268,11 @@ template <typename TIO, int N>
 // Two groups of 256 threads, a 4 x 4 tile of a 64 x 64 product each, work side by side on an item:
 //   pairs   Gm, M, dS and W's sums, then U, V, dx and F
 //   states  E from C h^T, then the states' parts of dC and dB, held in registers over the heads
-// One group doing both in turn took 361 us against 321 us for 4096 tokens, 24 heads, N = 64, and 35
-// against 34 us for 512 tokens, 4 heads; at N = 128 the two are level (4 x 2048 tokens, 48 heads:
-// 1.60 and 1.62 ms).
+// One group doing both in turn took 361 us against 321 us for 4096 tokens, 24 heads, N = 64, and at
+// N = 128 the two were level.  The products are rolled loops of 80 instructions: unrolled four
+// times, the code outgrew the instruction cache (80 KB against 51 KB: 321 against 283 us, and 1.61
+// against 1.36 ms for 4 x 2048 tokens, 48 heads, N = 128).  8 x 8 tiles read half as much shared
+// memory a multiply-add but leave a warp a scheduler, or bodies of 150 instructions and more: 1.49 ms.
 __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const SimtBwd p) {
     using SM = MainSmem<N>;
     extern __shared__ float sm[];

@@ -19,8 +19,10 @@
 // stays in registers, as stored, between its reductions and its results.  A segment belongs to
 // `tps` threads of a block (blockDim.x), 8 elements a thread up to 1024 threads, blockDim.y
 // segments side by side; the block walks rows by a grid stride with its weights in registers.
-// Copies to shared memory some rows ahead (cp.async) measured slower than loads by more threads
-// (residual backward of 32768 x 2560: 246 us against 227 us).  In the backward pass the thread
+// Measured against a copy's 6.55 TB/s: residual forward 98 % and backward 96 % (32768 x 2560), gated
+// forward 77 % (16384 x 5120 in 8 groups) and backward 78 % (one group).  Copies to shared memory
+// some rows ahead (cp.async) were slower than loads by more threads (residual backward 246 us
+// against 227 us then, 212 us now).  In the backward pass the thread
 // owns the same columns of every row it sees, so dw is summed in registers over the rows, stored
 // once per block to the workspace, and a second kernel adds the blocks' sums in a fixed order (no
 // atomics: the same call gives the same bits).
@@ -52,7 +54,7 @@ int norm_sm_count() {
 
 // Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register
 // pair; here they cost more in registers and moves than they saved: gated forward of 16384 x 5120
-// took 156 us with them against 117 us.)
+// took 156 us with them against 117 us without, both before the row loaded ahead.)
 struct f2 { float x, y; };
 __device__ __forceinline__ f2 pk(float a, float b) { return {a, b}; }
 __device__ __forceinline__ f2 pk(float a) { return {a, a}; }
@@ -459,8 +461,12 @@ __global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : 0) ssd_gated_
     }
 }
 
+// (One block an SM asked for by name gives the compiler 96 registers up to 640 threads; left open it
+// takes fewer and is slower, 165 against 120 us for 30000 x 1025.  At 1024 threads it is the other way
+// round, 207 against 193 us for 8192 x 8192.)
 template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
-__global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : kThr == kPairThreads ? 1 : 0) ssd_gated_norm_backward_kernel(const GateBwd p) {
+__global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : kThr == kPairThreads ? 1 : 0)
+ssd_gated_norm_backward_kernel(const GateBwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
@@ -560,14 +566,17 @@ struct Shape {
     size_t smem;
 };
 
-// Threads an SM holds of the one-vector kernels: their registers are 48 in the residual forward pass, 56
-// in the gated one, 96 in the backward passes (which hold dw and a row ahead); 48 element by element.
+// Threads an SM holds of the one-vector kernels: their registers are up to 48 in the residual forward
+// pass, 56 in the gated one on bf16, 96 in the backward passes (which hold dw and a row ahead).
 constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
 
 // Vector accesses need every operand's row starts on 16 bytes and segments of whole vectors
 // (`vec`); otherwise elements are read one by one, in pairs.  A thread takes one vector of a segment
 // up to 1024 threads and two beyond: more threads with one vector each measured faster than fewer
 // with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
+// The gated norm's short segments (`warps`, 257 to 1024 elements) go to a warp each instead, whose
+// sums need no barrier: forward of 16384 x 5120 in 8 groups 100 us against 107 us, backward of 65536 x
+// 512 74 us against 77 us; the residual norm, bound by memory, is slower that way (102 against 93 us).
 // `ld`: the longest row stride in bytes.  The rows of a block's segments start within 2^32 bytes of
 // its first one's (a thread's offset has 32 bits), or the block takes one segment at a time.
 Shape norm_shape(long long rows, int groups, int L, bool vec, bool warps, int resident, long long ld) {
@@ -646,7 +655,8 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, false, kFwdThreads, std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0}));
+    const long long ld = std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0});
+    const Shape sh = norm_shape(rows, 1, D, vec, false, kFwdThreads, ld);
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -662,8 +672,9 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
     const int eb = io == SSD_BF16 ? 2 : 4, rb = res_dtype == SSD_BF16 ? 2 : 4;
     const bool vec = D % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(r, ld_r, rb) && vec_ok(dro, ld_dro, rb) &&
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
-    const Shape sh = norm_shape(rows, 1, D, vec, false, kBwdThreads, std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0,
-                                                                      dres ? ld_dres * rb : 0}));
+    const long long ld =
+        std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0, dres ? ld_dres * rb : 0});
+    const Shape sh = norm_shape(rows, 1, D, vec, false, kBwdThreads, ld);
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
     const char* name = "ssd_residual_norm_backward";
@@ -701,7 +712,8 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, true, kBwdThreads, std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
+    const Shape sh = norm_shape(rows, groups, L, vec, true, kBwdThreads,
+                                std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
     const char* name = "ssd_gated_norm_backward";
