@@ -9,6 +9,7 @@ library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -599,6 +600,14 @@ def _rows(t, name, dtype=None, shape=None):
     return rows, D, ld
 
 
+def _new_rows(like, dtype):
+    """A new contiguous tensor of like's shape."""
+    if dtype == like.dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
+
+
+@functools.lru_cache(maxsize=1024)  # a function of its arguments and the GPU model
 def norm_backward_workspace_size(rows, D, groups=1) -> int:
     return int(lib().ssd_norm_backward_workspace_size(rows, D, groups))
 
@@ -606,9 +615,20 @@ def norm_backward_workspace_size(rows, D, groups=1) -> int:
 def _norm_workspace(workspace, rows, D, groups, like):
     if workspace is None:
         need = norm_backward_workspace_size(rows, D, groups)
-        if need:
-            workspace = like.new_empty(need // 4)  # fp32; a multiple of 256 bytes
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        return (like.new_empty(need // 4) if need else None), need  # fp32; a multiple of 256 bytes
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _norm_stream(stream, first, **others):
+    """The call's stream, after _check_device: the device numbers are compared first, as a norm of
+    few rows is bound by the host's time."""
+    dev = first.get_device()
+    same = dev == torch.cuda.current_device()
+    for t in others.values():
+        same = same and (t is None or t.get_device() == dev)
+    if not same:
+        _check_device(first.device, **others)
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, residual_out=None, stream=None):
@@ -623,16 +643,18 @@ def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, resid
     ld_res = 0
     if residual is not None:
         _, _, ld_res = _rows(residual, "residual", None, x.shape)
+    ld_ro = ld_out = D
     if residual_out is None:
-        residual_out = torch.empty_like(x, dtype=torch.float32) if residual is None else torch.empty_like(residual)
-    _, _, ld_ro = _rows(residual_out, "residual_out", None if residual is None else residual.dtype, x.shape)
+        residual_out = _new_rows(x if residual is None else residual, torch.float32 if residual is None else residual.dtype)
+    else:
+        _, _, ld_ro = _rows(residual_out, "residual_out", None if residual is None else residual.dtype, x.shape)
     if out is None:
-        out = torch.empty_like(x)
-    _, _, ld_out = _rows(out, "out", x.dtype, x.shape)
-    _check_device(x.device, weight=weight, residual=residual, out=out, residual_out=residual_out)
+        out = _new_rows(x, x.dtype)
+    else:
+        _, _, ld_out = _rows(out, "out", x.dtype, x.shape)
+    s = _norm_stream(stream, x, weight=weight, residual=residual, out=out, residual_out=residual_out)
     st = lib().ssd_residual_norm(rows, D, io, _io(residual_out), _ptr(x), ld_x, _ptr(residual), ld_res, float(scale),
-                                 _ptr(weight), float(eps), _ptr(out), ld_out, _ptr(residual_out), ld_ro,
-                                 _stream(stream))
+                                 _ptr(weight), float(eps), _ptr(out), ld_out, _ptr(residual_out), ld_ro, s)
     _check(st, "ssd_residual_norm")
     return out, residual_out
 
@@ -649,23 +671,25 @@ def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1
     ld_dro = ld_dres = 0
     if dresidual_out is not None:
         _, _, ld_dro = _rows(dresidual_out, "dresidual_out", r.dtype, r.shape)
+    ld_dx = D
     if dx is None:
-        dx = torch.empty_like(dout)
-    _, _, ld_dx = _rows(dx, "dx", dout.dtype, dout.shape)
-    if dresidual is None and want_dresidual:
-        dresidual = torch.empty_like(r)
+        dx = _new_rows(dout, dout.dtype)
+    else:
+        _, _, ld_dx = _rows(dx, "dx", dout.dtype, dout.shape)
     if dresidual is not None:
         _, _, ld_dres = _rows(dresidual, "dresidual", r.dtype, r.shape)
+    elif want_dresidual:
+        dresidual, ld_dres = _new_rows(r, r.dtype), D
     if dweight is None:
         dweight = torch.empty_like(weight)
-    _need(dweight, "dweight", torch.float32, (D,))
+    else:
+        _need(dweight, "dweight", torch.float32, (D,))
     workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight)
-    _check_device(dout.device, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
-                  dweight=dweight, workspace=workspace)
+    s = _norm_stream(stream, dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
+                     dweight=dweight, workspace=workspace)
     st = lib().ssd_residual_norm_backward(rows, D, io, _io(r), _ptr(dout), ld_do, _ptr(r), ld_r, _ptr(weight),
                                           _ptr(dresidual_out), ld_dro, float(scale), float(eps), _ptr(dx), ld_dx,
-                                          _ptr(dresidual), ld_dres, _ptr(dweight), _ptr(workspace), ws_bytes,
-                                          _stream(stream))
+                                          _ptr(dresidual), ld_dres, _ptr(dweight), _ptr(workspace), ws_bytes, s)
     _check(st, "ssd_residual_norm_backward")
     return dx, dresidual, dweight
 
@@ -678,12 +702,14 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
     io = _io(y)
     _, _, ld_z = _rows(z, "z", y.dtype, y.shape)
     _need(weight, "weight", torch.float32, (D,))
+    ld_out = D
     if out is None:
-        out = torch.empty_like(y)
-    _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
-    _check_device(y.device, z=z, weight=weight, out=out)
+        out = _new_rows(y, y.dtype)
+    else:
+        _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
+    s = _norm_stream(stream, y, z=z, weight=weight, out=out)
     st = lib().ssd_gated_norm(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
-                              _ptr(weight), float(eps), _ptr(out), ld_out, _stream(stream))
+                              _ptr(weight), float(eps), _ptr(out), ld_out, s)
     _check(st, "ssd_gated_norm")
     return out
 
@@ -697,19 +723,23 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
     _, _, ld_y = _rows(y, "y", dout.dtype, dout.shape)
     _, _, ld_z = _rows(z, "z", dout.dtype, dout.shape)
     _need(weight, "weight", torch.float32, (D,))
+    ld_dy = ld_dz = D
     if dy is None:
-        dy = torch.empty_like(y)
-    _, _, ld_dy = _rows(dy, "dy", y.dtype, y.shape)
+        dy = _new_rows(y, y.dtype)
+    else:
+        _, _, ld_dy = _rows(dy, "dy", y.dtype, y.shape)
     if dz is None:
-        dz = torch.empty_like(y)
-    _, _, ld_dz = _rows(dz, "dz", y.dtype, y.shape)
+        dz = _new_rows(y, y.dtype)
+    else:
+        _, _, ld_dz = _rows(dz, "dz", y.dtype, y.shape)
     if dweight is None:
         dweight = torch.empty_like(weight)
-    _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, groups, weight)
-    _check_device(dout.device, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
+    else:
+        _need(dweight, "dweight", torch.float32, (D,))
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight)
+    s = _norm_stream(stream, dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
     st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
                                        _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,
-                                       _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, _stream(stream))
+                                       _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, s)
     _check(st, "ssd_gated_norm_backward")
     return dy, dz, dweight
