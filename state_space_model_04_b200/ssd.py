@@ -183,6 +183,18 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _checked_stream(stream, first, **others):
+    """The call's stream, after _check_device: the device numbers are compared first, as small calls
+    are bound by the host's time."""
+    dev = first.get_device()
+    same = dev == torch.cuda.current_device()
+    for t in others.values():
+        same = same and (t is None or t.get_device() == dev)
+    if not same:
+        _check_device(first.device, **others)
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def _io(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return SSD_BF16
@@ -309,31 +321,32 @@ def prefill_backward(dy, x, dt, A, B, C, D, h0=None, dh_final=None, grads=None, 
                              torch.empty_like(B), torch.empty_like(C), torch.empty_like(D),
                              dt.new_empty((b, H, P, N)) if want_dh0 else None,
                              None if dt_bias is None else torch.empty_like(dt_bias))
-    _need(grads.dx, "dx", x.dtype, x.shape)
-    _need(grads.ddt, "ddt", torch.float32, (b, T, H))
-    _need(grads.dA, "dA", torch.float32, (H,))
-    _need(grads.dB, "dB", x.dtype, B.shape)
-    _need(grads.dC, "dC", x.dtype, C.shape)
-    _need(grads.dD, "dD", torch.float32, (H,))
-    if grads.dh0 is not None:
-        _need(grads.dh0, "dh0", torch.float32, (b, H, P, N))
-    if grads.ddt_bias is not None:
-        if not dt_raw:
-            raise ValueError("ddt_bias belongs to the raw step only (pass dt_raw=True)")
-        _need(grads.ddt_bias, "ddt_bias", torch.float32, (H,))
+    else:
+        _need(grads.dx, "dx", x.dtype, x.shape)
+        _need(grads.ddt, "ddt", torch.float32, (b, T, H))
+        _need(grads.dA, "dA", torch.float32, (H,))
+        _need(grads.dB, "dB", x.dtype, B.shape)
+        _need(grads.dC, "dC", x.dtype, C.shape)
+        _need(grads.dD, "dD", torch.float32, (H,))
+        if grads.dh0 is not None:
+            _need(grads.dh0, "dh0", torch.float32, (b, H, P, N))
+        if grads.ddt_bias is not None:
+            if not dt_raw:
+                raise ValueError("ddt_bias belongs to the raw step only (pass dt_raw=True)")
+            _need(grads.ddt_bias, "ddt_bias", torch.float32, (H,))
     need = prefill_backward_workspace_size(b, T, H, P, N, G, io)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check_device(x.device, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
-                  workspace=workspace, **grads._asdict())
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    dx, ddt, dA, dB, dC, dD, dh0, ddt_bias = grads
+    s = _checked_stream(stream, x, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
+                        workspace=workspace, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dh0=dh0, ddt_bias=ddt_bias)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     shape = (b, T, H, P, N, G, io, _ptr(dy), _ptr(x), _ptr(dt))
-    rest = (_ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h0), _ptr(dh_final), _ptr(grads.dx), _ptr(grads.ddt))
-    sums = (_ptr(grads.dA), _ptr(grads.dB), _ptr(grads.dC), _ptr(grads.dD), _ptr(grads.dh0), _ptr(workspace), ws_bytes,
-            _stream(stream))
+    rest = (_ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h0), _ptr(dh_final), _ptr(dx), _ptr(ddt))
+    sums = (_ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dh0), _ptr(workspace), ws_bytes, s)
     if dt_raw:
         st = lib().ssd_prefill_backward_dt_raw(*shape, _ptr(dt_bias), float(dt_min), float(dt_max), *rest,
-                                               _ptr(grads.ddt_bias), *sums)
+                                               _ptr(ddt_bias), *sums)
         _check(st, "ssd_prefill_backward_dt_raw")
     else:
         st = lib().ssd_prefill_backward(*shape, *rest, *sums)
@@ -619,18 +632,6 @@ def _norm_workspace(workspace, rows, D, groups, like):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _norm_stream(stream, first, **others):
-    """The call's stream, after _check_device: the device numbers are compared first, as a norm of
-    few rows is bound by the host's time."""
-    dev = first.get_device()
-    same = dev == torch.cuda.current_device()
-    for t in others.values():
-        same = same and (t is None or t.get_device() == dev)
-    if not same:
-        _check_device(first.device, **others)
-    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
-
-
 def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, residual_out=None, stream=None):
     """The norm ahead of a block, with the residual add in it: r = residual + scale * x,
     out = r * (mean(r^2) + eps)^(-1/2) * weight over the last dimension.  x [..., D] bf16 or fp32,
@@ -652,7 +653,7 @@ def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, resid
         out = _new_rows(x, x.dtype)
     else:
         _, _, ld_out = _rows(out, "out", x.dtype, x.shape)
-    s = _norm_stream(stream, x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    s = _checked_stream(stream, x, weight=weight, residual=residual, out=out, residual_out=residual_out)
     st = lib().ssd_residual_norm(rows, D, io, _io(residual_out), _ptr(x), ld_x, _ptr(residual), ld_res, float(scale),
                                  _ptr(weight), float(eps), _ptr(out), ld_out, _ptr(residual_out), ld_ro, s)
     _check(st, "ssd_residual_norm")
@@ -685,7 +686,7 @@ def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1
     else:
         _need(dweight, "dweight", torch.float32, (D,))
     workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight)
-    s = _norm_stream(stream, dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
+    s = _checked_stream(stream, dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
                      dweight=dweight, workspace=workspace)
     st = lib().ssd_residual_norm_backward(rows, D, io, _io(r), _ptr(dout), ld_do, _ptr(r), ld_r, _ptr(weight),
                                           _ptr(dresidual_out), ld_dro, float(scale), float(eps), _ptr(dx), ld_dx,
@@ -707,7 +708,7 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
         out = _new_rows(y, y.dtype)
     else:
         _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
-    s = _norm_stream(stream, y, z=z, weight=weight, out=out)
+    s = _checked_stream(stream, y, z=z, weight=weight, out=out)
     st = lib().ssd_gated_norm(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
                               _ptr(weight), float(eps), _ptr(out), ld_out, s)
     _check(st, "ssd_gated_norm")
@@ -737,7 +738,7 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
     else:
         _need(dweight, "dweight", torch.float32, (D,))
     workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight)
-    s = _norm_stream(stream, dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
+    s = _checked_stream(stream, dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
     st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
                                        _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,
                                        _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, s)
