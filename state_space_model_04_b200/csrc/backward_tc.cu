@@ -14,8 +14,8 @@
 //                S^T = B C^T is computed once and held in registers, dB and dC accumulate in
 //                TMEM over the heads, and the pair terms dS are summed over the heads in
 //                registers and multiplied with B and C once a group.  A group's heads may lie in
-//                several CTAs; each then stores its sums in fp32 and a third pass adds them in
-//                CTA order.
+//                several CTAs; each then stores its sums in fp32 and a third pass (join) adds them
+//                in CTA order.
 //
 // Per item the main pass multiplies (rows j or i, 128 each)
 //   G^T = X dY^T,   V = B dh^T (hi, lo),   Y = C h^T (hi, lo),
@@ -29,7 +29,7 @@
 // Bound: memory, with the latency between a pass's roles close behind.  Per item the main pass
 // moves 48 KB of x, dy, dx and 64 KB of state halves, the state pass 32 KB and 64 KB.  8 x 4096
 // tokens, 80 heads: state pass 433 us (4.5 TB/s, 69 % of a copy's rate), main pass 590 us
-// (3.9 TB/s, 59 %; tensor pipe 26 %, issue slots 42 %), join 26 us.  Under a sustained load of
+// (3.9 TB/s, 59 %; tensor pipe 26 %, issue slots 42 %), join 14 us.  Under a sustained load of
 // these calls the 1000 W power limit takes the clock from 1.97 to 1.6 GHz and 1.08 ms become 1.24.
 #include <algorithm>
 #include <atomic>
@@ -58,6 +58,8 @@ struct BwdTc {
     BwdArgs a;
     int nc;                 // chunks a sequence
     int ctas;               // of the main pass
+    int per_group;          // CTAs a (chunk, group) where each CTA stays in one, or 0: an even split,
+    int each, more;         // `each` items a CTA, one more in the first `more`
     int nseg, cseg;         // the state pass's segments a sequence, chunks a segment
     float* seg_end;         // [b H][2 directions][nseg - 1][P][N] end states of segments run from zero (the first
                             // from the initial state)
@@ -528,6 +530,14 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
 
 // The items of one CTA, [lo, hi) of items = b nc H (< 2^31), in order: item (chunk bc of all
 // sequences' chunks, head h), the head's place hh in its group.  Divisions happen once.
+// First item of CTA x: the items split evenly (the first `more` CTAs hold one more), or each group's
+// heads over its CTAs.  Items are fewer than 2^31.
+__device__ __forceinline__ int first_item(const BwdTc& p, int x) {
+    if (p.per_group == 0) return x * p.each + min(x, p.more);
+    const int hg = p.a.H / p.a.G;
+    return x / p.per_group * hg + x % p.per_group * hg / p.per_group;
+}
+
 struct Walk {
     int k, n, h, hh, bc;  // k-th of n
     int H, hg;
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int role = role_of(warp), q = warp & 3;
     const int H = p.a.H, G = p.a.G, T = p.a.T, hg = H / G;
-    const int lo = (int)(p.items * blockIdx.x / p.ctas), hi = (int)(p.items * (blockIdx.x + 1) / p.ctas);
+    const int lo = first_item(p, blockIdx.x), hi = first_item(p, blockIdx.x + 1);
     uint8_t* small = smem + kMSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 336);
@@ -1161,41 +1171,40 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ dB, dC of split groups
-// kJoinSplit blocks per (chunk, group); a group whose heads lie in one CTA has been stored already.
-constexpr int kJoinThreads = 256, kJoinSplit = 16;
+// kJoinSplit blocks a (chunk, group), or, split evenly, for every place where one CTA's items end and the
+// next one's begin; where that is the first such place inside a group, they add up its parts.  One
+// vector of 4 a thread keeps enough loads in flight for few groups of many parts (8 groups of 16
+// parts: 17 us, with two vectors 24 us).
+constexpr int kJoinThreads = 256, kJoinSplit = 2 * kBlk * kN / 4 / kJoinThreads;
 __global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __grid_constant__ BwdTc p, const HeadSums hs,
                                                                        unsigned join_blocks) {
     griddep_wait();
     if (blockIdx.x >= join_blocks) return head_sum<kJoinThreads>(hs, (int)(blockIdx.x - join_blocks));
-    const long long unit = blockIdx.x / kJoinSplit, hg = p.a.H / p.a.G, it0 = unit * hg, it1 = it0 + hg;
-    // CTA x holds items [items x / ctas, items (x + 1) / ctas): the CTA of an item by that rule
-    auto owner = [&](long long it) {
-        long long x = it * p.ctas / p.items;
-        while (p.items * (x + 1) / p.ctas <= it) ++x;
-        while (p.items * x / p.ctas > it) --x;
-        return x;
-    };
-    const long long x0 = owner(it0), x1 = owner(it1 - 1);
-    if (x0 == x1) return;
-    const int g = (int)(unit % p.a.G), bc = (int)(unit / p.a.G), bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
-    const int rows = min(kBlk, p.a.T - t0);
-    constexpr int kPart = 2 * kBlk * kN / 4 / kJoinSplit;  // vectors of 4 a block
-    const int from = (int)(blockIdx.x % kJoinSplit) * kPart;
-#pragma unroll
-    for (int i = from + threadIdx.x; i < from + kPart; i += kJoinThreads) {
-        const int which = i / (kBlk * kN / 4), e = (i % (kBlk * kN / 4)) * 4, r = e / kN, c = e % kN;
-        if (r >= rows) continue;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (long long x = x0; x <= x1; ++x) {
-            // a CTA's first group sits in its slot 0, a later one (its last) in slot 1
-            const int slot = it0 <= p.items * x / p.ctas ? 0 : 1;
-            const float4 v = *reinterpret_cast<const float4*>(p.part + ((x * 2 + slot) * 2 + which) * kBlk * kN + e);
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.a.dC : p.a.dB) + (((size_t)bi * p.a.T + t0 + r) * p.a.G + g) * kN + c;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    const int hg = p.a.H / p.a.G;
+    int x0 = blockIdx.x / kJoinSplit, x1, unit, slot = 0;  // the group, and the CTAs that hold its items
+    if (p.per_group) {
+        unit = x0, x0 = unit * p.per_group, x1 = x0 + p.per_group - 1;
+    } else {
+        const int cut = first_item(p, x0 + 1);
+        unit = cut / hg;
+        const int from = first_item(p, x0), it0 = unit * hg, last = it0 + hg - 1, longer = p.more * (p.each + 1);
+        if (cut == it0 || from > it0) return;
+        x1 = last < longer ? last / (p.each + 1) : p.more + (last - longer) / p.each;
+        slot = from < it0;  // a CTA's first group sits in its slot 0, a later one (its last) in slot 1
     }
+    const int g = unit % p.a.G, bc = unit / p.a.G, bi = bc / p.nc, t0 = (bc % p.nc) * kBlk;
+    const int rows = min(kBlk, p.a.T - t0);
+    const int i = (int)(blockIdx.x % kJoinSplit) * kJoinThreads + threadIdx.x;
+    const int which = i / (kBlk * kN / 4), e = (i % (kBlk * kN / 4)) * 4, r = e / kN, c = e % kN;
+    if (r >= rows) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int x = x0; x <= x1; ++x) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part + (((size_t)x * 2 + (x == x0 ? slot : 0)) * 2 + which) * kBlk * kN + e);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? p.a.dC : p.a.dB) + (((size_t)bi * p.a.T + t0 + r) * p.a.G + g) * kN + c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
 // once, thread-safely
@@ -1208,6 +1217,26 @@ int tc_sm_count() {
         return v;
     }();
     return n;
+}
+
+// CTAs of the main pass.  An even split of the items loads the SMs best, but a CTA whose run crosses
+// from one (chunk, group) into the next begins two of them, and the groups cut are joined afterwards.
+// With few groups each can have CTAs of its own.  In units of an item's 3.2 us a crossing costs about
+// 2.5 and its join as much, a join of k parts of whole groups 0.6 + 0.07 k.  Main pass and join, split
+// evenly and by groups: 1024 items in 128 groups 71 and 54 us, 768 in 32 groups 61 and 52 us, 3072 in 64
+// groups 127 and 122 us; more groups than SMs leave the even split only.
+void plan_main(BwdTc* p) {
+    const int sms = tc_sm_count(), hg = p->a.H / p->a.G, items = (int)p->items, groups = items / hg;
+    p->ctas = std::min(items, sms);
+    p->per_group = 0;
+    const int most = (items + p->ctas - 1) / p->ctas;
+    double best = most + 5.0;
+    for (int k = 1; k <= hg && groups * (long long)k <= sms; ++k) {
+        const double cost = (hg + k - 1) / k + (k > 1 ? 0.6 + 0.07 * k : 0.0);
+        if (cost < best) best = cost, p->per_group = k;
+    }
+    if (p->per_group) p->ctas = groups * p->per_group;
+    p->each = items / p->ctas, p->more = items % p->ctas;
 }
 
 // Segments of the state pass.  A CTA walks its chunks one after another, so a pass costs about
@@ -1231,7 +1260,7 @@ size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
     p->a = a;
     p->nc = (a.T + kBlk - 1) / kBlk;
     p->items = (long long)a.b * p->nc * a.H;
-    p->ctas = (int)std::min<long long>(p->items, tc_sm_count());
+    plan_main(p);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char* r = ws ? ws + o : nullptr;
@@ -1303,7 +1332,7 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
         SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_main_kernel, dim3(p.ctas), kThreads, kMSmem, s, p));
     }
     {
-        const unsigned join_blocks = (unsigned)((size_t)a.b * p.nc * a.G * kJoinSplit);
+        const unsigned join_blocks = p.per_group == 1 ? 0 : (unsigned)(kJoinSplit * (p.per_group ? p.ctas / p.per_group : p.ctas - 1));
         const HeadSums hs{p.pA, p.pD, p.pb, a.b * p.nc, a.H, a.dA, a.dD, a.dbias};
         LaunchScope ls("ssd_bwd_tc_join", s);
         SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_join_kernel, dim3(join_blocks + hs.blocks()), kJoinThreads, 0, s, p, hs, join_blocks));

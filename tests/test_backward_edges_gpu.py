@@ -140,6 +140,19 @@ def test_long_sequences_of_few_heads(shape):
     run_case(make_prefill(b, T, H, 64, N, G, 64, dtype="bf16", h0_std=0.3, seed=sum(shape)), tc=True)
 
 
+@pytest.mark.parametrize("shape", [(1, 1500, 37, 128, 1), (1, 300, 80, 128, 1), (2, 1300, 64, 128, 8)])
+def test_heads_over_many_blocks(shape):
+    """A group's heads over several blocks in uneven parts; one head a block; more groups than SMs."""
+    b, T, H, N, G = shape
+    run_case(make_prefill(b, T, H, 64, N, G, 64, dtype="bf16", h0_std=0.3, seed=sum(shape)), tc=True)
+
+
+@pytest.mark.parametrize("shape", [(1, 700, 37, 64, 1), (1, 60, 80, 128, 1), (2, 640, 64, 64, 8)])
+def test_heads_over_many_blocks_fp32(shape):
+    b, T, H, N, G = shape
+    run_case(make_prefill(b, T, H, 64, N, G, 64, dtype="f32", h0_std=0.3, seed=sum(shape)))
+
+
 def test_bf16_on_the_fp32_pipes():
     """The hook that routes the prefill to the fp32 pipes routes its gradients too."""
     ssd.debug_force_fma_prefill(True)
