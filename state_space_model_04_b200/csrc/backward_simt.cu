@@ -20,7 +20,7 @@
 // it); the gradients per chunk, a block walking heads of one B/C group with dB and dC in
 // registers; sums.  Bound by the fp32 pipes and the shared memory that feeds them: per token and
 // head about 57,000 multiply-adds at N = 128 against 6 KB of state traffic.  4 x 2048 tokens, 48
-// heads, N = 128, fp32: 1.89 ms, 24 TFLOP/s, a third of the fp32 pipes' rate.
+// heads, N = 128, fp32: 1.82 ms, 25 TFLOP/s, a third of the fp32 pipes' rate.
 #include <algorithm>
 #include "backward.cuh"
 #include "tc.cuh"
@@ -550,9 +550,18 @@ size_t simt_layout(const BwdArgs& a, char* ws, SimtBwd* p) {
     p->nc = (a.T + kQ - 1) / kQ;
     const size_t bc = (size_t)a.b * p->nc, u = bc * a.H;
     const int hg = a.H / a.G;
-    // one block holds an SM: split a group's heads until there are two waves of blocks
-    const size_t want = 2 * (size_t)bwd_sm_count();
-    p->splits = (int)std::min<size_t>(hg, std::max<size_t>(1, (want + bc * a.G - 1) / (bc * a.G)));
+    // A block holds an SM.  More blocks a group fill the last wave better, but each begins with the
+    // group's S and ends with its dB and dC, about 0.8 of a head's time, and adds a part to the sums
+    // (64 groups of 24 heads on 148 SMs: 239 us with 2 blocks a group, 251 with 4, 297 with 5).
+    const int sms = bwd_sm_count();
+    const size_t groups = bc * a.G;
+    double best = 0.0;
+    p->splits = 1;
+    for (int n = 1; n <= hg && (n == 1 || groups * (n - 1) < 8 * (size_t)sms); ++n) {
+        const double waves = (double)((groups * n + sms - 1) / sms);
+        const double cost = waves * ((hg + n - 1) / n + 0.8) + (n > 1 ? 0.3 + 0.02 * n : 0.0);
+        if (n == 1 || cost < best) best = cost, p->splits = n;
+    }
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char* r = ws ? ws + o : nullptr;
