@@ -528,8 +528,6 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
-// The items of one CTA, [lo, hi) of items = b nc H (< 2^31), in order: item (chunk bc of all
-// sequences' chunks, head h), the head's place hh in its group.  Divisions happen once.
 // First item of CTA x: the items split evenly (the first `more` CTAs hold one more), or each group's
 // heads over its CTAs.  Items are fewer than 2^31.
 __device__ __forceinline__ int first_item(const BwdTc& p, int x) {
@@ -538,6 +536,8 @@ __device__ __forceinline__ int first_item(const BwdTc& p, int x) {
     return x / p.per_group * hg + x % p.per_group * hg / p.per_group;
 }
 
+// The items of one CTA, [lo, hi) of items = b nc H (< 2^31), in order: item (chunk bc of all
+// sequences' chunks, head h), the head's place hh in its group.  Divisions happen once.
 struct Walk {
     int k, n, h, hh, bc;  // k-th of n
     int H, hg;

@@ -195,6 +195,15 @@ def _checked_stream(stream, first, **others):
     return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
+def _scratch(like, nbytes, stream):
+    """A temporary workspace.  It is freed when the call returns: work on another stream than the
+    current one, whose memory it comes from, has to keep it from being handed out before."""
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    if stream is not None:
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return ws
+
+
 def _io(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return SSD_BF16
@@ -336,7 +345,7 @@ def prefill_backward(dy, x, dt, A, B, C, D, h0=None, dh_final=None, grads=None, 
             _need(grads.ddt_bias, "ddt_bias", torch.float32, (H,))
     need = prefill_backward_workspace_size(b, T, H, P, N, G, io)
     if workspace is None and need:
-        workspace = x.new_empty(need, dtype=torch.uint8)
+        workspace = _scratch(x, need, stream)
     dx, ddt, dA, dB, dC, dD, dh0, ddt_bias = grads
     s = _checked_stream(stream, x, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
                         workspace=workspace, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dh0=dh0, ddt_bias=ddt_bias)
@@ -625,10 +634,10 @@ def norm_backward_workspace_size(rows, D, groups=1) -> int:
     return int(lib().ssd_norm_backward_workspace_size(rows, D, groups))
 
 
-def _norm_workspace(workspace, rows, D, groups, like):
+def _norm_workspace(workspace, rows, D, groups, like, stream):
     if workspace is None:
         need = norm_backward_workspace_size(rows, D, groups)
-        return (like.new_empty(need // 4) if need else None), need  # fp32; a multiple of 256 bytes
+        return (_scratch(like, need, stream) if need else None), need
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -685,7 +694,7 @@ def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1
         dweight = torch.empty_like(weight)
     else:
         _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight)
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight, stream)
     s = _checked_stream(stream, dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
                      dweight=dweight, workspace=workspace)
     st = lib().ssd_residual_norm_backward(rows, D, io, _io(r), _ptr(dout), ld_do, _ptr(r), ld_r, _ptr(weight),
@@ -737,7 +746,7 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
         dweight = torch.empty_like(weight)
     else:
         _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight)
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight, stream)
     s = _checked_stream(stream, dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
     st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
                                        _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,

@@ -243,6 +243,25 @@ def test_streams_and_graphs(io, N):
     same(outs[0], want2)
 
 
+def test_temporary_workspace_on_another_stream():
+    """A call on a stream of its own without a workspace given: memory taken on the current stream right
+    behind the call is not the call's workspace, still in use."""
+    s = torch.cuda.Stream()
+    for io, N in (("bf16", 128), ("f32", 64)):
+        t, dy, d = draw(2, 2048, 8, N, 1, io, 54)
+        want = call(t, dy, d, check=True)
+        need = ssd.prefill_backward_workspace_size(2, 2048, 8, 64, N, 1, ssd.SSD_F32 if io == "f32" else ssd.SSD_BF16)
+        torch.cuda.synchronize()
+        for stream in (s, s.cuda_stream):
+            outs = []
+            for _ in range(4):
+                outs.append(call(t, dy, d, stream=stream))
+                torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+            torch.cuda.synchronize()
+            for o in outs:
+                same(o, want)
+
+
 def test_wait_that_runs_out():
     """The starved call gives up after its limit and says so; the next call is right."""
     t, dy, d = draw(1, 300, 2, 128, 1, "bf16", 49)

@@ -299,6 +299,23 @@ def test_other_stream_graph_and_repeat():
         assert torch.equal(a, b)
 
 
+def test_temporary_workspace_on_another_stream():
+    """Memory taken on the current stream right behind a call on another is not the call's workspace."""
+    g = gen(31)
+    x, r, w = rand(g, 20000, 2560, dtype=BF), rand(g, 20000, 2560), 1 + 0.1 * rand(g, 2560)
+    want = ssd.residual_norm_backward(x, r, w)[2], ssd.gated_norm_backward(x, x, x, w)[2]
+    need = ssd.norm_backward_workspace_size(20000, 2560)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a = ssd.residual_norm_backward(x, r, w, stream=s)[2]
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        b = ssd.gated_norm_backward(x, x, x, w, stream=s)[2]
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
 def test_gradients_against_differences():
     """Central differences of sum(out * c) along random directions, fp32."""
     g = gen(31)
