@@ -20,7 +20,7 @@
 // `tps` threads of a block (blockDim.x), 8 elements a thread up to 1024 threads, blockDim.y
 // segments side by side; the block walks rows by a grid stride with its weights in registers.
 // Measured against a copy's 6.55 TB/s: residual forward 98 % and backward 96 % (32768 x 2560), gated
-// forward 77 % (16384 x 5120 in 8 groups) and backward 78 % (one group).  Copies to shared memory
+// forward 79 % (16384 x 5120 in 8 groups) and backward 78 % (one group).  Copies to shared memory
 // some rows ahead (cp.async) were slower than loads by more threads (residual backward 246 us
 // against 227 us then, 212 us now).  In the backward pass the thread
 // owns the same columns of every row it sees, so dw is summed in registers over the rows, stored
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
 }
 
 template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
-__global__ void __launch_bounds__(kThr, kThr == kWarpThreads ? 2 : 0) ssd_gated_norm_kernel(const GateFwd p) {
+__global__ void __launch_bounds__(kThr, kThr != kWarpThreads ? 0 : sizeof(TIO) == 2 && VPT <= 3 ? 3 : 2)
+ssd_gated_norm_kernel(const GateFwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
@@ -574,12 +575,13 @@ constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
 // (`vec`); otherwise elements are read one by one, in pairs.  A thread takes one vector of a segment
 // up to 1024 threads and two beyond: more threads with one vector each measured faster than fewer
 // with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
-// The gated norm's short segments (`warps`, 257 to 1024 elements) go to a warp each instead, whose
-// sums need no barrier: forward of 16384 x 5120 in 8 groups 100 us against 107 us, backward of 65536 x
+// The gated norm's short segments (257 to 1024 elements) go to a warp each instead, whose sums need no
+// barrier, `warps` blocks of them an SM (0: never): forward of 16384 x 5120 in 8 groups 97 us against
+// 107 us (two blocks 100 us; on fp32 three blocks spill, 67 against 64 us for 65536 x 512), backward of 65536 x
 // 512 74 us against 77 us; the residual norm, bound by memory, is slower that way (102 against 93 us).
 // `ld`: the longest row stride in bytes.  The rows of a block's segments start within 2^32 bytes of
 // its first one's (a thread's offset has 32 bits), or the block takes one segment at a time.
-Shape norm_shape(long long rows, int groups, int L, bool vec, bool warps, int resident, long long ld) {
+Shape norm_shape(long long rows, int groups, int L, bool vec, int warps, int resident, long long ld) {
     Shape s;
     s.V = vec ? 8 : 2;
     const int n = (L + s.V - 1) / s.V;
@@ -590,7 +592,7 @@ Shape norm_shape(long long rows, int groups, int L, bool vec, bool warps, int re
     const int thr = s.tps * s.seg;
     s.smem = 2 * sizeof(float2) * s.seg * 32;
     // one wave of blocks: each holds its weights, and in the backward pass stores a part of dw
-    if (s.warps) resident = 2 * kWarpThreads;
+    if (s.warps) resident = (s.vpt <= 3 ? warps : 2) * kWarpThreads;
     else if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
     else if (!vec) resident = kFwdThreads;
     const int per_sm = std::max(1, std::min(kMaxBlocksPerSM, resident / thr));
@@ -643,7 +645,7 @@ size_t norm_workspace_bytes(long long rows, int D, int groups) {
     size_t parts = 0;
     for (int v = 0; v < 3; ++v) {
         if (v && L % 8) continue;
-        const Shape s = norm_shape(rows, groups, L, v != 0, v == 2, kBwdThreads, 0);
+        const Shape s = norm_shape(rows, groups, L, v != 0, v == 2 ? 2 : 0, kBwdThreads, 0);
         parts = std::max(parts, (size_t)s.blocks * s.seg);
     }
     return round_up(parts * D * sizeof(float), 256);
@@ -656,7 +658,7 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
     const long long ld = std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0});
-    const Shape sh = norm_shape(rows, 1, D, vec, false, kFwdThreads, ld);
+    const Shape sh = norm_shape(rows, 1, D, vec, 0, kFwdThreads, ld);
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -674,7 +676,7 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
     const long long ld =
         std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0, dres ? ld_dres * rb : 0});
-    const Shape sh = norm_shape(rows, 1, D, vec, false, kBwdThreads, ld);
+    const Shape sh = norm_shape(rows, 1, D, vec, 0, kBwdThreads, ld);
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
     const char* name = "ssd_residual_norm_backward";
@@ -695,7 +697,7 @@ int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first,
                       cudaStream_t s) {
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) && vec_ok(out, ld_out, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, true, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
+    const Shape sh = norm_shape(rows, groups, L, vec, io == SSD_BF16 ? 3 : 2, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
     const GateFwd p{y, z, w, out, rows, ld_y, ld_z, ld_out, D, L, eps};
     const char* name = "ssd_gated_norm";
     if (io == SSD_F32)
@@ -712,7 +714,7 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, true, kBwdThreads,
+    const Shape sh = norm_shape(rows, groups, L, vec, 2, kBwdThreads,
                                 std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
