@@ -52,9 +52,10 @@ int norm_sm_count() {
     return n;
 }
 
-// Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register
-// pair; here they cost more in registers and moves than they saved: gated forward of 16384 x 5120
-// took 156 us with them against 117 us without, both before the row loaded ahead.)
+// Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register pair;
+// here they save issue slots and cost registers and moves: in a loop of calls residual backward of
+// 32768 x 2560 took 213 us with them against 208 us, gated backward of 16384 x 5120 170 against 172 us
+// and of 4096 x 16384 185 against 174 us.)
 struct f2 { float x, y; };
 __device__ __forceinline__ f2 pk(float a, float b) { return {a, b}; }
 __device__ __forceinline__ f2 pk(float a) { return {a, a}; }
