@@ -29,7 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
-#include "common.cuh"
+#include "tc.cuh"
 
 namespace ssd {
 namespace {
@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
     SSD_NORM_PROLOGUE(p.D)
     SSD_NORM_WEIGHT(p.w)
     SSD_NORM_DW
+    griddep_launch();
     const f2 scale2 = pk(p.scale);
     const At<const TIO> pg(static_cast<const TIO*>(p.dout), p.ld_dout);
     const At<const TRES> pr(static_cast<const TRES*>(p.r), p.ld_r), pd(static_cast<const TRES*>(p.dr_out), p.ld_dro);
@@ -473,6 +474,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
     SSD_NORM_DW
+    griddep_launch();
     const At<const TIO> pg(static_cast<const TIO*>(p.dout) + base, p.ld_dout), py(static_cast<const TIO*>(p.y) + base, p.ld_y),
         pz(static_cast<const TIO*>(p.z) + base, p.ld_z);
     const At<TIO> pdy(static_cast<TIO*>(p.dy) + base, p.ld_dy), pdz(static_cast<TIO*>(p.dz) + base, p.ld_dz);
@@ -547,6 +549,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
 // dw[c] = sum over the parts, in part order per thread row and then over the thread rows.
 __global__ void __launch_bounds__(32 * kSumRows) ssd_norm_dweight_kernel(const float* part, float* dw, int parts, int D) {
     __shared__ float s[kSumRows][33];
+    griddep_wait();  // started while the backward pass ends
     const int c = blockIdx.x * 32 + threadIdx.x;
     float a = 0.f;
     if (c < D)
@@ -616,8 +619,7 @@ int launch_norm(const char* name, K k, const Shape& sh, int groups, const Prm& p
 
 int launch_dweight(const float* part, float* dw, int parts, int D, cudaStream_t s) {
     LaunchScope ls("ssd_norm_dweight", s);
-    ssd_norm_dweight_kernel<<<(D + 31) / 32, dim3(32, kSumRows), 0, s>>>(part, dw, parts, D);
-    SSD_CUDA_TRY(cudaGetLastError());
+    SSD_CUDA_TRY(launch_pdl(ssd_norm_dweight_kernel, dim3((D + 31) / 32), dim3(32, kSumRows), 0, s, part, dw, parts, D));
     return SSD_OK;
 }
 

@@ -434,11 +434,11 @@ int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_
 // Launches `k` with programmatic stream serialization: it may start while the grid ahead of
 // it in the stream still runs, and waits (griddep_wait) where it needs that grid's results.
 template <typename... Param>
-cudaError_t launch_pdl(void (*k)(Param...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
+cudaError_t launch_pdl(void (*k)(Param...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        const Param&... prm) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
