@@ -60,10 +60,11 @@ struct BwdTc {
     int ctas;               // of the main pass
     int per_group;          // CTAs a (chunk, group) where each CTA stays in one, or 0: an even split,
     int each, more;         // `each` items a CTA, one more in the first `more`
-    int nseg, cseg;         // the state pass's segments a sequence, chunks a segment
-    float* seg_end;         // [b H][2 directions][nseg - 1][P][N] end states of segments run from zero (the first
-                            // from the initial state)
-    float* seg_decay;       // [b H][2][nseg - 1] their whole decay
+    int n_whole;            // (sequence, head) pairs the state pass walks whole; the others in
+    int nseg, cseg;         // nseg segments of cseg chunks
+    float* seg_end;         // [split pairs][2 directions][nseg - 1][P][N] end states of segments run from zero
+                            // (the first from the initial state)
+    float* seg_decay;       // [split pairs][2][nseg - 1] their whole decay
     long long items;        // b nc H
     float* terms;           // [items][kTerms][128]
     uint8_t* img_h;         // [items][kImage] state entering the chunk
@@ -186,11 +187,13 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int H = p.a.H, nc = p.nc;
-    const int segs = kEnds ? p.nseg - 1 : p.nseg;
-    const int u = blockIdx.x / segs, seg = blockIdx.x % segs, dir = blockIdx.y;
+    // the pairs walked whole first, being the longest, then the segments of the others
+    const int segs = kEnds ? p.nseg - 1 : p.nseg, dir = blockIdx.x & 1, x = (blockIdx.x >> 1) - (kEnds ? 0 : p.n_whole);
+    const bool whole = x < 0;
+    const int u = p.n_whole + (whole ? x : x / segs), seg = whole ? 0 : x % segs;
     const int h = u % H, bi = u / H, g = h / (H / p.a.G);
     // this CTA's chunks in walking order: [c0, c0 + n)
-    const int c0 = seg * p.cseg, n = min(p.cseg, nc - c0);
+    const int c0 = seg * p.cseg, n = whole ? nc : min(p.cseg, nc - c0);
     auto chunk = [&](int k) { return dir ? nc - 1 - c0 - k : c0 + k; };
     uint8_t* small = smem + kSSmall;
     uint64_t* bars = reinterpret_cast<uint64_t*>(small);
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
     } else if (warp >= 12) {
         const int q = warp & 3, r = q * 32 + lane, half = (warp - 12) >> 2, p0 = 32 * half;  // state row n, columns p0 ..
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + p0;
-        const size_t un = (size_t)u * 2 + dir;  // (sequence, head, direction)
+        const size_t un = (size_t)(u - p.n_whole) * 2 + dir;  // of the split pairs
         const size_t at = (size_t)p0 * kN + r;  // [p][n]
         const float* init = dir ? p.a.dhf : p.a.h0;
         f32x2 st[16];
@@ -1239,21 +1242,42 @@ void plan_main(BwdTc* p) {
     p->each = items / p->ctas, p->more = items % p->ctas;
 }
 
-// Segments of the state pass.  A CTA walks its chunks one after another, so a pass costs about
-// waves x (chunks a CTA + a start of two chunks' time).  More segments mean fewer chunks a CTA, but
-// the ends kernel then walks all but the last once more (without the stores: 16 us against 20 us for
-// 11 chunks), and each fold of an end is taken as a quarter of a chunk.  The cheapest count wins.
-void plan_segments(int b, int H, int nc, int* nseg, int* cseg) {
-    const double sms = tc_sm_count(), units = 2.0 * b * H;
+// Pairs of the state pass walked whole, and segments of the others.  A CTA walks its chunks one after
+// another, which costs a chunk's time each and a start of about two.  Segments fill the SMs that whole
+// pairs leave idle in their last wave, but the ends kernel walks all but the last of them once more
+// (without the stores: 16 us against 20 us for 11 chunks), and each fold of an end is taken as a
+// quarter of a chunk.  Whole pairs are scheduled first; the cheapest of a few dozen plans wins.
+void plan_segments(int b, int H, int nc, int* n_whole, int* nseg, int* cseg) {
+    const int sms = tc_sm_count(), pairs = b * H, waves = 2 * pairs / sms;
     double best = 0.0;
-    *nseg = 1, *cseg = nc;
-    for (int n = 1; n <= std::min(nc, 64); ++n) {
-        const int len = (nc + n - 1) / n, m = (nc + len - 1) / len;
-        if (m != n) continue;
-        double cost = std::ceil(units * n / sms) * (len + 2.0);
-        if (n > 1) cost += std::ceil(units * (n - 1) / sms) * (0.8 * len + 2.0) + 0.25 * (n - 1) + 2.0;
-        if (n == 1 || cost < best) best = cost, *nseg = n, *cseg = len;
+    bool first = true;
+    auto consider = [&](int whole, int n) {
+        const int len = (nc + n - 1) / n, split = pairs - whole;
+        if ((nc + len - 1) / len != n) return;
+        const double wt = nc + 2.0, st = len + 2.0 + 0.25 * (n - 1), et = 0.8 * len + 2.0;
+        const int q = 2 * whole / sms, r = 2 * whole % sms;  // full waves of whole pairs, and the SMs of one more
+        const double s = 2.0 * split * n;
+        double cost = q * wt;
+        if (s > 0.0) {
+            const double beside = (sms - r) * std::floor(r ? wt / st : 0.0);  // segments done beside the last wave
+            if (r && s <= beside) cost += std::max(wt, std::ceil(s / (sms - r)) * st);
+            else cost += (r ? wt : 0.0) + std::ceil((s - beside) / sms) * st;
+            if (n > 1) cost += std::ceil(2.0 * split * (n - 1) / sms) * et + 5.0;
+        } else if (r) {
+            cost += wt;
+        }
+        if (first || cost < best) best = cost, *n_whole = whole, *nseg = n, *cseg = len, first = false;
+    };
+    consider(pairs, 1);
+    for (int n = 2; n <= std::min(nc, 64); ++n) {
+        consider(0, n);
+        for (int w = std::max(0, waves - 1); w <= waves; ++w)
+            for (int f = 0; f < 8; ++f) {  // w waves of whole pairs and f eighths of one more
+                const int whole = (w * sms + f * sms / 8) / 2;
+                if (whole > 0 && whole < pairs) consider(whole, n);
+            }
     }
+    if (*n_whole == pairs) *nseg = 1, *cseg = nc;
 }
 
 size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
@@ -1271,8 +1295,8 @@ size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
     p->terms = reinterpret_cast<float*>(take(n * kTermBytes));
     p->img_h = reinterpret_cast<uint8_t*>(take(n * kImage));
     p->img_g = reinterpret_cast<uint8_t*>(take(n * kImage));
-    plan_segments(a.b, a.H, p->nc, &p->nseg, &p->cseg);
-    const size_t ends = (size_t)a.b * a.H * 2 * (p->nseg - 1);
+    plan_segments(a.b, a.H, p->nc, &p->n_whole, &p->nseg, &p->cseg);
+    const size_t ends = ((size_t)a.b * a.H - p->n_whole) * 2 * (p->nseg - 1);
     p->seg_end = reinterpret_cast<float*>(take(ends * kP * kN * 4));
     p->seg_decay = reinterpret_cast<float*>(take(ends * 4));
     p->part = reinterpret_cast<float*>(take((size_t)p->ctas * 4 * kBlk * kN * 4));
@@ -1319,13 +1343,14 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
         ssd_bwd_tc_terms_kernel<<<dim3(a.b * p.nc, (a.H + 7) / 8), kTermThreads, 0, s>>>(p);
         SSD_CUDA_TRY(cudaGetLastError());
     }
+    const int split = a.b * a.H - p.n_whole;
     if (p.nseg > 1) {
         LaunchScope ls("ssd_bwd_tc_ends", s);
-        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<true>, dim3(a.b * a.H * (p.nseg - 1), 2), kSThreads, kSSmem, s, p));
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<true>, dim3(2 * split * (p.nseg - 1)), kSThreads, kSSmem, s, p));
     }
     {
         LaunchScope ls("ssd_bwd_tc_state", s);
-        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<false>, dim3(a.b * a.H * p.nseg, 2), kSThreads, kSSmem, s, p));
+        SSD_CUDA_TRY(launch_pdl(ssd_bwd_tc_state_kernel<false>, dim3(2 * (p.n_whole + split * p.nseg)), kSThreads, kSSmem, s, p));
     }
     {
         LaunchScope ls("ssd_bwd_tc_main", s);

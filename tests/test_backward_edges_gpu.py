@@ -133,9 +133,10 @@ def test_absent_states(io, N, h0, dhf):
     check_grads(got, ref, bounds(t, dy, d, ref, on_tc(io, N)))
 
 
-@pytest.mark.parametrize("shape", [(1, 3000, 1, 128, 1), (1, 5000, 3, 128, 3), (2, 2049, 2, 128, 1)])
-def test_long_sequences_of_few_heads(shape):
-    """Few heads: the pass over the states splits a sequence into segments."""
+@pytest.mark.parametrize("shape", [(1, 3000, 1, 128, 1), (1, 5000, 3, 128, 3), (2, 2049, 2, 128, 1), (1, 2500, 76, 128, 2)])
+def test_long_sequences(shape):
+    """The pass over the states splits sequences into segments: all of them with few heads, and those
+    that would begin another wave of blocks with just too many."""
     b, T, H, N, G = shape
     run_case(make_prefill(b, T, H, 64, N, G, 64, dtype="bf16", h0_std=0.3, seed=sum(shape)), tc=True)
 
