@@ -442,14 +442,15 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
                 rc[k] = s_E[t] + s_row[t] - col[k] * dtv[k];
             }
             float suf = rc[0] + rc[1], pre = f[0] + f[1];  // suffix sum of rc, prefix sum of f over lanes
-            const float fs = pre;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float a = __shfl_down_sync(0xffffffffu, suf, o), c = __shfl_up_sync(0xffffffffu, pre, o);
                 if (lane + o < 32) suf += a;
                 if (lane >= o) pre += c;
             }
-            pre -= fs;
+            // the F ahead of the lane's tokens, by a shift: less their own F, the rounding of those would stay
+            pre = __shfl_up_sync(0xffffffffu, pre, 1);
+            if (lane == 0) pre = 0.f;
             float sA = 0.f, sD = 0.f, sb = 0.f;
             const float Ah = p.a.A[h];
 #pragma unroll

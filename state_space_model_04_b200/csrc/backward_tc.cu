@@ -1090,7 +1090,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             float* out = p.a.ddt + ((size_t)bi * T + t0 + lane) * H + h;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                da = carry[g] + suf[g] + (run + pre[g] - f[g]);
+                // the F ahead of the token, by a shift: less its own F, the rounding of that would stay
+                const float up = __shfl_up_sync(0xffffffffu, pre[g], 1);
+                da = carry[g] + suf[g] + (lane ? run + up : run);
                 run += __shfl_sync(0xffffffffu, pre[g], 31);
                 const float ddt = fmaf(Ah, da, dir[g]) * slope[g];
                 if (t0 + 32 * g + lane < T) {

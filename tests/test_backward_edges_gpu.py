@@ -110,6 +110,17 @@ def test_weak_and_strong_decay(io, N, scale):
 
 
 @pytest.mark.parametrize("io,N", PATHS)
+@pytest.mark.parametrize("T", [2, 66, 129])
+def test_dA_behind_strong_steps(io, N, T):
+    """With no state entering and steps that erase it, dA is what the last adjoint sends back through
+    one step's decay, many orders below x, dy and the adjoint: what a token adds to the adjoint itself
+    must leave no rounding in it."""
+    for seed in (236, 391):
+        run_case(make_prefill(1, T, 16, 64, N, 8, 64, dtype=io, h0_std=0.0, seed=seed, dt_scale=20.0), seed,
+                 tc=on_tc(io, N))
+
+
+@pytest.mark.parametrize("io,N", PATHS)
 def test_no_decay_and_zero_steps(io, N):
     """A = 0 (a plain running sum) and steps of zero length, which leave the state alone."""
     t, dy, d = draw(1, 150, 2, N, 1, io, 42)
