@@ -1,4 +1,5 @@
-"""B200-native (sm_100a) Mamba-2 SSD hot path: chunked prefill and O(1) cached decode.
+"""B200-native (sm_100a) Mamba-2 SSD hot path: chunked prefill and O(1) cached decode, with the
+prefill's gradients and the norms of the block around it.
 
 The compute lives in libssd_b200.so (hand-written CUDA for sm_100a, C ABI in
 include/ssd.h); this package is its thin Python binding.  Build it in-tree with

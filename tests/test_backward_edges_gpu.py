@@ -255,6 +255,27 @@ def test_streams_and_graphs(io, N):
     same(outs[0], want2)
 
 
+def test_two_calls_at_once():
+    """Calls of both paths and a prefill side by side on streams of their own."""
+    cases = [draw(2, 1500, 12, N, 1, io, 55) for io, N in PATHS]
+    want = [call(*c) for c in cases]
+    t = cases[3][0]
+    y = ssd.prefill(t["x"], t["dt"], t["A"], t["B"], t["C"], t["D"], h0=t["h0"])[0]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    for _ in range(6):
+        outs = []
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                outs.append(call(*c))
+        with torch.cuda.stream(streams[4]):
+            y2 = ssd.prefill(t["x"], t["dt"], t["A"], t["B"], t["C"], t["D"], h0=t["h0"])[0]
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            same(o, w)
+        assert torch.equal(y, y2)
+
+
 def test_temporary_workspace_on_another_stream():
     """A call on a stream of its own without a workspace given: memory taken on the current stream right
     behind the call is not the call's workspace, still in use."""
