@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
     SSD_NORM_PROLOGUE(p.D)
     SSD_NORM_WEIGHT(p.w)
     SSD_NORM_DW
-    griddep_launch();
+    if (p.part) griddep_launch();  // the weight gradient follows, and waits
     const f2 scale2 = pk(p.scale);
     const At<const TIO> pg(static_cast<const TIO*>(p.dout), p.ld_dout);
     const At<const TRES> pr(static_cast<const TRES*>(p.r), p.ld_r), pd(static_cast<const TRES*>(p.dr_out), p.ld_dro);
@@ -474,7 +474,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
     const int base = blockIdx.y * p.L;
     SSD_NORM_WEIGHT(p.w + base)
     SSD_NORM_DW
-    griddep_launch();
+    if (p.part) griddep_launch();  // the weight gradient follows, and waits
     const At<const TIO> pg(static_cast<const TIO*>(p.dout) + base, p.ld_dout), py(static_cast<const TIO*>(p.y) + base, p.ld_y),
         pz(static_cast<const TIO*>(p.z) + base, p.ld_z);
     const At<TIO> pdy(static_cast<TIO*>(p.dy) + base, p.ld_dy), pdz(static_cast<TIO*>(p.dz) + base, p.ld_dz);
