@@ -394,6 +394,12 @@ SSD_API int ssd_prefill_backward_dt_raw(int b, int T, int H, int P, int N, int G
  * Errors: SSD_ERR_INVALID_ARG if wait_limit_ns is outside [1e6, 1e10]. */
 SSD_API int ssd_debug_starve_next_prefill_backward(unsigned long long wait_limit_ns);
 
+/* Test hook: in the next tensor-core ssd_prefill_backward(_dt_raw) of this process one role of the
+ * main pass's warps (0 pair, 1 row, 2 MMA issue, 3 ddt, 4 store, 5 load, 6 <h, dh>) sleeps 20 us
+ * before it reads each item, so that a wait missing in another role shows.  The gradients stay the
+ * same bits.  Errors: SSD_ERR_INVALID_ARG for another role. */
+SSD_API int ssd_debug_lag_next_prefill_backward(int role);
+
 /* ------------------------------------------------------------------------------------
  * Norms around a block  (the block the SSD sits in: a norm of the residual stream ahead of
  * its input projection, a gated norm between the SSD and its output projection)

@@ -17,6 +17,7 @@ from .ssd import (  # noqa: F401
     debug_force_fma_prefill,
     debug_force_prefill_segments,
     debug_force_prefill_split,
+    debug_lag_next_prefill_backward,
     debug_starve_next_prefill,
     debug_starve_next_prefill_backward,
     decode_loop,

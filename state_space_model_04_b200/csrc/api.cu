@@ -62,6 +62,7 @@ bool backward_tc_supported(int P, int N, int io);
 size_t backward_tc_workspace_bytes(const BwdArgs& a);
 int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s);
 void backward_tc_starve_next(unsigned long long wait_ns);
+int backward_tc_lag_next(int role);
 size_t norm_workspace_bytes(long long rows, int D, int groups);
 int launch_residual_norm(long long rows, int D, int io, int res_dtype, const void* x, long long ld_x,
                          const void* res, long long ld_res, float scale, const float* w, float eps, void* out,
@@ -626,6 +627,11 @@ int ssd_debug_starve_next_prefill_backward(unsigned long long wait_limit_ns) {
         return set_error(SSD_ERR_INVALID_ARG, "wait_limit_ns %llu outside [1e6, 1e10]", wait_limit_ns);
     backward_tc_starve_next(wait_limit_ns);
     return SSD_OK;
+}
+
+int ssd_debug_lag_next_prefill_backward(int role) {
+    g_detail[0] = 0;
+    return backward_tc_lag_next(role);
 }
 
 static BwdArgs backward_shape(int b, int T, int H, int N, int G, int io) {

@@ -74,6 +74,7 @@ struct BwdTc {
     int* status;
     unsigned long long wait_ns;
     int starve;
+    int lag;                // role of the main pass that sleeps before it reads an item, or -1
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -444,6 +445,11 @@ __global__ void __launch_bounds__(kSThreads, 1) ssd_bwd_tc_state_kernel(const __
 // every wait is one call.
 constexpr int kWarps = 20, kThreads = 32 * kWarps;
 enum { ROLE_PAIR, ROLE_ROW, ROLE_ISSUER, ROLE_DDT, ROLE_STORE, ROLE_PRODUCER, ROLE_DOT };
+// Test hook: a role held back at every item shows whether the others wait for it where they have to.
+constexpr unsigned kLagNs = 20000;  // several items' time
+__device__ __forceinline__ void lag(const BwdTc& p, int role) {
+    if (p.lag == role) __nanosleep(kLagNs);
+}
 __device__ __forceinline__ int role_of(int warp) {
     const int q = warp & 3, j = warp >> 2;
     if (j < 4 - q) return ROLE_PAIR;  // c = q + j
@@ -640,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             live = wt(MB_FULLXY + s, k >> 1, 101) && (k < 2 || wt(MB_SUMEMPTY + s, (k - 2) >> 1, 102)) &&
                    wt(MB_GFULL, k, 103);
             if (!live) break;
+            lag(p, ROLE_PAIR);
             tc_fence_after();
             const float* cs2 = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + kTermCs2 * kBlk;
             float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
@@ -703,8 +710,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             arrive(MB_SUMFULL + s);
             arrive(MB_EMPTYT + s);
             if (i.last()) {
-                // dS^T [j][i] in bf16 over the h image, once the item's products have read it
-                live = wt(MB_EMPTYST, k, 104);
+                // dS^T [j][i] in bf16 over the h image, once the item's products and <h, dh> have read
+                // it.  This is the one barrier not waited for at every item, and a parity alone would
+                // take phase k - 2 for phase k while the <h, dh> warps still read item k - 1; V being
+                // done says that its states had landed, so phase k - 1 is complete
+                live = wt(MB_VDONE, k, 106) && wt(MB_EMPTYST, k, 104);
                 if (!live) break;
                 uint8_t* tile = smem + kMH;
                 if (diagonal) {
@@ -780,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const int k = i.k, s = k & 1;
             live = wt(MB_FULLXY + s, k >> 1, 110) && (k < 1 || wt(MB_DBDONE, k - 1, 111));
             if (!live) break;
+            lag(p, ROLE_ROW);
             const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
             const float er = terms[kTermE * kBlk + r], wr = terms[kTermW * kBlk + r], dtr = terms[kTermDt * kBlk + r];
             const float Dh = D_next;
@@ -892,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             for (Walk i(lo, hi, H, hg); i.more(); i.next()) {
                 const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
                 const size_t it = (size_t)(lo + k);
+                lag(p, ROLE_PRODUCER);
                 if (k >= 2 && !(w1(MB_EMPTYXY + s, (k - 2) >> 1, 60) && w1(MB_EMPTYT + s, (k - 2) >> 1, 61))) break;
                 const uint32_t f = bar(MB_FULLXY + s);
                 mbar_expect_tx(f, 2 * kRegion + kTermBytes);
@@ -967,6 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
                 const int k = i.k, s = k & 1;
                 const bool fresh = i.first();
                 const uint32_t stage = s * kReg;
+                lag(p, ROLE_ISSUER);
                 // G^T's columns: U of the item before has read M^T there
                 ok = k < 1 || w1(MB_UDONE, k - 1, 70);
                 if (!ok) break;
@@ -1044,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             A_next = p.a.A[i.next_head()];
             ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
             if (!ok) break;
+            lag(p, ROLE_DDT);
             const float* sums = reinterpret_cast<const float*>(smem + kMSums + s * kSumBytes) + lane;
             const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + lane;
             // da_t adds a prefix of F (exclusive) and a suffix of E + rows - columns.  Lane l holds
@@ -1119,6 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             for (Walk i(lo, hi, H, hg); i.more(); i.next()) {
                 const int k = i.k, s = k & 1, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
                 if (!w1(MB_DXSTAGED + s, k >> 1, 92)) break;
+                lag(p, ROLE_STORE);
                 tma_store_4d(sbase + kMX + s * kRegion, &p.tm_dx, 0, i.h, t0, bi);
                 bulk_commit();
                 bulk_wait_read0();
@@ -1136,6 +1151,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const int s = k & 1;
             ok = wt(MB_FULLST, k, 95);
             if (!ok) break;
+            lag(p, ROLE_DOT);
             const uint4 *h4 = reinterpret_cast<const uint4*>(smem + kMH), *g4 = reinterpret_cast<const uint4*>(smem + kMG);
             f32x2 z2 = 0ull, c2 = 0ull;
 #pragma unroll 2
@@ -1309,6 +1325,7 @@ size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
 }
 
 std::atomic<unsigned long long> g_starve_bwd{0};
+std::atomic<int> g_lag_bwd{-1};
 
 }  // namespace
 
@@ -1321,6 +1338,13 @@ size_t backward_tc_workspace_bytes(const BwdArgs& a) {
 
 void backward_tc_starve_next(unsigned long long wait_ns) { g_starve_bwd.store(wait_ns); }
 
+int backward_tc_lag_next(int role) {
+    if (role < 0 || role > ROLE_DOT)
+        return set_error(SSD_ERR_INVALID_ARG, "role %d outside [0, %d]", role, (int)ROLE_DOT);
+    g_lag_bwd.store(role);
+    return SSD_OK;
+}
+
 // ws: the status word at its start, the passes' scratch `offset` bytes behind it
 int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s) {
     BwdTc p;
@@ -1331,6 +1355,7 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     const unsigned long long starve = g_starve_bwd.exchange(0);
     p.starve = starve != 0;
     p.wait_ns = starve ? starve : kWaitLimitNs;
+    p.lag = g_lag_bwd.exchange(-1);
     int st;
     if ((st = make_map(&p.tm_x, a.x, kP, a.H, a.T, a.b)) != SSD_OK) return st;
     if ((st = make_map(&p.tm_dy, a.dy, kP, a.H, a.T, a.b)) != SSD_OK) return st;

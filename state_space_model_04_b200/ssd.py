@@ -64,6 +64,8 @@ def lib() -> ctypes.CDLL:
         L.ssd_debug_starve_next_prefill.restype = _i
         L.ssd_debug_starve_next_prefill_backward.argtypes = [ctypes.c_ulonglong]
         L.ssd_debug_starve_next_prefill_backward.restype = _i
+        L.ssd_debug_lag_next_prefill_backward.argtypes = [_i]
+        L.ssd_debug_lag_next_prefill_backward.restype = _i
         L.ssd_prefill_local_state_workspace_size.argtypes = [_i] * 7
         L.ssd_prefill_local_state_workspace_size.restype = _sz
         L.ssd_prefill_local_state.argtypes = [_i] * 7 + [_vp] * 7 + [_sz, _vp]
@@ -380,6 +382,12 @@ def debug_starve_next_prefill_backward(wait_limit_s=0.1):
     """The same hook for the next tensor-core prefill_backward."""
     _check(lib().ssd_debug_starve_next_prefill_backward(int(wait_limit_s * 1e9)),
            "ssd_debug_starve_next_prefill_backward")
+
+
+def debug_lag_next_prefill_backward(role):
+    """Test hook: one role of warps of the next tensor-core prefill_backward's main pass is held back at
+    every item (0 pair, 1 row, 2 MMA issue, 3 ddt, 4 store, 5 load, 6 <h, dh>); the results are the same."""
+    _check(lib().ssd_debug_lag_next_prefill_backward(int(role)), "ssd_debug_lag_next_prefill_backward")
 
 
 def prefill_local_state(x, dt, A, B, h_local=None, log_decay=None, workspace=None, stream=None):

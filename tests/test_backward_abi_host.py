@@ -85,3 +85,9 @@ def test_too_many_chunks_for_one_launch():
 @pytest.mark.parametrize("ns", [0, 999999, 10**10 + 1])
 def test_starve_limit_refusals(ns):
     assert ssd.lib().ssd_debug_starve_next_prefill_backward(ns) == INVALID
+
+
+@pytest.mark.parametrize("role", [-1, 7])
+def test_lag_role_refusals(role):
+    assert ssd.lib().ssd_debug_lag_next_prefill_backward(role) == INVALID
+    assert ssd.last_error() != ""
