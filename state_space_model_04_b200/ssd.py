@@ -5,6 +5,10 @@ module checks tensor dtypes/devices/shapes, allocates outputs and workspaces wit
 (device memory and streams are the only things torch provides) and forwards raw
 pointers to the C ABI declared in include/ssd.h.  There is no CPU fallback: if the
 library is missing or a call fails, an exception is raised.
+
+Calls run on the current stream, or on `stream`: a torch.cuda.Stream or a raw handle.  What such a call
+allocates belongs to that stream; the order between it and the current one, for the operands going in and
+the results coming out, is the caller's.
 """
 from __future__ import annotations
 
@@ -185,8 +189,8 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _checked_stream(stream, first, **others):
-    """The call's stream, after _check_device: the device numbers are compared first, as small calls
+def _checked_stream(first, **others):
+    """The current stream, after _check_device: the device numbers are compared first, as small calls
     are bound by the host's time."""
     dev = first.get_device()
     same = dev == torch.cuda.current_device()
@@ -194,16 +198,25 @@ def _checked_stream(stream, first, **others):
         same = same and (t is None or t.get_device() == dev)
     if not same:
         _check_device(first.device, **others)
-    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+    return _raw_stream(dev) if _raw_stream is not None else _stream(None)
 
 
-def _scratch(like, nbytes, stream):
-    """A temporary workspace.  It is freed when the call returns: work on another stream than the
-    current one, whose memory it comes from, has to keep it from being handed out before."""
-    ws = like.new_empty(nbytes, dtype=torch.uint8)
-    if stream is not None:
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-    return ws
+def _on(stream, call, *args):
+    """call(*args) on a stream given by name.  What the call allocates, its workspace and its results,
+    comes from that stream's memory: a block of the current stream's could still be in use by work queued
+    there, and would be handed out there again while the call runs.  The results are handed over to the
+    current stream, so that they may be dropped with its work on them still queued."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        results = call(*args)
+    if here.cuda_stream != stream.cuda_stream:
+        for t in results if isinstance(results, tuple) else (results,):
+            if t is not None:
+                t.record_stream(here)
+    return results
 
 
 def _io(t: torch.Tensor) -> int:
@@ -240,6 +253,9 @@ def prefill(x, dt, A, B, C, D, chunk=256, h0=None, y=None, h_final=None, workspa
     dt_raw=True passes dt as the raw step (ssd_prefill_dt_raw): the kernels form
     clamp(softplus(dt + dt_bias[h]), dt_min, dt_max) themselves; dt_bias [H] f32 or None.
     check=True synchronises and raises if a device-side wait recorded an error."""
+    if stream is not None:
+        return _on(stream, prefill, x, dt, A, B, C, D, chunk, h0, y, h_final, workspace, want_final, None, check, dt_raw,
+                   dt_bias, dt_min, dt_max)
     _need(x, "x")
     io = _io(x)
     b, T, H, P = x.shape
@@ -308,6 +324,9 @@ def prefill_backward(dy, x, dt, A, B, C, D, h0=None, dh_final=None, grads=None, 
     dt_raw=True, ddt is the gradient of the raw step and ddt_bias [H] that of the bias (None without
     one).  grads: a PrefillGrads whose tensors take the results instead of new ones.
     check=True synchronises and raises if a device-side wait recorded an error."""
+    if stream is not None:
+        return _on(stream, prefill_backward, dy, x, dt, A, B, C, D, h0, dh_final, grads, want_dh0, workspace, None, check,
+                   dt_raw, dt_bias, dt_min, dt_max)
     _need(x, "x")
     io = _io(x)
     b, T, H, P = x.shape
@@ -347,9 +366,9 @@ def prefill_backward(dy, x, dt, A, B, C, D, h0=None, dh_final=None, grads=None, 
             _need(grads.ddt_bias, "ddt_bias", torch.float32, (H,))
     need = prefill_backward_workspace_size(b, T, H, P, N, G, io)
     if workspace is None and need:
-        workspace = _scratch(x, need, stream)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     dx, ddt, dA, dB, dC, dD, dh0, ddt_bias = grads
-    s = _checked_stream(stream, x, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
+    s = _checked_stream(x, dy=dy, dt=dt, A=A, B=B, C=C, D=D, h0=h0, dh_final=dh_final, dt_bias=dt_bias,
                         workspace=workspace, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dh0=dh0, ddt_bias=ddt_bias)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     shape = (b, T, H, P, N, G, io, _ptr(dy), _ptr(x), _ptr(dt))
@@ -394,6 +413,8 @@ def prefill_local_state(x, dt, A, B, h_local=None, log_decay=None, workspace=Non
     """The state these tokens leave when started from zero, and their total log decay
     sum(dt * A), per (sequence, head): returns (h_local [b,H,P,N] f32, log_decay [b,H] f32).
     x [b,T,H,P] bf16, dt [b,T,H] f32, A [H] f32, B [b,T,G,N] bf16 (ssd_prefill_local_state)."""
+    if stream is not None:
+        return _on(stream, prefill_local_state, x, dt, A, B, h_local, log_decay, workspace)
     _need(x, "x", torch.bfloat16)
     b, T, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -420,6 +441,8 @@ def prefill_local_state(x, dt, A, B, h_local=None, log_decay=None, workspace=Non
 def prefill_context_scan(rank, h_local_all, log_decay_all, h0=None, h_in=None, stream=None):
     """State entering context shard `rank` from the rank-major gathered local states
     [world,b,H,P,N] and log decays [world,b,H] (ssd_prefill_context_scan)."""
+    if stream is not None:
+        return _on(stream, prefill_context_scan, rank, h_local_all, log_decay_all, h0, h_in)
     world, b, H, P, N = h_local_all.shape
     _need(h_local_all, "h_local_all", torch.float32)
     _need(log_decay_all, "log_decay_all", torch.float32, (world, b, H))
@@ -490,6 +513,8 @@ def _decode_shapes(h, conv_state, A, D, conv_w, conv_b, G):
 def decode_step(h, conv_state, xbc, dt, A, D, conv_w, conv_b, G=1, act=SSD_ACT_SILU, y=None,
                 workspace=None, stream=None):
     """One decode step for all layers; h and conv_state are updated in place.  Returns y."""
+    if stream is not None:
+        return _on(stream, decode_step, h, conv_state, xbc, dt, A, D, conv_w, conv_b, G, act, y, workspace)
     layers, b, H, P, N, k, Dc = _decode_shapes(h, conv_state, A, D, conv_w, conv_b, G)
     _need(xbc, "xbc", None, (layers, b, Dc))
     io = _io(xbc)
@@ -578,6 +603,8 @@ def decode_loop(h, conv_state, xbc_ring, dt_ring, A, D, conv_w, conv_b, n_steps,
     """Run n_steps decode steps as one graph launch (ssd_decode_loop: plan built, launched,
     released, no host synchronisation inside).  Returns y_ring [ring, layers, b, H, P]; the
     call waits for the launch before returning because its workspace is a temporary."""
+    if stream is not None:
+        return _on(stream, decode_loop, h, conv_state, xbc_ring, dt_ring, A, D, conv_w, conv_b, n_steps, G, act)
     layers, b, H, P, N, k, Dc = _decode_shapes(h, conv_state, A, D, conv_w, conv_b, G)
     ring = xbc_ring.shape[0]
     _need(xbc_ring, "xbc_ring", None, (ring, layers, b, Dc))
@@ -591,7 +618,7 @@ def decode_loop(h, conv_state, xbc_ring, dt_ring, A, D, conv_w, conv_b, n_steps,
                                _ptr(dt_ring), ring, _ptr(A), _ptr(D), _ptr(conv_w), _ptr(conv_b), _ptr(y_ring),
                                int(n_steps), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "ssd_decode_loop")
-    torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
+    torch.cuda.current_stream().synchronize()
     return y_ring
 
 
@@ -642,10 +669,10 @@ def norm_backward_workspace_size(rows, D, groups=1) -> int:
     return int(lib().ssd_norm_backward_workspace_size(rows, D, groups))
 
 
-def _norm_workspace(workspace, rows, D, groups, like, stream):
+def _norm_workspace(workspace, rows, D, groups, like):
     if workspace is None:
         need = norm_backward_workspace_size(rows, D, groups)
-        return (_scratch(like, need, stream) if need else None), need
+        return (like.new_empty(need, dtype=torch.uint8) if need else None), need
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -655,6 +682,8 @@ def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, resid
     weight [D] fp32, residual [..., D] fp32 (or bf16 beside bf16 x) or None (r = scale * x).
     Returns (out, r): out in x's type, r in the residual's (fp32 without one, or residual_out's).
     residual_out may be the residual itself (updated in place).  Operands may be slices of wider rows."""
+    if stream is not None:
+        return _on(stream, residual_norm, x, weight, residual, scale, eps, out, residual_out)
     rows, D, ld_x = _rows(x, "x")
     io = _io(x)
     _need(weight, "weight", torch.float32, (D,))
@@ -670,7 +699,7 @@ def residual_norm(x, weight, residual=None, scale=1.0, eps=1e-5, out=None, resid
         out = _new_rows(x, x.dtype)
     else:
         _, _, ld_out = _rows(out, "out", x.dtype, x.shape)
-    s = _checked_stream(stream, x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    s = _checked_stream(x, weight=weight, residual=residual, out=out, residual_out=residual_out)
     st = lib().ssd_residual_norm(rows, D, io, _io(residual_out), _ptr(x), ld_x, _ptr(residual), ld_res, float(scale),
                                  _ptr(weight), float(eps), _ptr(out), ld_out, _ptr(residual_out), ld_ro, s)
     _check(st, "ssd_residual_norm")
@@ -682,6 +711,9 @@ def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1
     """Gradients of residual_norm from r as it returned it: dout the gradient of out, dresidual_out
     that of r (None: zero).  Returns (dx, dresidual, dweight): dx in dout's type, dresidual in r's
     (None with want_dresidual=False), dweight [D] fp32.  dresidual may be dresidual_out itself."""
+    if stream is not None:
+        return _on(stream, residual_norm_backward, dout, r, weight, dresidual_out, scale, eps, dx, dresidual, dweight,
+                   want_dresidual, workspace)
     rows, D, ld_do = _rows(dout, "dout")
     io = _io(dout)
     _, _, ld_r = _rows(r, "r", None, dout.shape)
@@ -702,8 +734,8 @@ def residual_norm_backward(dout, r, weight, dresidual_out=None, scale=1.0, eps=1
         dweight = torch.empty_like(weight)
     else:
         _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight, stream)
-    s = _checked_stream(stream, dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, 1, weight)
+    s = _checked_stream(dout, r=r, weight=weight, dresidual_out=dresidual_out, dx=dx, dresidual=dresidual,
                      dweight=dweight, workspace=workspace)
     st = lib().ssd_residual_norm_backward(rows, D, io, _io(r), _ptr(dout), ld_do, _ptr(r), ld_r, _ptr(weight),
                                           _ptr(dresidual_out), ld_dro, float(scale), float(eps), _ptr(dx), ld_dx,
@@ -716,6 +748,8 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
     """The norm behind the SSD with its SiLU gate, over groups of D / groups elements of the last
     dimension: norm(y * silu(z)) * weight, or norm(y) * weight * silu(z) with norm_before_gate.
     y, z [..., D] bf16 or fp32 (either may be a slice of a wider row), weight [D] fp32."""
+    if stream is not None:
+        return _on(stream, gated_norm, y, z, weight, groups, eps, norm_before_gate, out)
     rows, D, ld_y = _rows(y, "y")
     io = _io(y)
     _, _, ld_z = _rows(z, "z", y.dtype, y.shape)
@@ -725,7 +759,7 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
         out = _new_rows(y, y.dtype)
     else:
         _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
-    s = _checked_stream(stream, y, z=z, weight=weight, out=out)
+    s = _checked_stream(y, z=z, weight=weight, out=out)
     st = lib().ssd_gated_norm(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
                               _ptr(weight), float(eps), _ptr(out), ld_out, s)
     _check(st, "ssd_gated_norm")
@@ -736,6 +770,9 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
                         dweight=None, workspace=None, stream=None):
     """Gradients of gated_norm: returns (dy, dz, dweight), dweight [D] fp32.  dy and dz may be
     slices of wider rows (the input projection's gradient)."""
+    if stream is not None:
+        return _on(stream, gated_norm_backward, dout, y, z, weight, groups, eps, norm_before_gate, dy, dz, dweight,
+                   workspace)
     rows, D, ld_do = _rows(dout, "dout")
     io = _io(dout)
     _, _, ld_y = _rows(y, "y", dout.dtype, dout.shape)
@@ -754,8 +791,8 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
         dweight = torch.empty_like(weight)
     else:
         _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight, stream)
-    s = _checked_stream(stream, dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight)
+    s = _checked_stream(dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
     st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
                                        _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,
                                        _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, s)
