@@ -44,13 +44,17 @@ constexpr int kP = 64, kN = 128;
 constexpr uint32_t kRegion = kBlk * 128;        // one [128 rows][64 bf16] swizzled box: 16 KB
 constexpr uint32_t kImage = 2 * kRegion;        // a state: hi, lo, each [128 n][64 p]
 // per-token terms of an item, [kTerms][128] fp32 (a: step sizes times A; cs: its prefix sum in the
-// chunk, csub: in the token's 32-token group)
-constexpr int kTermCs2 = 0;                     // csub log2(e)
-constexpr int kTermE = 1;                       // exp(cs)
-constexpr int kTermW = 2;                       // exp(cs_last - cs)
-constexpr int kTermDt = 3;                      // dt
-constexpr int kTermSlope = 4;                   // of dt over its raw step (1 without one)
+// chunk, csub: in the token's 32-token group).  csub log2(e) takes the first two places, in two parts,
+// token pairs as {hi, hi, lo, lo}: a step that erases the state leaves a prefix sum in the thousands, of
+// which fp32 alone keeps too little for the decay between two tokens behind it
+constexpr int kTermCs2 = 0;
+constexpr int kTermE = 2;                       // exp(cs)
+constexpr int kTermW = 3;                       // exp(cs_last - cs)
+constexpr int kTermDt = 4;                      // dt
 constexpr int kTerms = 5;
+// where the parts of a token's csub log2(e) are
+__device__ __forceinline__ int cs2_at(int token) { return kTermCs2 * kBlk + 4 * (token >> 1) + (token & 1); }
+constexpr int kCs2Lo = 2;
 constexpr uint32_t kTermBytes = kTerms * kBlk * 4;
 
 struct BwdTc {
@@ -67,6 +71,7 @@ struct BwdTc {
     float* seg_decay;       // [split pairs][2][nseg - 1] their whole decay
     long long items;        // b nc H
     float* terms;           // [items][kTerms][128]
+    float* slope;           // [items][128] of dt over its raw step, or nullptr (dt is given)
     uint8_t* img_h;         // [items][kImage] state entering the chunk
     uint8_t* img_g;         // [items][kImage] adjoint of the state leaving it
     float* part;            // [ctas][2][2][128][128] sums of dB, dC of a CTA's first and last group
@@ -151,11 +156,14 @@ __global__ void __launch_bounds__(kTermThreads) ssd_bwd_tc_terms_kernel(const __
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const double c = end[q] + cs[q];
-        t[kTermCs2 * kBlk + 32 * q] = (float)(cs[q] * 1.4426950408889634);
+        const double c2 = cs[q] * 1.4426950408889634;
+        float* two = t - lane + cs2_at(32 * q + lane);
+        two[0] = (float)c2;
+        two[kCs2Lo] = (float)(c2 - (double)(float)c2);
         t[kTermE * kBlk + 32 * q] = expf((float)c);
         t[kTermW * kBlk + 32 * q] = expf((float)(run - c));
         t[kTermDt * kBlk + 32 * q] = dt[q];
-        t[kTermSlope * kBlk + 32 * q] = slope[q];
+        if (p.slope) p.slope[((size_t)bc * p.a.H + h) * kBlk + 32 * q + lane] = slope[q];
     }
 }
 
@@ -648,15 +656,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             if (!live) break;
             lag(p, ROLE_PAIR);
             tc_fence_after();
-            const float* cs2 = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + kTermCs2 * kBlk;
+            const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes);
             float* sums = reinterpret_cast<float*>(smem + kMSums + s * kSumBytes);
-            const float dtj = cs2[(kTermDt - kTermCs2) * kBlk + r];
+            const float dtj = terms[kTermDt * kBlk + r];
             // L_ij = exp(cs_i - cs_j) = 2^(csub_i + d): -d is csub_j, less the totals of the groups
-            // between
-            float d = -cs2[r];
+            // between.  The high parts' sums are exact where they cancel, and round where L is small
+            float d = -terms[cs2_at(r)], dl = -terms[cs2_at(r) + kCs2Lo];
 #pragma unroll 1
-            for (int b = q; b < c; ++b) d += cs2[32 * b + 31];
-            const f32x2 d2 = pack2(d, d), dt2 = pack2(dtj, dtj);
+            for (int b = q; b < c; ++b) d += terms[cs2_at(32 * b + 31)], dl += terms[cs2_at(32 * b + 31) + kCs2Lo];
+            const f32x2 d2 = pack2(d, d), dl2 = pack2(dl, dl), dt2 = pack2(dtj, dtj);
+            const float4* cs2 = reinterpret_cast<const float4*>(terms + cs2_at(32 * c));
             f32x2 col2 = 0ull;
             float gd = 0.f;
 #pragma unroll
@@ -675,9 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int m = 8 * half + j;
-                    const float2 v = *reinterpret_cast<const float2*>(cs2 + 32 * c + 2 * m);
+                    const float4 v = cs2[m];
                     float l0, l1, a, b;
-                    unpack2(add2(pack2(v.x, v.y), d2), l0, l1);
+                    unpack2(add2(add2(pack2(v.x, v.y), d2), add2(pack2(v.z, v.w), dl2)), l0, l1);
                     // above the diagonal S is zero and dS is dropped in the end; the bound keeps L finite
                     // there (below it L <= 1)
                     const f32x2 l = pack2(ex2(fminf(l0, 64.f)), ex2(fminf(l1, 64.f)));
@@ -1055,6 +1064,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const int k = i.k, s = k & 1, h = i.h, bi = i.bc / p.nc, t0 = (i.bc - bi * p.nc) * kBlk;
             const float Ah = A_next;
             A_next = p.a.A[i.next_head()];
+            float slope[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) slope[g] = p.slope ? p.slope[(size_t)(lo + k) * kBlk + 32 * g + lane] : 1.f;
             ok = wt(MB_FULLXY + s, k >> 1, 90) && wt(MB_SUMFULL + s, k >> 1, 91);
             if (!ok) break;
             lag(p, ROLE_DDT);
@@ -1062,11 +1074,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             const float* terms = reinterpret_cast<const float*>(smem + kMTerms + s * kTermBytes) + lane;
             // da_t adds a prefix of F (exclusive) and a suffix of E + rows - columns.  Lane l holds
             // tokens 32 g + l; the four groups' scans run side by side
-            float f[4], dt[4], suf[4], dir[4], slope[4], sD = 0.f;
+            float f[4], dt[4], suf[4], dir[4], sD = 0.f;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 dt[g] = terms[kTermDt * kBlk + 32 * g];
-                slope[g] = terms[kTermSlope * kBlk + 32 * g];
                 const float fj = sums[kSumF * kBlk + 32 * g], gd = sums[kSumGd * kBlk + 32 * g];
                 float row = sums[kSumE * kBlk + 32 * g], col = 0.f;
 #pragma unroll
@@ -1311,6 +1322,7 @@ size_t tc_layout(const BwdArgs& a, char* ws, BwdTc* p) {
     };
     const size_t n = (size_t)p->items;
     p->terms = reinterpret_cast<float*>(take(n * kTermBytes));
+    p->slope = reinterpret_cast<float*>(take(n * kBlk * 4));
     p->img_h = reinterpret_cast<uint8_t*>(take(n * kImage));
     p->img_g = reinterpret_cast<uint8_t*>(take(n * kImage));
     plan_segments(a.b, a.H, p->nc, &p->n_whole, &p->nseg, &p->cseg);
@@ -1351,6 +1363,7 @@ int launch_backward_tc(const BwdArgs& a, void* ws, size_t offset, cudaStream_t s
     memset(&p, 0, sizeof(p));
     tc_layout(a, static_cast<char*>(ws) + offset, &p);
     if (!a.dbias) p.pb = nullptr;
+    if (!a.dtm.raw) p.slope = nullptr;
     p.status = static_cast<int*>(ws);
     const unsigned long long starve = g_starve_bwd.exchange(0);
     p.starve = starve != 0;
