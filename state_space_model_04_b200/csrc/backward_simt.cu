@@ -12,8 +12,9 @@
 //   da_t = exp(cs_Q) <h, dh> + sum_{i >= t} E_i + sum_{j < t} F_j + sum_{i >= t > j} W_ij
 //   W = Gm S L dt,  E_i = exp(cs_i) dy_i . h C_i,  F_j = dt_j exp(cs_Q - cs_j) x_j . dh B_j
 // da_t adds the pairs (i, j) that straddle t, as a suffix sum of W's row sums less its column
-// sums over i > j: both sums are of the same fp32 numbers, so what has to cancel does, and no
-// term of the whole sequence's length enters.
+// sums over i > j: no term of the whole sequence's length enters.  Both sums are of the same fp32
+// numbers and in fp64, so what has to cancel does: behind a step that erases the state nothing may be
+// left, as dA takes da_t times that step.
 //
 // Launches: decay terms and the chunks' own states in both directions; a scan over the chunks (in
 // place: slot c ends up with the state entering chunk c, or the adjoint of the state leaving
@@ -259,9 +260,9 @@ __device__ __noinline__ float raw_slope(float z, float lo, float hi) { return dt
 template <int N> struct MainSmem {
     static constexpr int kB = 0, kC = kB + kQ * N, kH = kC + kQ * N, kG = kH + kP * N, kX = kG + kP * N,
                          kY = kX + kQ * kP, kS = kY + kQ * kP, kM = kS + kQ * kQ, kTerms = kM + kQ * kQ;
-    // per-token: cs (two floats), dt, e, w, row sums, column parts [8], Gm S and Gm on the diagonal, E, F;
-    // then the warps' sums of <h, dh>
-    static constexpr int kFloats = kTerms + kQ * (2 + 3 + 1 + 8 + 2 + 2) + 16;
+    // per-token: cs (two floats), row sums and column parts [8] (fp64), dt, e, w, Gm S and Gm on the
+    // diagonal, E, F; then the warps' sums of <h, dh>
+    static constexpr int kFloats = kTerms + kQ * (2 + 2 + 16 + 3 + 2 + 2) + 16;
 };
 
 template <typename TIO, int N>
@@ -279,10 +280,10 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
     float *sB = sm + SM::kB, *sC = sm + SM::kC, *sH = sm + SM::kH, *sG = sm + SM::kG, *sX = sm + SM::kX,
           *sY = sm + SM::kY, *sS = sm + SM::kS, *sM = sm + SM::kM;
     float2* s_cs = reinterpret_cast<float2*>(sm + SM::kTerms);  // log2(e) cs in two parts
-    float *s_dt = sm + SM::kTerms + 2 * kQ, *s_e = s_dt + kQ, *s_w = s_e + kQ;
-    float* s_row = s_w + kQ;        // [kQ] sum_j W_ij
-    float* s_col = s_row + kQ;      // [8 warps][kQ] parts of sum_i Gm S L (i > j)
-    float* s_dia = s_col + 8 * kQ;  // [kQ] Gm_jj S_jj, and [kQ] Gm_jj behind it
+    double* s_row = reinterpret_cast<double*>(s_cs + kQ);  // [kQ] sum_j W_ij (i > j)
+    double* s_col = s_row + kQ;                            // [8 warps][kQ] parts of sum_i Gm S L (i > j)
+    float *s_dt = reinterpret_cast<float*>(s_col + 8 * kQ), *s_e = s_dt + kQ, *s_w = s_e + kQ;
+    float* s_dia = s_w + kQ;        // [kQ] Gm_jj S_jj, and [kQ] Gm_jj behind it
     float* s_E = s_dia + 2 * kQ;    // [kQ] E_i
     float* s_F = s_E + kQ;          // [kQ] F_j / dt_j
     float* s_z = s_F + kQ;          // [16] warp sums of <h, dh>
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
         if (pairs) {
             // ---- Gm, M = S L, dS, W's sums (rows i = 4 ty + a, columns j = 4 tx + b)
             {
-                float gm[4][4] = {}, row[4] = {}, colp[4] = {}, dtj[4];
+                float gm[4][4] = {}, dtj[4];
+                double row[4] = {}, colp[4] = {};
                 float2 cj[4];
                 mm_nt<kP>(sY, sX, ty, tx, gm);
 #pragma unroll
@@ -359,8 +361,8 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
                         m[c] = sv[c] * l;
                         const float wv = a == c && ty == tx ? 0.f : gm[a][c] * m[c];  // i > j
                         dS[a][c] = fmaf(gm[a][c] * l, dtj[c], dS[a][c]);
-                        row[a] = fmaf(wv, dtj[c], row[a]);
-                        colp[c] += wv;
+                        row[a] = fma((double)wv, (double)dtj[c], row[a]);
+                        colp[c] += (double)wv;
                     }
                     if (ty == tx) s_dia[i] = gm[a][a] * m[a], s_dia[kQ + i] = gm[a][a];
                     *reinterpret_cast<float4*>(sM + at<64>(i, tx)) = make_float4(m[0], m[1], m[2], m[3]);
@@ -430,21 +432,25 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
 #pragma unroll
             for (int k = 0; k < 16; ++k) zz += s_z[k];
             zz *= s_e[kQ - 1];
-            float col[2], rc[2], f[2], dtv[2];
+            double rc[2];
+            float col[2], f[2], dtv[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int t = 2 * lane + k;
-                col[k] = 0.f;
+                double cw = 0.0;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) col[k] += s_col[q * kQ + t];
+                for (int q = 0; q < 8; ++q) cw += s_col[q * kQ + t];
+                col[k] = (float)cw;
                 dtv[k] = s_dt[t];
                 f[k] = s_F[t] * dtv[k];
-                rc[k] = s_E[t] + s_row[t] - col[k] * dtv[k];
+                rc[k] = (double)s_E[t] + (s_row[t] - cw * (double)dtv[k]);
             }
-            float suf = rc[0] + rc[1], pre = f[0] + f[1];  // suffix sum of rc, prefix sum of f over lanes
+            double suf = rc[0] + rc[1];  // suffix sum of rc, prefix sum of f over lanes
+            float pre = f[0] + f[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float a = __shfl_down_sync(0xffffffffu, suf, o), c = __shfl_up_sync(0xffffffffu, pre, o);
+                const double a = __shfl_down_sync(0xffffffffu, suf, o);
+                const float c = __shfl_up_sync(0xffffffffu, pre, o);
                 if (lane + o < 32) suf += a;
                 if (lane >= o) pre += c;
             }
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(2 * kThreads, 1) ssd_bwd_chunk_kernel(const Si
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int t = 2 * lane + k;
-                const float da = zz + (k ? suf - rc[0] : suf) + (k ? pre + f[0] : pre);
+                const float da = zz + (float)(k ? suf - rc[0] : suf) + (k ? pre + f[0] : pre);
                 float ddt = fmaf(Ah, da, s_dia[t] + col[k] + s_F[t]);
                 if (t < valid) {
                     const size_t o = (tok + t) * H + h;

@@ -1117,7 +1117,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_bwd_tc_main_kernel(const __gr
             for (int g = 0; g < 4; ++g) {
                 // the F ahead of the token, by a shift: less its own F, the rounding of that would stay
                 const float up = __shfl_up_sync(0xffffffffu, pre[g], 1);
-                da = carry[g] + suf[g] + (lane ? run + up : run);
+                // every pair that straddles a token has its decay as a factor: where that is zero in fp32, so
+                // is da, of which the suffix sums leave a rounding that dA would take times a large step
+                da = dt[g] * Ah < -104.f ? 0.f : carry[g] + suf[g] + (lane ? run + up : run);
                 run += __shfl_sync(0xffffffffu, pre[g], 31);
                 const float ddt = fmaf(Ah, da, dir[g]) * slope[g];
                 if (t0 + 32 * g + lane < T) {

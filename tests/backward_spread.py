@@ -16,6 +16,8 @@ once, so dA takes the sum of dt_t times da_t's root instead of the root of a sum
                                a rounding a term: 3 sqrt(128) u < 34 u; decays 2 ulp and |c| u in the exponent
                                c, where e^c leaves |c| <= 16 to count: 18 u a factor, two of them; a scan
                                step of 2 u a chunk of 64: (70 + 2 chunks) u
+  all                          a decay below 2^-126 (1.2e-38) may come out as zero: 1e-30 an element, which is that
+                               times operands of up to 1e7
 """
 import torch
 
@@ -58,7 +60,7 @@ def spread(dy, x, dt, A, B, C, D, h0=None, dhf=None):
 def limits(sp, ref, T, io, tc):
     """Bounds on the 2-norm of each gradient's error.  io: the type of x; tc: on the tensor cores."""
     f = 4 * 2.0 ** -16 if tc else (70 + 2 * -(-T // 64)) * U
-    out = {k: f * sp[k].norm().item() for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dh0")}
+    out = {k: f * sp[k].norm().item() + 1e-30 * sp[k].numel() ** 0.5 for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dh0")}
     if io == torch.bfloat16:
         for k, n in (("dx", 1), ("dB", 2), ("dC", 2)):
             out[k] += 1.25 * V * ((n * tc * sp[k].square().sum() + ref[k].square().sum()) / 3).sqrt().item()
