@@ -172,15 +172,25 @@ __device__ __forceinline__ float2 segment_sum_packed(float a, float b, float2* r
     return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
 }
 
-// 1 / (1 + 2^(-z log2 e)), both approximations within 2 ulp
-__device__ __forceinline__ float sigmoid1(float z) {
+// The gate's sigmoid.  For bf16 operands 1 / (1 + 2^(-z log2 e)) by the two approximate instructions
+// (2 ulp each): the product's rounding makes it |z| 2^-24 off for negative z, at most 2^-17 down to
+// z = -87.3, below which it is zero (silu(z) above -1.1e-36); the results round by 2^-8.  For fp32 operands
+// e^z / (1 + e^z) or 1 / (1 + e^-z), whichever has the exponential below one: no larger error for closed
+// gates, and none lost before the exponential itself is.
+__device__ __forceinline__ float sigmoid1(__nv_bfloat16, float z) {
     float a = z * -1.4426950408889634f;
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
     a += 1.f;
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
     return a;
 }
-__device__ __forceinline__ f2 sigmoid2(f2 z) { return {sigmoid1(z.x), sigmoid1(z.y)}; }
+__device__ __forceinline__ float sigmoid1(float, float z) {
+    const float e = expf(-fabsf(z));
+    float r = 1.f + e;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r));
+    return z < 0.f ? e * r : r;
+}
+template <typename T> __device__ __forceinline__ f2 sigmoid2(f2 z) { return {sigmoid1(T(), z.x), sigmoid1(T(), z.y)}; }
 
 struct ResFwd {
     const void* x;
@@ -444,7 +454,7 @@ ssd_gated_norm_kernel(const GateFwd p) {
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 const f2 zv = pair(z[i], j);
-                gt[i][j] = mul(zv, sigmoid2(zv));
+                gt[i][j] = mul(zv, sigmoid2<TIO>(zv));
                 a[i][j] = kNormFirst ? pair(y[i], j) : mul(pair(y[i], j), gt[i][j]);
                 ss = fma(a[i][j], a[i][j], ss);
             }
@@ -501,7 +511,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
             if (in && left[i] > 0) {
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) {
-                    const f2 zv = pair(z[i], j), s1 = sigmoid2(zv), gate = mul(zv, s1);
+                    const f2 zv = pair(z[i], j), s1 = sigmoid2<TIO>(zv), gate = mul(zv, s1);
                     if constexpr (!kLean) sg[i][j] = s1;
                     const f2 n = kNormFirst ? pair(y[i], j) : mul(pair(y[i], j), gate);              // what is normalised
                     const f2 t = mul(kNormFirst ? mul(pair(g[i], j), gate) : pair(g[i], j), w(i, j));  // its gradient over k
@@ -522,7 +532,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
                 for (int j = 0; j < kPairs; ++j) {
                     const f2 zv = pair(z[i], j), yv = pair(y[i], j), go = pair(g[i], j);
                     f2 s1;
-                    if constexpr (kLean) s1 = sigmoid2(zv);
+                    if constexpr (kLean) s1 = sigmoid2<TIO>(zv);
                     else s1 = sg[i][j];
                     const f2 gate = mul(zv, s1);
                     const f2 dgate = fma(gate, fma(s1, pk(-1.f), pk(1.f)), s1);  // silu'(z)
