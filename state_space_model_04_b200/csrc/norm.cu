@@ -35,7 +35,7 @@ namespace ssd {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kWarpThreads = 256, kWarpVectors = 4;  // blocks of a warp a segment, and its vectors a thread
+constexpr int kWarpThreads = 256;   // blocks of a warp a segment
 constexpr int kPairThreads = 640;   // blocks up to here are built with more registers a thread
 constexpr int kMaxBlocksPerSM = 8;
 constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
@@ -424,8 +424,11 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
     SSD_NORM_DW_STORE(0)
 }
 
+// Vectors a thread up to which the forward pass runs three blocks of warp segments an SM (two beyond).
+__host__ __device__ constexpr int three_blocks(bool bf16, bool norm_first) { return !bf16 ? 0 : norm_first ? 2 : 3; }
+
 template <typename TIO, bool kNormFirst, int V, int VPT, int kThr>
-__global__ void __launch_bounds__(kThr, kThr != kWarpThreads ? 0 : sizeof(TIO) == 2 && VPT <= 3 ? 3 : 2)
+__global__ void __launch_bounds__(kThr, kThr != kWarpThreads ? 0 : VPT <= three_blocks(sizeof(TIO) == 2, kNormFirst) ? 3 : 2)
 ssd_gated_norm_kernel(const GateFwd p) {
     SSD_NORM_PROLOGUE(p.L)
     const int base = blockIdx.y * p.L;
@@ -589,24 +592,30 @@ constexpr int kFwdThreads = 1280, kGatedThreads = 1152, kBwdThreads = 672;
 // (`vec`); otherwise elements are read one by one, in pairs.  A thread takes one vector of a segment
 // up to 1024 threads and two beyond: more threads with one vector each measured faster than fewer
 // with more (gated backward, 5120 bf16 elements: two vectors a thread took 371 us).
-// The gated norm's short segments (257 to 1024 elements) go to a warp each instead, whose sums need no
-// barrier, `warps` blocks of them an SM (0: never): forward of 16384 x 5120 in 8 groups 97 us against
-// 107 us (two blocks 100 us; on fp32 three blocks spill, 67 against 64 us for 65536 x 512), backward of 65536 x
-// 512 74 us against 77 us; the residual norm, bound by memory, is slower that way (102 against 93 us).
+// The gated norm's short segments, from 257 elements, go to a warp each instead, whose sums need no
+// barrier, up to as many vectors a thread (`warp_vectors`, 0: never) as its registers hold, and three
+// blocks of them an SM up to `three` vectors, where they still fit.  Warps against blocks in us, 84 M
+// elements in groups of 384, 640 and 1024 (2 to 4 vectors), the two orders alike but where told:
+//   forward bf16   100 117   94 104   84 95            three blocks an SM against two 100 117, 94 97, and
+//                                                      norm first, where three spill at 640, 133 98
+//   forward fp32   165 167   167 197  174 154 (norm first 192 197)
+//   backward bf16  187 210   179 196  227 169
+//   backward fp32  279 330   383 307  465 304
+// The residual norm, bound by memory, is slower that way (102 against 93 us).
 // `ld`: the longest row stride in bytes.  The rows of a block's segments start within 2^32 bytes of
 // its first one's (a thread's offset has 32 bits), or the block takes one segment at a time.
-Shape norm_shape(long long rows, int groups, int L, bool vec, int warps, int resident, long long ld) {
+Shape norm_shape(long long rows, int groups, int L, bool vec, int warp_vectors, int three, int resident, long long ld) {
     Shape s;
     s.V = vec ? 8 : 2;
     const int n = (L + s.V - 1) / s.V;
-    s.warps = warps && vec && n > 32 && n <= 32 * kWarpVectors;
+    s.warps = vec && n > 32 && n <= 32 * warp_vectors;
     s.vpt = s.warps ? (n + 31) / 32 : n <= kMaxThreads ? 1 : vec ? 2 : n <= 4 * kMaxThreads ? 4 : 8;
     s.tps = ((n + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.seg = s.tps >= 256 ? 1 : std::max(1, 256 / s.tps);
     const int thr = s.tps * s.seg;
     s.smem = 2 * sizeof(float2) * s.seg * 32;
     // one wave of blocks: each holds its weights, and in the backward pass stores a part of dw
-    if (s.warps) resident = (s.vpt <= 3 ? warps : 2) * kWarpThreads;
+    if (s.warps) resident = (s.vpt <= three ? 3 : 2) * kWarpThreads;
     else if (s.vpt > 1 || thr > kPairThreads) resident = kMaxThreads;
     else if (!vec) resident = kFwdThreads;
     const int per_sm = std::max(1, std::min(kMaxBlocksPerSM, resident / thr));
@@ -641,9 +650,12 @@ int launch_dweight(const float* part, float* dw, int parts, int D, cudaStream_t 
                                                                  : kernel<A, B, 2, 1, kMaxThreads>))                   \
      : sh.V == 8 ? kernel<A, B, 8, 2, kMaxThreads>                                                                     \
      : sh.vpt == 4 ? kernel<A, B, 2, 4, kMaxThreads> : kernel<A, B, 2, 8, kMaxThreads>)
-#define SSD_NORM_PICK_GATED(kernel, A, B)                                                                              \
-    (!sh.warps ? SSD_NORM_PICK(kernel, A, B) : sh.vpt == 2 ? kernel<A, B, 8, 2, kWarpThreads>                          \
-     : sh.vpt == 3 ? kernel<A, B, 8, 3, kWarpThreads> : kernel<A, B, 8, 4, kWarpThreads>)
+#define SSD_NORM_WARP2(kernel, A, B) kernel<A, B, 8, 2, kWarpThreads>
+#define SSD_NORM_WARP3(kernel, A, B) (sh.vpt == 2 ? SSD_NORM_WARP2(kernel, A, B) : kernel<A, B, 8, 3, kWarpThreads>)
+#define SSD_NORM_WARP4(kernel, A, B) (sh.vpt < 4 ? SSD_NORM_WARP3(kernel, A, B) : kernel<A, B, 8, 4, kWarpThreads>)
+// WARP: the instances of a warp a segment, up to the type's and direction's vectors below
+#define SSD_NORM_PICK_GATED(kernel, A, B, WARP) (sh.warps ? WARP(kernel, A, B) : SSD_NORM_PICK(kernel, A, B))
+constexpr int kFwdWarpBf16 = 4, kFwdWarpF32 = 3, kBwdWarpBf16 = 3, kBwdWarpF32 = 2;
 
 bool vec_ok(const void* p, long long ld, int elem) {
     return !p || (aligned16(p) && (ld * elem) % 16 == 0);
@@ -658,7 +670,7 @@ size_t norm_workspace_bytes(long long rows, int D, int groups) {
     size_t parts = 0;
     for (int v = 0; v < 3; ++v) {
         if (v && L % 8) continue;
-        const Shape s = norm_shape(rows, groups, L, v != 0, v == 2 ? 2 : 0, kBwdThreads, 0);
+        const Shape s = norm_shape(rows, groups, L, v != 0, v == 2 ? std::max(kBwdWarpBf16, kBwdWarpF32) : 0, 0, kBwdThreads, 0);
         parts = std::max(parts, (size_t)s.blocks * s.seg);
     }
     return round_up(parts * D * sizeof(float), 256);
@@ -671,7 +683,7 @@ int launch_residual_norm(long long rows, int D, int io, int res_dtype, const voi
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, eb) && vec_ok(res, ld_res, rb) && vec_ok(out, ld_out, eb) &&
                      vec_ok(r, ld_r, rb) && aligned16(w);
     const long long ld = std::max({ld_x * eb, ld_out * eb, res ? ld_res * rb : 0, r ? ld_r * rb : 0});
-    const Shape sh = norm_shape(rows, 1, D, vec, 0, kFwdThreads, ld);
+    const Shape sh = norm_shape(rows, 1, D, vec, 0, 0, kFwdThreads, ld);
     const ResFwd p{x, res, w, out, r, rows, ld_x, ld_res, ld_out, ld_r, D, scale, eps};
     const char* name = "ssd_residual_norm";
     if (io == SSD_F32) return launch_norm(name, SSD_NORM_PICK(ssd_residual_norm_kernel, float, float), sh, 1, p, s);
@@ -689,7 +701,7 @@ int launch_residual_norm_backward(long long rows, int D, int io, int res_dtype, 
                      vec_ok(dx, ld_dx, eb) && vec_ok(dres, ld_dres, rb) && aligned16(w);
     const long long ld =
         std::max({ld_dout * eb, ld_r * rb, dro ? ld_dro * rb : 0, dx ? ld_dx * eb : 0, dres ? ld_dres * rb : 0});
-    const Shape sh = norm_shape(rows, 1, D, vec, 0, kBwdThreads, ld);
+    const Shape sh = norm_shape(rows, 1, D, vec, 0, 0, kBwdThreads, ld);
     const ResBwd p{dout, r, w, dro, dx, dres, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_r, ld_dro,
                    ld_dx, ld_dres, D, scale, eps};
     const char* name = "ssd_residual_norm_backward";
@@ -710,14 +722,19 @@ int launch_gated_norm(long long rows, int D, int groups, int io, int norm_first,
                       cudaStream_t s) {
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) && vec_ok(out, ld_out, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, io == SSD_BF16 ? 3 : 2, kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
+    const Shape sh = norm_shape(rows, groups, L, vec, io == SSD_BF16 ? kFwdWarpBf16 : kFwdWarpF32,
+                                three_blocks(io == SSD_BF16, norm_first != 0), kGatedThreads, std::max({ld_y, ld_z, ld_out}) * eb);
     const GateFwd p{y, z, w, out, rows, ld_y, ld_z, ld_out, D, L, eps};
     const char* name = "ssd_gated_norm";
     if (io == SSD_F32)
-        return norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, true), sh, groups, p, s)
-                          : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, false), sh, groups, p, s);
-    return norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, true), sh, groups, p, s)
-                      : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, false), sh, groups, p, s);
+        return launch_norm(name,
+                           norm_first ? SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, true, SSD_NORM_WARP3)
+                                      : SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, float, false, SSD_NORM_WARP3),
+                           sh, groups, p, s);
+    return launch_norm(name,
+                       norm_first ? SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, true, SSD_NORM_WARP4)
+                                  : SSD_NORM_PICK_GATED(ssd_gated_norm_kernel, __nv_bfloat16, false, SSD_NORM_WARP4),
+                       sh, groups, p, s);
 }
 
 int launch_gated_norm_backward(long long rows, int D, int groups, int io, int norm_first, const void* dout,
@@ -727,19 +744,22 @@ int launch_gated_norm_backward(long long rows, int D, int groups, int io, int no
     const int eb = io == SSD_BF16 ? 2 : 4, L = D / groups;
     const bool vec = L % 8 == 0 && vec_ok(dout, ld_dout, eb) && vec_ok(y, ld_y, eb) && vec_ok(z, ld_z, eb) &&
                      vec_ok(dy, ld_dy, eb) && vec_ok(dz, ld_dz, eb) && aligned16(w);
-    const Shape sh = norm_shape(rows, groups, L, vec, 2, kBwdThreads,
+    const Shape sh = norm_shape(rows, groups, L, vec, io == SSD_BF16 ? kBwdWarpBf16 : kBwdWarpF32, 0, kBwdThreads,
                                 std::max({ld_dout, ld_y, ld_z, ld_dy, ld_dz}) * eb);
     const GateBwd p{dout, y, z, w, dy, dz, dw ? static_cast<float*>(ws) : nullptr, rows, ld_dout, ld_y, ld_z, ld_dy,
                     ld_dz, D, L, eps};
     const char* name = "ssd_gated_norm_backward";
     int st;
     if (io == SSD_F32)
-        st = norm_first ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, true), sh, groups, p, s)
-                        : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, false), sh, groups, p, s);
+        st = launch_norm(name,
+                         norm_first ? SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, true, SSD_NORM_WARP2)
+                                    : SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, float, false, SSD_NORM_WARP2),
+                         sh, groups, p, s);
     else
-        st = norm_first
-                 ? launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, true), sh, groups, p, s)
-                 : launch_norm(name, SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, false), sh, groups, p, s);
+        st = launch_norm(name,
+                         norm_first ? SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, true, SSD_NORM_WARP3)
+                                    : SSD_NORM_PICK_GATED(ssd_gated_norm_backward_kernel, __nv_bfloat16, false, SSD_NORM_WARP3),
+                         sh, groups, p, s);
     if (st != SSD_OK || !dw) return st;
     return launch_dweight(static_cast<float*>(ws), dw, sh.blocks * sh.seg, D, s);
 }
