@@ -93,6 +93,17 @@ int cuda_status(cudaError_t e, const char* where) {
     return set_error(SSD_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+int device_sms() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            v <= 0)
+            v = 148;
+        return v;
+    }();
+    return n;
+}
+
 // The dynamic shared-memory limit is a per-device attribute of a kernel: set it once per
 // (kernel, device, size) instead of on every launch (a host call each time).
 int smem_limit_once(const void* func, int bytes) {

@@ -539,18 +539,6 @@ __global__ void __launch_bounds__(kThreads) ssd_bwd_sums_kernel(const SimtBwd p,
     st4(static_cast<TIO*>(which ? p.a.dC : p.a.dB) + at, s);
 }
 
-// once, thread-safely
-int bwd_sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            v <= 0)
-            v = 148;
-        return v;
-    }();
-    return n;
-}
-
 // Carves the workspace; returns its size.  ws = nullptr: the size only.
 size_t simt_layout(const BwdArgs& a, char* ws, SimtBwd* p) {
     p->a = a;
@@ -560,7 +548,7 @@ size_t simt_layout(const BwdArgs& a, char* ws, SimtBwd* p) {
     // A block holds an SM.  More blocks a group fill the last wave better, but each begins with the
     // group's S and ends with its dB and dC, about 0.8 of a head's time, and adds a part to the sums
     // (64 groups of 24 heads on 148 SMs: 239 us with 2 blocks a group, 251 with 4, 297 with 5).
-    const int sms = bwd_sm_count();
+    const int sms = device_sms();
     const size_t groups = bc * a.G;
     double best = 0.0;
     p->splits = 1;

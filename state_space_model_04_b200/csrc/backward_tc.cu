@@ -1241,18 +1241,6 @@ __global__ void __launch_bounds__(kJoinThreads) ssd_bwd_tc_join_kernel(const __g
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
-// once, thread-safely
-int tc_sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            v <= 0)
-            v = 148;
-        return v;
-    }();
-    return n;
-}
-
 // CTAs of the main pass.  An even split of the items loads the SMs best, but a CTA whose run crosses
 // from one (chunk, group) into the next begins two of them, and the groups cut are joined afterwards.
 // With few groups each can have CTAs of its own.  In units of an item's 3.2 us a crossing costs about
@@ -1260,7 +1248,7 @@ int tc_sm_count() {
 // evenly and by groups: 1024 items in 128 groups 71 and 54 us, 768 in 32 groups 61 and 52 us, 3072 in 64
 // groups 127 and 122 us; more groups than SMs leave the even split only.
 void plan_main(BwdTc* p) {
-    const int sms = tc_sm_count(), hg = p->a.H / p->a.G, items = (int)p->items, groups = items / hg;
+    const int sms = device_sms(), hg = p->a.H / p->a.G, items = (int)p->items, groups = items / hg;
     p->ctas = std::min(items, sms);
     p->per_group = 0;
     const int most = (items + p->ctas - 1) / p->ctas;
@@ -1279,7 +1267,7 @@ void plan_main(BwdTc* p) {
 // (without the stores: 16 us against 20 us for 11 chunks), and each fold of an end is taken as a
 // quarter of a chunk.  Whole pairs are scheduled first; the cheapest of a few dozen plans wins.
 void plan_segments(int b, int H, int nc, int* n_whole, int* nseg, int* cseg) {
-    const int sms = tc_sm_count(), pairs = b * H, waves = 2 * pairs / sms;
+    const int sms = device_sms(), pairs = b * H, waves = 2 * pairs / sms;
     double best = 0.0;
     bool first = true;
     auto consider = [&](int whole, int n) {

@@ -53,6 +53,10 @@ __device__ __forceinline__ float dt_value(float v, const DtMap& m, int h) {
 // Map a CUDA error to a status with detail.
 int cuda_status(cudaError_t e, const char* where);
 
+// SMs of the device current at the first call (148 when no device answers); initialised once,
+// thread-safely.
+int device_sms();
+
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current device, once.
 int smem_limit_once(const void* func, int bytes);
 

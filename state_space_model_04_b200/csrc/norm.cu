@@ -40,18 +40,6 @@ constexpr int kPairThreads = 640;   // blocks up to here are built with more reg
 constexpr int kMaxBlocksPerSM = 8;
 constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
 
-// once, thread-safely
-int norm_sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            v <= 0)
-            v = 148;
-        return v;
-    }();
-    return n;
-}
-
 // Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register pair;
 // here they save issue slots and cost registers and moves: in a loop of calls residual backward of
 // 32768 x 2560 took 213 us with them against 208 us, gated backward of 16384 x 5120 170 against 172 us
@@ -624,7 +612,7 @@ Shape norm_shape(long long rows, int groups, int L, bool vec, int warp_vectors, 
         s.smem = 2 * sizeof(float2) * 32;
     }
     const long long want = (rows + s.seg - 1) / s.seg;
-    s.blocks = (int)std::min(want, std::max<long long>(1, (long long)norm_sm_count() * per_sm / groups));
+    s.blocks = (int)std::min(want, std::max<long long>(1, (long long)device_sms() * per_sm / groups));
     return s;
 }
 

@@ -563,26 +563,13 @@ chunk_output_small_kernel(int T, int H, int G, int L, int nc, int ks, const IoT*
     }
 }
 
-// SMs of the device current at the first call (148 when no device answers); initialised
-// once, thread-safely
-int sm_count_simt() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            v <= 0)
-            v = 148;
-        return v;
-    }();
-    return n;
-}
-
 // Slices per chunk for the chunk-state pass: enough CTAs for two per SM when (chunks x
 // heads x sequences) alone fall short, at most one per 32 tokens of the chunk, and at most
 // 256 MB of partial states.
 int state_slices(int b, int T, int H, int N, int L) {
     const int nc = (T + L - 1) / L;
     const double units = (double)nc * H * b;
-    int ks = (int)std::ceil(2.0 * sm_count_simt() / std::max(units, 1.0));
+    int ks = (int)std::ceil(2.0 * device_sms() / std::max(units, 1.0));
     ks = std::max(1, std::min(ks, L / kSliceTokens));
     while (ks > 1 && units * ks * kP * N * sizeof(float) > 256.0 * 1024 * 1024) --ks;
     return ks;
@@ -593,7 +580,7 @@ int state_slices(int b, int T, int H, int N, int L) {
 template <typename IoT, typename CsT, int N>
 int launch_output(int b, int T, int H, int G, int L, int nc, int ks, const IoT* x, const float* dt, const DtMap& dtm,
                   const IoT* Bm, const IoT* Cm, const float* D, const CsT* cs, const float* S, void* y, cudaStream_t s) {
-    const bool small = (double)nc * ((L + 63) / 64) * H * b < 2.0 * sm_count_simt();
+    const bool small = (double)nc * ((L + 63) / 64) * H * b < 2.0 * device_sms();
     const int TR = small ? kSmallRows : 64;
     const size_t smem = small ? small_smem_bytes<N>() : sizeof(float) * (64 * (N + 1) + 64 * (N + 1) + 64 * 65 + 64 * kP);
     auto k4 = small ? chunk_output_small_kernel<IoT, CsT, N> : chunk_output_kernel<IoT, CsT, N, 64>;
