@@ -40,14 +40,10 @@ constexpr int kPairThreads = 640;   // blocks up to here are built with more reg
 constexpr int kMaxBlocksPerSM = 8;
 constexpr int kSumRows = 32;        // threads along the parts in the dw sum kernel
 
-// Two fp32 values.  (sm_100's packed fp32 instructions hold such a pair in an aligned register pair;
-// here they save issue slots and cost registers and moves: in a loop of calls residual backward of
-// 32768 x 2560 took 213 us with them against 208 us, gated backward of 16384 x 5120 170 against 172 us
-// and of 4096 x 16384 185 against 174 us.)
+// Two fp32 values, operation by operation.  (The packed fp32 instructions of sm_100 hold such a pair in an
+// aligned register pair: they save issue slots here and cost registers and moves, level at best.)
 struct f2 { float x, y; };
-__device__ __forceinline__ f2 pk(float a, float b) { return {a, b}; }
-__device__ __forceinline__ f2 pk(float a) { return {a, a}; }
-__device__ __forceinline__ void un(f2 v, float& a, float& b) { a = v.x, b = v.y; }
+__device__ __forceinline__ f2 both(float a) { return {a, a}; }
 __device__ __forceinline__ f2 mul(f2 a, f2 b) { return {a.x * b.x, a.y * b.y}; }
 __device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return {fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
 
@@ -71,13 +67,13 @@ template <typename T> __device__ __forceinline__ void load(Raw<T, 2>& r, const T
 __device__ __forceinline__ float f32(float v) { return v; }
 __device__ __forceinline__ float f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ f2 pair(const Raw<float, 8>& r, int j) {
-    return j == 0 ? pk(r.a.x, r.a.y) : j == 1 ? pk(r.a.z, r.a.w) : j == 2 ? pk(r.b.x, r.b.y) : pk(r.b.z, r.b.w);
+    return j == 0 ? f2{r.a.x, r.a.y} : j == 1 ? f2{r.a.z, r.a.w} : j == 2 ? f2{r.b.x, r.b.y} : f2{r.b.z, r.b.w};
 }
 __device__ __forceinline__ f2 pair(const Raw<__nv_bfloat16, 8>& r, int j) {
     const uint32_t u = j == 0 ? r.a.x : j == 1 ? r.a.y : j == 2 ? r.a.z : r.a.w;
-    return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    return f2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
 }
-template <typename T> __device__ __forceinline__ f2 pair(const Raw<T, 2>& r, int) { return pk(f32(r.a), f32(r.b)); }
+template <typename T> __device__ __forceinline__ f2 pair(const Raw<T, 2>& r, int) { return f2{f32(r.a), f32(r.b)}; }
 
 // Keeps the compiler from carrying the unpacked values of a bf16 operand across a reduction beside
 // the stored ones: they are unpacked again behind it, for half the registers.
@@ -87,18 +83,14 @@ __device__ __forceinline__ void repack(Raw<__nv_bfloat16, 8>& r) {
 template <typename R> __device__ __forceinline__ void repack(R&) {}
 
 __device__ __forceinline__ void store(float* p, const f2 (&v)[4], int) {
-    float4 a, b;
-    un(v[0], a.x, a.y), un(v[1], a.z, a.w), un(v[2], b.x, b.y), un(v[3], b.z, b.w);
-    *reinterpret_cast<float4*>(p) = a;
-    *reinterpret_cast<float4*>(p + 4) = b;
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 __device__ __forceinline__ void store(__nv_bfloat16* p, const f2 (&v)[4], int) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float a, b;
-        un(v[i], a, b);
-        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);
         u[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -106,10 +98,8 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const f2 (&v)[4], int) {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 template <typename T> __device__ __forceinline__ void store(T* p, const f2 (&v)[1], int n) {
-    float a, b;
-    un(v[0], a, b);
-    put(p, a);
-    if (n > 1) put(p + 1, b);
+    put(p, v[0].x);
+    if (n > 1) put(p + 1, v[0].y);
 }
 
 // Sum of a (and b) over the threads of one segment.  A segment of at most 32 threads is one
@@ -298,17 +288,13 @@ template <typename T> struct At {
         _Pragma("unroll") for (int i = 0; i < VPT; ++i)                                                   \
             if (left[i] > 0) store(part + col[i], dw[i], left[i]);                                        \
     }
-__device__ __forceinline__ float hsum(f2 v) {
-    float a, b;
-    un(v, a, b);
-    return a + b;
-}
+__device__ __forceinline__ float hsum(f2 v) { return v.x + v.y; }
 
 template <typename TIO, typename TRES, int V, int VPT, int kThr>
 __global__ void __launch_bounds__(kThr, kThr == kPairThreads ? 2 : 1) ssd_residual_norm_kernel(const ResFwd p) {
     SSD_NORM_PROLOGUE(p.D)
     SSD_NORM_WEIGHT(p.w)
-    const f2 scale2 = pk(p.scale);
+    const f2 scale2 = both(p.scale);
     const At<const TIO> px(static_cast<const TIO*>(p.x), p.ld_x);
     const At<const TRES> pres(static_cast<const TRES*>(p.res), p.ld_res);
     const At<TIO> pout(static_cast<TIO*>(p.out), p.ld_out);
@@ -333,7 +319,7 @@ __global__ void __launch_bounds__(kThr, kThr == kPairThreads ? 2 : 1) ssd_residu
             }
         const float k = rsqrtf(segment_sum<false>(hsum(ss), 0.f, red, flip).x * inv_len + p.eps);
         flip ^= 1;
-        const f2 k2 = pk(k);
+        const f2 k2 = both(k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (in && left[i] > 0) {
@@ -351,7 +337,7 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
     SSD_NORM_WEIGHT(p.w)
     SSD_NORM_DW
     if (p.part) griddep_launch();  // the weight gradient follows, and waits
-    const f2 scale2 = pk(p.scale);
+    const f2 scale2 = both(p.scale);
     const At<const TIO> pg(static_cast<const TIO*>(p.dout), p.ld_dout);
     const At<const TRES> pr(static_cast<const TRES*>(p.r), p.ld_r), pd(static_cast<const TRES*>(p.dr_out), p.ld_dro);
     const At<TIO> pdx(static_cast<TIO*>(p.dx), p.ld_dx);
@@ -389,7 +375,7 @@ __global__ void __launch_bounds__(kThr) ssd_residual_norm_backward_kernel(const 
         const float2 sum = segment_sum<true>(hsum(ss), hsum(gr), red, flip);
         flip ^= 1;
         const float k = rsqrtf(sum.x * inv_len + p.eps);
-        const f2 k2 = pk(k), m2 = pk(-sum.y * inv_len * k * k);
+        const f2 k2 = both(k), m2 = both(-sum.y * inv_len * k * k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (in && left[i] > 0) {
@@ -451,7 +437,7 @@ ssd_gated_norm_kernel(const GateFwd p) {
             }
         const float k = rsqrtf(segment_sum<false>(hsum(ss), 0.f, red, flip).x * inv_len + p.eps);
         flip ^= 1;
-        const f2 k2 = pk(k);
+        const f2 k2 = both(k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (in && left[i] > 0) {
@@ -513,7 +499,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
         const float2 sum = segment_sum_packed(hsum(ss), hsum(gv), red, flip);
         flip ^= 1;
         const float k = rsqrtf(sum.x * inv_len + p.eps);
-        const f2 k2 = pk(k), m2 = pk(-sum.y * inv_len * k * k);
+        const f2 k2 = both(k), m2 = both(-sum.y * inv_len * k * k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (in && left[i] > 0) {
@@ -526,7 +512,7 @@ ssd_gated_norm_backward_kernel(const GateBwd p) {
                     if constexpr (kLean) s1 = sigmoid2<TIO>(zv);
                     else s1 = sg[i][j];
                     const f2 gate = mul(zv, s1);
-                    const f2 dgate = fma(gate, fma(s1, pk(-1.f), pk(1.f)), s1);  // silu'(z)
+                    const f2 dgate = fma(gate, fma(s1, both(-1.f), both(1.f)), s1);  // silu'(z)
                     if (kNormFirst) {
                         const f2 n = mul(yv, k2), t = mul(go, gate);
                         dw[i][j] = fma(t, n, dw[i][j]);
