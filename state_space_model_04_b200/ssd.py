@@ -30,6 +30,7 @@ _i = ctypes.c_int
 _ll = ctypes.c_longlong
 _sz = ctypes.c_size_t
 _vp = ctypes.c_void_p
+_INT_MAX = 2**31 - 1  # ctypes cuts larger numbers short
 
 
 class SSDError(RuntimeError):
@@ -636,6 +637,8 @@ def _rows(t, name, dtype=None, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     D = t.shape[-1]
+    if D > _INT_MAX:
+        raise ValueError("%s: rows of %d elements" % (name, D))
     rows = t.numel() // D if D else 0
     if rows == 0 or t.is_contiguous():
         return rows, D, D
@@ -655,6 +658,12 @@ def _rows(t, name, dtype=None, shape=None):
     if ld < D:
         raise ValueError("%s: its rows overlap (row stride %d, %d elements)" % (name, ld, D))
     return rows, D, ld
+
+
+def _groups(groups):
+    if not 1 <= groups <= _INT_MAX:
+        raise ValueError("groups=%r" % (groups,))
+    return int(groups)
 
 
 def _new_rows(like, dtype):
@@ -751,6 +760,7 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
     if stream is not None:
         return _on(stream, gated_norm, y, z, weight, groups, eps, norm_before_gate, out)
     rows, D, ld_y = _rows(y, "y")
+    groups = _groups(groups)
     io = _io(y)
     _, _, ld_z = _rows(z, "z", y.dtype, y.shape)
     _need(weight, "weight", torch.float32, (D,))
@@ -760,7 +770,7 @@ def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=Non
     else:
         _, _, ld_out = _rows(out, "out", y.dtype, y.shape)
     s = _checked_stream(y, z=z, weight=weight, out=out)
-    st = lib().ssd_gated_norm(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
+    st = lib().ssd_gated_norm(rows, D, groups, io, int(bool(norm_before_gate)), _ptr(y), ld_y, _ptr(z), ld_z,
                               _ptr(weight), float(eps), _ptr(out), ld_out, s)
     _check(st, "ssd_gated_norm")
     return out
@@ -774,6 +784,7 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
         return _on(stream, gated_norm_backward, dout, y, z, weight, groups, eps, norm_before_gate, dy, dz, dweight,
                    workspace)
     rows, D, ld_do = _rows(dout, "dout")
+    groups = _groups(groups)
     io = _io(dout)
     _, _, ld_y = _rows(y, "y", dout.dtype, dout.shape)
     _, _, ld_z = _rows(z, "z", dout.dtype, dout.shape)
@@ -791,9 +802,9 @@ def gated_norm_backward(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate
         dweight = torch.empty_like(weight)
     else:
         _need(dweight, "dweight", torch.float32, (D,))
-    workspace, ws_bytes = _norm_workspace(workspace, rows, D, int(groups), weight)
+    workspace, ws_bytes = _norm_workspace(workspace, rows, D, groups, weight)
     s = _checked_stream(dout, y=y, z=z, weight=weight, dy=dy, dz=dz, dweight=dweight, workspace=workspace)
-    st = lib().ssd_gated_norm_backward(rows, D, int(groups), io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
+    st = lib().ssd_gated_norm_backward(rows, D, groups, io, int(bool(norm_before_gate)), _ptr(dout), ld_do,
                                        _ptr(y), ld_y, _ptr(z), ld_z, _ptr(weight), float(eps), _ptr(dy), ld_dy,
                                        _ptr(dz), ld_dz, _ptr(dweight), _ptr(workspace), ws_bytes, s)
     _check(st, "ssd_gated_norm_backward")

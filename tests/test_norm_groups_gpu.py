@@ -28,3 +28,18 @@ def test_group_lengths(L, io, first, rows, groups):
     close(dy, ry, my, "dy")
     close(dz, rz, mz, "dz")
     close(dw, rw, mw, "dweight", 144 + rows / 64)
+
+
+def test_sizes_beyond_an_int_are_refused():
+    """2^32 + 1 groups are not one group, nor rows of 2^32 + 64 elements rows of 64."""
+    x, w = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    for groups in (2**32 + 1, 2**31, 0, -1):
+        with pytest.raises((ValueError, ssd.SSDError)):
+            ssd.gated_norm(x, x, w, groups=groups)
+        with pytest.raises((ValueError, ssd.SSDError)):
+            ssd.gated_norm_backward(x, x, x, w, groups=groups)
+    wide = torch.empty(0, 2**32 + 64, device="cuda")
+    with pytest.raises(ValueError):
+        ssd.residual_norm(wide, w)
+    with pytest.raises(ValueError):
+        ssd.gated_norm(wide, wide, w)
