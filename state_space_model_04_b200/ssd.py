@@ -207,16 +207,20 @@ def _on(stream, call, *args):
     comes from that stream's memory: a block of the current stream's could still be in use by work queued
     there, and would be handed out there again while the call runs.  The results are handed over to the
     current stream, so that they may be dropped with its work on them still queued."""
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == _stream(None):
+        return call(*args)
     if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     here = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
+    torch.cuda.set_stream(stream)
+    try:
         results = call(*args)
-    if here.cuda_stream != stream.cuda_stream:
-        for t in results if isinstance(results, tuple) else (results,):
-            if t is not None:
-                t.record_stream(here)
+    finally:
+        torch.cuda.set_stream(here)
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None:
+            t.record_stream(here)
     return results
 
 

@@ -141,3 +141,16 @@ def test_captured_on_a_stream_that_joins():
         torch.cuda.synchronize()
         same(got, want)
         del graph
+
+
+def test_the_current_stream_stays():
+    """Through a call on another stream, one that is refused among them."""
+    x, w = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    for here in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(here):
+            for s in handles(torch.cuda.Stream()):
+                ssd.residual_norm(x, w, stream=s)
+                assert torch.cuda.current_stream() == here
+                with pytest.raises(ssd.SSDError):
+                    ssd.residual_norm(x, w, eps=-1.0, stream=s)
+                assert torch.cuda.current_stream() == here
