@@ -367,7 +367,9 @@ SSD_API int ssd_decode_loop(int layers, int b, int H, int P, int N, int G, int k
  * accumulation), everything else on the fp32 pipes (64-token chunks).  Decay prefix sums and the
  * sums over chunks are fp64, states fp32.  On the tensor cores the fp32 gradients (ddt, dA, dD,
  * dh0) come from operands carried as two bf16 halves (16 bits) or exact; dx, dB and dC, stored
- * in bf16, round the pair terms and the states to bf16 once on the way.
+ * in bf16, round the pair terms and the states to bf16 once on the way.  Against 64 bits ddt, dA and
+ * dh0 are then off by 2 to 4e-6 of their 2-norm; a caller that wants fp32's 2e-7 passes the operands as
+ * SSD_F32, which takes the fp32 pipes throughout.
  * The workspace's first 256 bytes hold a device status word (see ssd_prefill_check).
  * Written buffers and the workspace must overlap nothing.  No atomics: the same call gives
  * bitwise the same gradients.

@@ -20,7 +20,8 @@
 // place: slot c ends up with the state entering chunk c, or the adjoint of the state leaving
 // it); the gradients per chunk, a block walking heads of one B/C group with dB and dC in
 // registers; sums.  Bound by the fp32 pipes and the shared memory that feeds them: per token and
-// head about 57,000 multiply-adds at N = 128 against 6 KB of state traffic.  4 x 2048 tokens, 48
+// head about 57,000 multiply-adds at N = 128 against 4 KB of state traffic (two fp32 states a chunk, each
+// written twice and read twice).  4 x 2048 tokens, 48
 // heads, N = 128, fp32: 1.82 ms, 25 TFLOP/s, a third of the fp32 pipes' rate.
 #include <algorithm>
 #include "backward.cuh"

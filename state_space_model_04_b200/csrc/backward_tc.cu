@@ -21,16 +21,17 @@
 //   G^T = X dY^T,   V = B dh^T (hi, lo),   Y = C h^T (hi, lo),
 //   dC += (e o dY) h,   dB += (w dt o X) dh,   U = w o V + M^T dY,  M^T = S^T o L^T
 // with G^T, V and Y in fp32 TMEM.  Precision: ddt, dA and dh0 are fp32 gradients, and what they
-// are made of (G, S, the decays, V, Y, the states) carries 16 bits or more: V and Y take both
+// are made of (G, S, V, Y, the states) carries 16 bits or more, the decays fp32's: V and Y take both
 // halves of the states, the state pass both halves of the weighted x and dy.  dx, dB and dC are
 // stored in bf16, so M, dS, the weighted rows and the states are rounded to bf16 once where they
 // feed only those.
 //
 // Bound: memory, with the latency between a pass's roles close behind.  Per item the main pass
 // moves 48 KB of x, dy, dx and 64 KB of state halves, the state pass 32 KB and 64 KB.  8 x 4096
-// tokens, 80 heads: state pass 433 us (4.5 TB/s, 69 % of a copy's rate), main pass 590 us
-// (3.9 TB/s, 59 %; tensor pipe 26 %, issue slots 42 %), join 14 us.  Under a sustained load of
-// these calls the 1000 W power limit takes the clock from 1.97 to 1.6 GHz and 1.08 ms become 1.24.
+// tokens, 80 heads, events around each launch: terms 27 us, state pass 443 us (4.5 TB/s, 69 % of a
+// copy's rate), main pass 612 us (3.8 TB/s, 57 %; tensor pipe 26 %, issue slots 44 %), join 19 us; the call
+// 1.09 ms.  Under a sustained load of these calls the 1000 W power limit takes the clock from 1.97 to
+// 1.6 GHz, and they take 1.17 to 1.26 ms by the board.
 #include <algorithm>
 #include <atomic>
 #include <cstring>

@@ -19,11 +19,11 @@
 // stays in registers, as stored, between its reductions and its results.  A segment belongs to
 // `tps` threads of a block (blockDim.x), 8 elements a thread up to 1024 threads, blockDim.y
 // segments side by side; the block walks rows by a grid stride with its weights in registers.
-// Measured against a copy's 6.55 TB/s: residual forward 98 % and backward 96 % (32768 x 2560), gated
-// forward 79 % (16384 x 5120 in 8 groups) and backward 78 % (one group).  Copies to shared memory
-// some rows ahead (cp.async) were slower than loads by more threads (residual backward 246 us
-// against 227 us then, 212 us now).  In the backward pass the thread
-// owns the same columns of every row it sees, so dw is summed in registers over the rows, stored
+// Measured in a graph of calls, against a copy's 6.55 TB/s: residual forward 154 us, 100 %, and backward
+// 201 us, 102 % (32768 x 2560, bf16, fp32 residual; bf16 residual 114 and 143 us, 90 %), gated forward
+// 94 us, 82 % (16384 x 5120 in 8 groups), and backward 163 us, 78 % (one group), in either order.  Copies
+// to shared memory some rows ahead (cp.async) were slower than loads by more threads.  In the backward
+// pass the thread owns the same columns of every row it sees, so dw is summed in registers over the rows, stored
 // once per block to the workspace, and a second kernel adds the blocks' sums in a fixed order (no
 // atomics: the same call gives the same bits).
 #include <algorithm>

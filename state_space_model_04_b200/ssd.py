@@ -8,7 +8,8 @@ library is missing or a call fails, an exception is raised.
 
 Calls run on the current stream, or on `stream`: a torch.cuda.Stream or a raw handle.  What such a call
 allocates belongs to that stream; the order between it and the current one, for the operands going in and
-the results coming out, is the caller's.
+the results coming out, is the caller's.  Nothing here takes part in autograd: results carry no graph, and
+the backward functions are calls of their own.
 """
 from __future__ import annotations
 
